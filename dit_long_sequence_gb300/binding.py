@@ -44,6 +44,12 @@ class AttnStrides(ctypes.Structure):
     _fields_ = [("q", Strides4), ("k", Strides4), ("v", Strides4), ("o", Strides4)]
 
 
+class AttnBwdStrides(ctypes.Structure):
+    _fields_ = [(n, Strides4) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
+
+
+DIT_ROPE_INTERLEAVED, DIT_ROPE_HALF = 0, 1
+_ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 _vp, _i, _i64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
 
@@ -87,6 +93,27 @@ def _declare(lib):
     lib.dit_attn_lse_merge.argtypes = [_vp, _i64, _i64, _vp, _i64, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp]
     lib.dit_qkv_to_head_major.restype = _i
     lib.dit_qkv_to_head_major.argtypes = [_vp, _i64, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp]
+    _d, _sz, _st = ctypes.c_double, ctypes.c_size_t, ctypes.POINTER(Strides4)
+    lib.dit_attn_bwd.restype = _i
+    lib.dit_attn_bwd.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(AttnBwdStrides), _i, _i, _i, _i,
+                                 _i, _i, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
+    lib.dit_attn_bwd_masked.restype = _i
+    lib.dit_attn_bwd_masked.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(AttnBwdStrides), _i, _i,
+                                        _i, _i, _i, _i, _vp, _i64, _i64, _i, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
+    lib.dit_attn_bwd_workspace_bytes.restype = _sz
+    lib.dit_attn_bwd_workspace_bytes.argtypes = [_i] * 7
+    lib.dit_layer_norm_fwd.restype = _i
+    lib.dit_layer_norm_fwd.argtypes = [_vp, _i, _st, _i, _i, _i, _i, _vp, _vp, _i, _f, _i, _vp, _i, _st, _vp, _vp, _vp]
+    lib.dit_layer_norm_bwd.restype = _i
+    lib.dit_layer_norm_bwd.argtypes = [_vp, _i, _st, _vp, _i, _st, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _st, _vp,
+                                       _vp, _vp, _sz, _vp]
+    lib.dit_layer_norm_bwd_workspace_bytes.restype = _sz
+    lib.dit_layer_norm_bwd_workspace_bytes.argtypes = [_i] * 5
+    lib.dit_rope.restype = _i
+    lib.dit_rope.argtypes = [_vp, _i, _st, _i, _i, _i, _i, _i, _i, _vp, ctypes.POINTER(_i), _i, _vp, _i64, _i64, _f, _i,
+                             _vp, _st, _vp]
+    lib.dit_rope_inv_freq.restype = _i
+    lib.dit_rope_inv_freq.argtypes = [_i, _d, _i, _d, _d, _d, _d, _vp, ctypes.POINTER(_f)]
     lib.dit_status_string.restype = ctypes.c_char_p
     lib.dit_status_string.argtypes = [_i]
     lib.dit_check_watchdog.restype = _i
@@ -117,7 +144,9 @@ EXPORTS = ("dit_attn_fwd", "dit_attn_fwd_ws", "dit_attn_fwd_workspace_bytes", "d
            "dit_attn_fwd_accumulate", "dit_attn_lse_merge", "dit_qkv_to_head_major",
            "dit_qkv_norm_rope_to_head_major", "dit_qkv_cast_fp8", "dit_attn_fwd_fp8", "dit_attn_fwd_fp8_ws", "dit_status_string",
            "dit_check_watchdog",
-           "dit_watchdog_selftest", "dit_version")
+           "dit_watchdog_selftest", "dit_version",
+           "dit_attn_bwd", "dit_attn_bwd_masked", "dit_attn_bwd_workspace_bytes", "dit_layer_norm_fwd",
+           "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope", "dit_rope_inv_freq")
 
 
 class DitError(RuntimeError):
@@ -508,6 +537,267 @@ def attn_fwd_fp8_ws(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, descales,
 def split_stacked_fp8(qkv8: torch.Tensor):
     """The q, k, v [B, N, H, D] views of a stacked [B, N, 3, H, D] FP8 buffer."""
     return qkv8[:, :, 0], qkv8[:, :, 1], qkv8[:, :, 2]
+
+
+def attn_bwd_workspace_bytes(B: int, Nq: int, Nkv: int, H: int, D: int, key_valid_len: int, masked: bool = False) -> int:
+    """Workspace of attn_bwd / attn_bwd_masked (current device)."""
+    return int(_lib.dit_attn_bwd_workspace_bytes(int(B), int(Nq), int(Nkv), int(H), int(D), int(key_valid_len),
+                                                 1 if masked else 0))
+
+
+def _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, dv, grad_dtype, workspace, masked):
+    B, Nq, H, D = q.shape
+    Nkv = k.shape[1]
+    for name, t in (("q", q), ("k", k), ("v", v), ("dout", dout)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda:
+            raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if k.shape != (B, Nkv, H, D) or v.shape != (B, Nkv, H, D) or dout.shape != q.shape:
+        raise ValueError("k and v must be [B, Nkv, H, D] matching q, dout [B, Nq, H, D]")
+    if out.dtype not in (torch.float32, torch.bfloat16) or out.shape != q.shape:
+        raise ValueError("out must be a [B, Nq, H, D] fp32 or bf16 tensor")
+    for name, t in (("lse", lse), ("dlse", dlse)):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, H, Nq) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 [B, H, Nq] tensor")
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("gradients are fp32 or bf16")
+    kvl = Nkv if key_valid_len is None else int(key_valid_len)
+    sc = float(D) ** -0.5 if scale is None else float(scale)
+    given = [g for g in (dq, dk, dv) if g is not None]
+    gt = given[0].dtype if given else grad_dtype
+    dq = torch.empty((B, Nq, H, D), dtype=gt, device=q.device) if dq is None else dq
+    dk = torch.empty((B, Nkv, H, D), dtype=gt, device=q.device) if dk is None else dk
+    dv = torch.empty((B, Nkv, H, D), dtype=gt, device=q.device) if dv is None else dv
+    for name, t, n in (("dq", dq, Nq), ("dk", dk, Nkv), ("dv", dv, Nkv)):
+        if t.dtype != gt or gt not in (torch.float32, torch.bfloat16) or tuple(t.shape) != (B, n, H, D):
+            raise ValueError(f"{name} must be a [B, {'Nq' if t is dq else 'Nkv'}, H, D] tensor, dq, dk and dv of one "
+                             "type (fp32 or bf16)")
+    if workspace is None:
+        nbytes = attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, kvl, masked)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    st = AttnBwdStrides(*(_strides4(t) for t in (q, k, v, out, dout, dq, dk, dv)))
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), DIT_F32 if out.dtype == torch.float32 else DIT_BF16,
+            lse.data_ptr(), dout.data_ptr(), None if dlse is None else dlse.data_ptr(), ctypes.byref(st), B, Nq, Nkv, H, D,
+            kvl)
+    tail = (sc, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), DIT_F32 if gt == torch.float32 else DIT_BF16,
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return head, tail, (dq, dk, dv), workspace
+
+
+def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+             dout: torch.Tensor, *, dlse: torch.Tensor | None = None, key_valid_len: int | None = None,
+             scale: float | None = None, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+             dv: torch.Tensor | None = None, grad_dtype: torch.dtype = torch.bfloat16,
+             workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of attn_fwd through `dit_attn_bwd`, the probabilities recomputed
+    from lse.
+
+    q, k, v, key_valid_len, scale as in the forward call, out and lse its
+    results, dout (bf16, strided like q) the gradient of out and dlse (optional)
+    that of lse.  dq [B, Nq, H, D], dk and dv [B, Nkv, H, D] may be given (e.g.
+    views of one fused [B, N, 3, H, D] gradient) or are allocated in grad_dtype;
+    keys past key_valid_len get zeros.  Returns (dq, dk, dv)."""
+    head, tail, grads, workspace = _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, dv,
+                                                  grad_dtype, workspace, False)
+    _check(_lib.dit_attn_bwd(*head, *tail, _stream_ptr(stream)), "dit_attn_bwd")
+    return grads
+
+
+def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                    dout: torch.Tensor, mask_bits: torch.Tensor, *, mask_rows: int | None = None,
+                    dlse: torch.Tensor | None = None, key_valid_len: int | None = None, scale: float | None = None,
+                    dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                    grad_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of attn_fwd_masked through `dit_attn_bwd_masked`: attn_bwd with
+    the forward call's mask_bits and mask_rows."""
+    if mask_bits.dtype != torch.int32 or mask_bits.dim() != 3 or mask_bits.stride(2) != 1 or not mask_bits.is_cuda:
+        raise ValueError("mask_bits must be an int32 CUDA tensor [B or 1, rows, words], words contiguous")
+    if mask_bits.shape[0] not in (1, q.shape[0]):
+        raise ValueError("mask_bits must have B or 1 batch entries")
+    rows = mask_bits.shape[1] if mask_rows is None else int(mask_rows)
+    if rows > mask_bits.shape[1]:
+        raise ValueError("mask_rows exceeds the mask's rows")
+    head, tail, grads, workspace = _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, dv,
+                                                  grad_dtype, workspace, True)
+    if 4 * ((head[-1] + 127) // 128) > mask_bits.shape[2]:
+        raise ValueError("mask_bits must have 4 * ceil(key_valid_len / 128) words a row")
+    sb = 0 if mask_bits.shape[0] == 1 else mask_bits.stride(0)
+    _check(_lib.dit_attn_bwd_masked(*head, mask_bits.data_ptr(), sb, mask_bits.stride(1), rows, *tail,
+                                    _stream_ptr(stream)), "dit_attn_bwd_masked")
+    return grads
+
+
+def _rows4(t: torch.Tensor) -> torch.Tensor:
+    """[B, N, C] seen as [B, N, 1, C]; [B, N, H, C] as it is."""
+    if t.dim() == 3:
+        return t.unsqueeze(2)
+    if t.dim() != 4:
+        raise ValueError("expected a [B, N, C] or [B, N, H, C] tensor")
+    return t
+
+
+_DTYPES = {torch.bfloat16: DIT_BF16, torch.float32: DIT_F32}
+
+
+def _norm_params(B, C, params):
+    """param_batches of weight / bias tensors ([C] or [B, C]), all of one shape."""
+    shape = None
+    for name, p in params:
+        if p is None:
+            continue
+        if p.dtype != torch.float32 or not p.is_contiguous() or tuple(p.shape) not in ((C,), (B, C)):
+            raise ValueError(f"{name} must be a contiguous fp32 [C] or [B, C] tensor")
+        if shape is not None and tuple(p.shape) != shape:
+            raise ValueError("weight and bias must have one shape")
+        shape = tuple(p.shape)
+    return B if shape is not None and len(shape) == 2 else 1
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+                   eps: float = 1e-6, center: bool = True, out: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, stream=None):
+    """Layer norm (center=False: RMS norm) of the last dimension of x through
+    `dit_layer_norm_fwd`.
+
+    x [B, N, C] or [B, N, H, C], bf16 or fp32, channels contiguous, other
+    strides free; weight and bias fp32 [C], or [B, C] for one set per batch entry
+    (modulation).  Returns (y, mean, rstd): y in out_dtype (default x's; fp32 x
+    may give bf16 y), mean (None without center) and rstd fp32 without the
+    channel dimension."""
+    x4 = _rows4(x)
+    B, N, H, C = x4.shape
+    if x.dtype not in _DTYPES or not x.is_cuda:
+        raise TypeError("x must be a bf16 or fp32 CUDA tensor")
+    groups = _norm_params(B, C, (("weight", weight), ("bias", bias)))
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype not in _DTYPES:
+        raise ValueError("out must have x's shape, bf16 or fp32")
+    o4 = _rows4(out)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if center else None
+    rc = _lib.dit_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x4)), B, N, H, C,
+                                 None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                                 groups, float(eps), 1 if center else 0, out.data_ptr(), _DTYPES[out.dtype],
+                                 ctypes.byref(_strides4(o4)), None if mean is None else mean.data_ptr(), rstd.data_ptr(),
+                                 _stream_ptr(stream))
+    _check(rc, "dit_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_bwd_workspace_bytes(B: int, N: int, H: int, C: int, param_batches: int = 1) -> int:
+    """Workspace of layer_norm_bwd (current device)."""
+    return int(_lib.dit_layer_norm_bwd_workspace_bytes(int(B), int(N), int(H), int(C), int(param_batches)))
+
+
+def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor | None, rstd: torch.Tensor,
+                   weight: torch.Tensor | None = None, *, has_bias: bool = True, dx: torch.Tensor | None = None,
+                   dweight: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of layer_norm_fwd through `dit_layer_norm_bwd`.
+
+    dy has the forward result's type, mean is None for an RMS norm, weight as
+    in the forward call.  Returns (dx, dweight, dbias): dx in x's type; dweight
+    and dbias fp32 in weight's shape, None without a weight (dbias also without
+    has_bias) unless a tensor to fill is given."""
+    x4, d4 = _rows4(x), _rows4(dy)
+    B, N, H, C = x4.shape
+    if x.dtype not in _DTYPES or dy.dtype not in _DTYPES or not x.is_cuda or not dy.is_cuda:
+        raise TypeError("x and dy must be bf16 or fp32 CUDA tensors")
+    if dy.shape != x.shape:
+        raise ValueError("dy must have x's shape")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of x's shape without the channels")
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dx.shape != x.shape or dx.dtype != x.dtype:
+        raise ValueError("dx must have x's shape and type")
+    if weight is not None and dweight is None:
+        dweight = torch.empty_like(weight)
+    if weight is not None and has_bias and dbias is None:
+        dbias = torch.empty_like(weight)
+    groups = _norm_params(B, C, (("weight", weight), ("dweight", dweight), ("dbias", dbias)))
+    if workspace is None and (dweight is not None or dbias is not None):
+        nbytes = layer_norm_bwd_workspace_bytes(B, N, H, C, groups)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+    rc = _lib.dit_layer_norm_bwd(dy.data_ptr(), _DTYPES[dy.dtype], ctypes.byref(_strides4(d4)), x.data_ptr(),
+                                 _DTYPES[x.dtype], ctypes.byref(_strides4(x4)), ptr(mean), rstd.data_ptr(), ptr(weight),
+                                 B, N, H, C, groups, 0 if mean is None else 1, dx.data_ptr(),
+                                 ctypes.byref(_strides4(_rows4(dx))), ptr(dweight), ptr(dbias), ptr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 _stream_ptr(stream))
+    _check(rc, "dit_layer_norm_bwd")
+    return dx, dweight, dbias
+
+
+def rope_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                  original_len: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """The frequency schedule of one position axis through `dit_rope_inv_freq`:
+    base^(-2i / rotary_dim), scaled for long contexts by factor: "linear"
+    (interpolated positions), "base" (a larger base) or "by_parts" (slow pairs
+    only, by the turns they make over original_len).  Returns (inv_freq, mscale):
+    a CPU fp64 tensor [rotary_dim / 2] for rope() and its amplitude factor.
+    Schedules of several axes are concatenated with torch.cat."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(k for k in _ROPE_SCALINGS if k)} or None")
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    freq = torch.empty(rotary_dim // 2, dtype=torch.float64)
+    mscale = ctypes.c_float()
+    rc = _lib.dit_rope_inv_freq(rotary_dim // 2, float(base), _ROPE_SCALINGS[scaling], float(factor), float(original_len),
+                                float(beta_fast), float(beta_slow), freq.data_ptr(), ctypes.byref(mscale))
+    _check(rc, "dit_rope_inv_freq")
+    return freq, mscale.value
+
+
+def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions: torch.Tensor | None = None, *,
+         layout: str = "interleaved", axis_pairs=None, offset: int = 0, mscale: float = 1.0, inverse: bool = False,
+         out: torch.Tensor | None = None, stream=None):
+    """Rotary positions of x [B, N, H, D] (bf16 or fp32, channels contiguous,
+    other strides free) through `dit_rope`.
+
+    inv_freq: CPU fp64 tensor, one angle per position step for each of the
+    rotary_dim / 2 pairs; layout "interleaved" (channels 2i, 2i+1) or "half"
+    (i, i + rotary_dim / 2).  positions: int32 CUDA tensor [N] or [B or 1, N, axes]
+    (None: 0, 1, ...), offset added; axis_pairs: how many pairs turn with each
+    axis.  inverse turns back (the gradient).  out may be x."""
+    B, N, H, D = x.shape
+    if x.dtype not in _DTYPES or not x.is_cuda:
+        raise TypeError("x must be a bf16 or fp32 CUDA tensor")
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous one-dimensional fp64 CPU tensor")
+    if layout not in ("interleaved", "half"):
+        raise ValueError('layout must be "interleaved" or "half"')
+    pairs = (inv_freq.numel(),) if axis_pairs is None else tuple(int(p) for p in axis_pairs)
+    axes = len(pairs)
+    if sum(pairs) != inv_freq.numel():
+        raise ValueError("axis_pairs must sum to the number of pairs")
+    pos_sb = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or not positions.is_cuda:
+            raise TypeError("positions must be an int32 CUDA tensor")
+        if positions.dim() == 1 and axes == 1:
+            positions = positions[None, :, None]
+        if positions.dim() != 3 or positions.shape[0] not in (1, B) or tuple(positions.shape[1:]) != (N, axes):
+            raise ValueError("positions must be [N] (one axis) or [B or 1, N, axes]")
+        if positions.numel() and not positions[0].is_contiguous():
+            raise ValueError("each batch entry's positions must be contiguous")
+        pos_sb = 0 if positions.shape[0] == 1 else positions.stride(0)
+    if out is None:
+        out = torch.empty((B, N, H, D), dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    rc = _lib.dit_rope(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x)), B, N, H, D, 2 * inv_freq.numel(),
+                       DIT_ROPE_HALF if layout == "half" else DIT_ROPE_INTERLEAVED, inv_freq.data_ptr(),
+                       (ctypes.c_int * axes)(*pairs), axes, None if positions is None else positions.data_ptr(), pos_sb,
+                       int(offset), float(mscale), 1 if inverse else 0, out.data_ptr(), ctypes.byref(_strides4(out)),
+                       _stream_ptr(stream))
+    _check(rc, "dit_rope")
+    return out
 
 
 def watchdog_selftest(limit_us: int = 100_000, stream=None):

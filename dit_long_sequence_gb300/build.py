@@ -26,7 +26,7 @@ LIB = os.path.join(BUILD, "libditattn.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libditattn_debug.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_fwd_fp8.cu", "qkv_cast_fp8.cu", "lse_merge.cu", "qkv_layout.cu",
-           "qkv_norm_rope.cu", "mask_occupancy.cu", "selftest.cu"]
+           "qkv_norm_rope.cu", "mask_occupancy.cu", "selftest.cu", "api_train.cu", "attn_bwd.cu", "layer_norm.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -17,6 +17,7 @@
 #ifdef DIT_DEBUG
 #include "dit_attn_debug.h"
 #endif
+#include "api_common.h"
 #include "internal.h"
 #include "split_plan.h"
 
@@ -34,7 +35,6 @@ static __device__ __align__(256) uint32_t g_noalloc_occ[kNoAllocOccWords];
 
 namespace {
 
-constexpr unsigned long long kWatchdogNs = 2000000000ull;  // 2 s per bounded wait
 constexpr int kMaxDevices = 64;
 
 #ifdef DIT_DEBUG
@@ -124,24 +124,19 @@ T* symbol_address(SymbolCache& c, const void* symbol) {
     return static_cast<T*>(addr);
 }
 
-unsigned int* status_word(int dev) {
-    if (dev < 0 || dev >= kMaxDevices) return nullptr;
-    return symbol_address<unsigned int>(g_dev[dev].status, g_status_word);
-}
-
 // Device address of the no-alloc occupancy scratch in the current context.
 uint32_t* noalloc_scratch(int dev) {
     if (dev < 0 || dev >= kMaxDevices) return nullptr;
     return symbol_address<uint32_t>(g_dev[dev].noalloc_occ, g_noalloc_occ);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-// Every buffer a kernel will touch must be memory of the current device (or
-// managed memory), and the stream one of the current device's: a host address
-// or another device's memory handed to a TMA copy or a store is refused here,
-// before anything is enqueued, instead of faulting the GPU.  Null entries are
-// skipped (the caller has already decided which buffers are required).
+unsigned int* status_word(int dev) {
+    if (dev < 0 || dev >= kMaxDevices) return nullptr;
+    return symbol_address<unsigned int>(g_dev[dev].status, g_status_word);
+}
+
 dit_status_t check_placement(std::initializer_list<const void*> ptrs, dit_stream_t stream) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DIT_ERR_CUDA;
@@ -157,6 +152,15 @@ dit_status_t check_placement(std::initializer_list<const void*> ptrs, dit_stream
     }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (s != nullptr && s != cudaStreamLegacy && s != cudaStreamPerThread) {
+        // A stream that is being captured may not be asked for its device (the
+        // query would end the capture); a launch into another device's capture
+        // fails by itself.
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return DIT_ERR_INVALID_ARG;
+        }
+        if (cap != cudaStreamCaptureStatusNone) return DIT_OK;
         int sdev = -1;
         if (cudaStreamGetDevice(s, &sdev) != cudaSuccess) {
             (void)cudaGetLastError();
@@ -167,11 +171,8 @@ dit_status_t check_placement(std::initializer_list<const void*> ptrs, dit_stream
     return DIT_OK;
 }
 
-// A [B, N, H, D] view as a 4-D TMA map (D, N, H, B) with 128-byte swizzle and
-// a box of one swizzle column (64 bf16 or 128 E4M3 channels) by 128 rows.
-// Rows n >= n_rows are outside the map and read as zeros.
 dit_status_t encode_view(CUtensorMap* map, const void* base, const dit_strides4_t& s, int B, int n_rows, int H,
-                         int D, bool fp8 = false) {
+                         int D, bool fp8) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return DIT_ERR_CUDA;
     const cuuint64_t eb = fp8 ? 1 : 2;
@@ -187,8 +188,7 @@ dit_status_t encode_view(CUtensorMap* map, const void* base, const dit_strides4_
     return r == CUDA_SUCCESS ? DIT_OK : DIT_ERR_INVALID_ARG;
 }
 
-// b, n, h strides of a TMA operand: positive, 16-byte multiples, < 2^39 elements.
-dit_status_t check_tma_strides(const dit_strides4_t& s, bool fp8 = false) {
+dit_status_t check_tma_strides(const dit_strides4_t& s, bool fp8) {
     if (s.d != 1) return DIT_ERR_UNSUPPORTED;
     const int64_t st[3] = {s.b, s.n, s.h};
     for (int64_t x : st) {
@@ -198,7 +198,9 @@ dit_status_t check_tma_strides(const dit_strides4_t& s, bool fp8 = false) {
     return DIT_OK;
 }
 
-}  // namespace
+#ifdef DIT_DEBUG
+unsigned long long debug_wait_limit_ns() { return g_dbg_limit_ns.load(); }
+#endif
 
 int device_sm_count(int dev) {
     if (dev >= 0 && dev < kMaxDevices) {

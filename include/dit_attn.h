@@ -24,6 +24,14 @@
  *                          buffer, and dit_attn_fwd_fp8 (dit_attn_fwd_fp8_ws
  *                          with the balancing workspace), the attention that
  *                          reads its output in place.
+ *   dit_attn_bwd           gradients of Q, K, V from the gradient of O, the
+ *                          probabilities recomputed from the LSE
+ *                          (dit_attn_bwd_masked with the general bit mask).
+ *   dit_layer_norm_fwd     layer norm / RMS norm of strided rows, one weight or
+ *   dit_layer_norm_bwd     one per batch entry, and its gradients.
+ *   dit_rope               rotary positions of a strided [B, N, H, D] view, and
+ *                          (inverse) their gradient; dit_rope_inv_freq gives
+ *                          frequency schedules, scaled for long contexts.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -458,6 +466,189 @@ dit_status_t dit_attn_fwd_fp8_ws(const void *q, const void *k, const void *v,
                                  void *out, dit_dtype_t out_dtype, float *lse,
                                  void *workspace, size_t workspace_bytes,
                                  dit_stream_t stream);
+
+/*
+ * dit_attn_bwd -- the gradients of dit_attn_fwd.
+ *
+ * The pages stop at the forward pass; this is its derivative, for callers that
+ * train the block.  With P_ij = exp(scale q_i.k_j - LSE_i) over the keys
+ * j < key_valid_len and dO the gradient of O:
+ *   dV = P^T dO,  delta_i = sum_d dO_id O_id - dLSE_i,  dS = P o (dO V^T - delta),
+ *   dQ = scale dS K,  dK = scale dS^T Q.
+ * P is recomputed from the LSE tile by tile and never stored.  Given the merged
+ * (O, LSE) of several key chunks, a call per chunk yields that chunk's dK and dV
+ * and its share of dQ (ask for fp32 gradients and add the shares).
+ *
+ * q, k, v   as in the forward call (bf16; strides by strides->q / k / v).
+ * out       the forward result O, out_dtype, strides->o (16-byte multiples,
+ *           a zero stride broadcasts).
+ * lse       fp32 [B, H, Nq] contiguous, the forward result.
+ * dout      bf16 gradient of O, strides->dout, under the rules of q.
+ * dlse      fp32 [B, H, Nq] contiguous gradient of the LSE, or NULL (zero).
+ * dq, dk, dv  gradients, grad_dtype, strides->dq / dk / dv: d contiguous, other
+ *           strides 16-byte multiples, no two rows at one place.  They must not
+ *           overlap one another or any input.  Rows j >= key_valid_len of dk and
+ *           dv are written as zeros; those rows of k and v are never read.
+ * A row with lse = -inf (no allowed key) contributes nothing.  All q, k, v and
+ * dout that are read must be finite: 0 * inf is NaN in the products.
+ * workspace device memory of dit_attn_bwd_workspace_bytes, 16-byte aligned, not
+ *           used by anything else until the stream has passed the call.  Needed
+ *           unless there is no key or no query.
+ * Arithmetic: scores, P, dS and all sums in fp32; P and dS rounded to bf16 once,
+ * as operands of the products (P enters dS unrounded); gradients rounded once.
+ * Results do not depend on timing: a repeated call gives the same bits.
+ * Sizes, scale and D as dit_attn_fwd; a zero size is a no-op, except that
+ * gradients over an empty sum are written as zeros.
+ */
+typedef struct {
+    dit_strides4_t q, k, v, o, dout, dq, dk, dv;
+} dit_attn_bwd_strides_t;
+
+dit_status_t dit_attn_bwd(const void *q, const void *k, const void *v,
+                          const void *out, dit_dtype_t out_dtype, const float *lse,
+                          const void *dout, const float *dlse,
+                          const dit_attn_bwd_strides_t *strides,
+                          int B, int Nq, int Nkv, int H, int D,
+                          int key_valid_len, float scale,
+                          void *dq, void *dk, void *dv, dit_dtype_t grad_dtype,
+                          void *workspace, size_t workspace_bytes,
+                          dit_stream_t stream);
+
+/*
+ * dit_attn_bwd_masked -- the gradients of dit_attn_fwd_masked: dit_attn_bwd with
+ * P_ij = 0 where the mask forbids key j to row i.  mask, strides and mask_rows
+ * as there (rows i >= mask_rows attend every key j < key_valid_len); tile pairs
+ * that the mask leaves empty are skipped.
+ */
+dit_status_t dit_attn_bwd_masked(const void *q, const void *k, const void *v,
+                                 const void *out, dit_dtype_t out_dtype, const float *lse,
+                                 const void *dout, const float *dlse,
+                                 const dit_attn_bwd_strides_t *strides,
+                                 int B, int Nq, int Nkv, int H, int D,
+                                 int key_valid_len,
+                                 const uint32_t *mask, int64_t mask_batch_stride,
+                                 int64_t mask_row_stride, int mask_rows,
+                                 float scale,
+                                 void *dq, void *dk, void *dv, dit_dtype_t grad_dtype,
+                                 void *workspace, size_t workspace_bytes,
+                                 dit_stream_t stream);
+
+/*
+ * dit_attn_bwd_workspace_bytes -- workspace of dit_attn_bwd (masked = 0) or
+ * dit_attn_bwd_masked (masked != 0) on the CURRENT device (the plan depends on
+ * its SM count): per-row statistics, the fp32 partial gradients of items that
+ * are cut into pieces because there are few of them, the mask's occupancy map.
+ * 0 when there is nothing to compute.  Host only.
+ */
+size_t dit_attn_bwd_workspace_bytes(int B, int Nq, int Nkv, int H, int D, int key_valid_len, int masked);
+
+/*
+ * dit_layer_norm_fwd -- y = (x - mean) * rstd * weight + bias over the C
+ * channels of every row (b, n, h), rstd = 1 / sqrt(sum (x - mean)^2 / C + eps).
+ *
+ * The norm before a diffusion transformer's attention and feed-forward parts
+ * and, without the mean and with H > 1, the head-wise RMS norm that
+ * dit_qkv_norm_rope_to_head_major applies to q and k (so that its gradient can
+ * be formed).  The pages give no formula.
+ *
+ * x, y      x_dtype / y_dtype, element (b, n, h, c) at b*s.b + n*s.n + h*s.h + c
+ *           (s.d = 1; x strides >= 0, y rows distinct).  bf16 -> bf16,
+ *           fp32 -> fp32 and fp32 -> bf16; bf16 -> fp32 is DIT_ERR_UNSUPPORTED.
+ *           Any C, alignment and stride work; 8 channels are moved at a time when
+ *           C and the strides are multiples of 8 and the pointers 16-byte
+ *           aligned.  y may be x (same type and strides).
+ * weight, bias  fp32 [param_batches, C] contiguous, or NULL (1 and 0);
+ *           param_batches is 1 or B (one set per batch entry: modulation).
+ * center    0: the mean is taken as 0 (RMS norm) and `mean` is not written.
+ * mean, rstd  fp32 [B, N, H] contiguous, kept for the backward pass.
+ * eps       finite, >= 0.  C at most 8192, B at most 65,535, B*N*H below 2^31,
+ *           else DIT_ERR_UNSUPPORTED.  A zero size is a no-op.
+ * Arithmetic in fp32 (the variance from deviations), y rounded once.
+ */
+dit_status_t dit_layer_norm_fwd(const void *x, dit_dtype_t x_dtype, const dit_strides4_t *x_strides,
+                                int B, int N, int H, int C,
+                                const float *weight, const float *bias, int param_batches,
+                                float eps, int center,
+                                void *y, dit_dtype_t y_dtype, const dit_strides4_t *y_strides,
+                                float *mean, float *rstd, dit_stream_t stream);
+
+/*
+ * dit_layer_norm_bwd -- with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum_c g / C - xh * sum_c (g xh) / C)   (no second term
+ *        without center),
+ *   dweight = sum over the rows of a parameter set of dy * xh,  dbias = of dy.
+ *
+ * dy        dy_dtype (the forward's y_dtype), dx x_dtype; strides as x and y there.
+ *           dx may be x or, in one type, dy (same strides).
+ * dweight, dbias  fp32 [param_batches, C] contiguous, either may be NULL (not formed).
+ *           They are overwritten; with no rows they are zeros.
+ * workspace device memory of dit_layer_norm_bwd_workspace_bytes, 16-byte aligned
+ *           (needed when dweight or dbias is formed).
+ * Sums in fp32 in a fixed order: a repeated call gives the same bits.
+ */
+dit_status_t dit_layer_norm_bwd(const void *dy, dit_dtype_t dy_dtype, const dit_strides4_t *dy_strides,
+                                const void *x, dit_dtype_t x_dtype, const dit_strides4_t *x_strides,
+                                const float *mean, const float *rstd, const float *weight,
+                                int B, int N, int H, int C, int param_batches, int center,
+                                void *dx, const dit_strides4_t *dx_strides,
+                                float *dweight, float *dbias,
+                                void *workspace, size_t workspace_bytes, dit_stream_t stream);
+
+/* Workspace bytes of dit_layer_norm_bwd on the current device (its SM count sets
+ * the number of partial sums).  Host only. */
+size_t dit_layer_norm_bwd_workspace_bytes(int B, int N, int H, int C, int param_batches);
+
+typedef enum { DIT_ROPE_INTERLEAVED = 0, DIT_ROPE_HALF = 1 } dit_rope_layout_t;
+
+/*
+ * dit_rope -- rotary positions: pair i of the first rotary_dim channels of every
+ * head turns by theta = (offset + position) * inv_freq[i],
+ *   (a, b) -> mscale * (a cos theta - b sin theta, a sin theta + b cos theta),
+ * channels (a, b) = (2i, 2i + 1) interleaved (the layout of
+ * dit_qkv_norm_rope_to_head_major) or (i, i + rotary_dim / 2) in the half
+ * layout; channels >= rotary_dim are copied.
+ *
+ * x, y      dtype, element (b, n, h, d) through their strides (s.d = 1; x strides
+ *           >= 0, y rows distinct); q and k of a stacked [B, N, 3, H, D]
+ *           projection are one call with 2 H heads.  y may be x (same strides).
+ *           Any alignment works; 16 bytes are moved at a time where pointers,
+ *           strides, D and (half layout) rotary_dim / 2 allow.
+ * rotary_dim  even, 2 to min(D, 256); D at most 1024, H at most 65,535.
+ * inv_freq  HOST array [rotary_dim / 2], fp64, read during the call; finite.
+ * axis_pairs  HOST array [n_axes], n_axes 1 to 4: how many of the pairs, in
+ *           order, turn with each position axis (video: time, height, width);
+ *           they sum to rotary_dim / 2.
+ * positions int32 device array, element (b, n, axis) at
+ *           b*positions_batch_stride + n*n_axes + axis (batch stride 0 shares
+ *           them), any sign; NULL (one axis only) is n itself.
+ * offset    added to every position (any 64-bit value).
+ * inverse   turns by -theta, still times mscale: the gradient of the forward
+ *           call (its transpose), and with mscale = 1 also its inverse.
+ * Angles are reduced exactly (integer arithmetic modulo one turn), so far
+ * positions lose nothing; fp32 arithmetic, y rounded once.
+ */
+dit_status_t dit_rope(const void *x, dit_dtype_t dtype, const dit_strides4_t *x_strides,
+                      int B, int N, int H, int D, int rotary_dim, dit_rope_layout_t layout,
+                      const double *inv_freq, const int *axis_pairs, int n_axes,
+                      const int32_t *positions, int64_t positions_batch_stride, int64_t offset,
+                      float mscale, int inverse,
+                      void *y, const dit_strides4_t *y_strides, dit_stream_t stream);
+
+/* Frequency schedules of one axis, w_i = base^(-i / pairs) first:
+ * PLAIN w_i; LINEAR w_i / factor (positions interpolated); BASE with
+ * base * factor^(pairs / (pairs - 1)) in place of base (the slowest pair is
+ * slowed by factor, the fastest left alone); BY_PARTS
+ * keep_i w_i + (1 - keep_i) w_i / factor, keep_i = the turns
+ * original_len * w_i / 2 pi mapped from [beta_slow, beta_fast] to [0, 1], and
+ * mscale = 0.1 ln factor + 1 (1 otherwise). */
+typedef enum { DIT_ROPE_PLAIN = 0, DIT_ROPE_LINEAR = 1, DIT_ROPE_BASE = 2, DIT_ROPE_BY_PARTS = 3 } dit_rope_scaling_t;
+
+/* dit_rope_inv_freq -- a schedule above into the host arrays inv_freq [pairs]
+ * (1 to 128) and mscale [1].  factor >= 1 where it is used, base and
+ * original_len > 0, beta_fast > beta_slow.  Host only, no CUDA call. */
+dit_status_t dit_rope_inv_freq(int pairs, double base, dit_rope_scaling_t scaling, double factor,
+                               double original_len, double beta_fast, double beta_slow,
+                               double *inv_freq, float *mscale);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *dit_status_string(dit_status_t s);
