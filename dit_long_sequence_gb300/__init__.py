@@ -15,5 +15,6 @@ __all__ = ["attn_fwd", "attn_fwd_ws", "attn_fwd_workspace_bytes", "attn_fwd_mask
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)   # later uses find it without coming here
+        return value
     raise AttributeError(name)

@@ -48,6 +48,7 @@ class AttnBwdStrides(ctypes.Structure):
     _fields_ = [(n, Strides4) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
 
 
+_BwdStrideWords = ctypes.c_int64 * (ctypes.sizeof(AttnBwdStrides) // 8)
 DIT_ROPE_INTERLEAVED, DIT_ROPE_HALF = 0, 1
 _ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 _vp, _i, _i64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
@@ -95,10 +96,10 @@ def _declare(lib):
     lib.dit_qkv_to_head_major.argtypes = [_vp, _i64, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp]
     _d, _sz, _st = ctypes.c_double, ctypes.c_size_t, ctypes.POINTER(Strides4)
     lib.dit_attn_bwd.restype = _i
-    lib.dit_attn_bwd.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(AttnBwdStrides), _i, _i, _i, _i,
+    lib.dit_attn_bwd.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                                  _i, _i, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
     lib.dit_attn_bwd_masked.restype = _i
-    lib.dit_attn_bwd_masked.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(AttnBwdStrides), _i, _i,
+    lib.dit_attn_bwd_masked.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i,
                                         _i, _i, _i, _i, _vp, _i64, _i64, _i, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
     lib.dit_attn_bwd_workspace_bytes.restype = _sz
     lib.dit_attn_bwd_workspace_bytes.argtypes = [_i] * 7
@@ -166,8 +167,12 @@ def raw():
 
 
 def _stream_ptr(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:   # the current device's current stream, without a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream)
+
+
+_DTYPES = {torch.bfloat16: DIT_BF16, torch.float32: DIT_F32}
 
 
 def _strides4(t: torch.Tensor) -> Strides4:
@@ -562,19 +567,25 @@ def _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, 
         raise ValueError("gradients are fp32 or bf16")
     kvl = Nkv if key_valid_len is None else int(key_valid_len)
     sc = float(D) ** -0.5 if scale is None else float(scale)
-    given = [g for g in (dq, dk, dv) if g is not None]
-    gt = given[0].dtype if given else grad_dtype
-    dq = torch.empty((B, Nq, H, D), dtype=gt, device=q.device) if dq is None else dq
-    dk = torch.empty((B, Nkv, H, D), dtype=gt, device=q.device) if dk is None else dk
-    dv = torch.empty((B, Nkv, H, D), dtype=gt, device=q.device) if dv is None else dv
-    for name, t, n in (("dq", dq, Nq), ("dk", dk, Nkv), ("dv", dv, Nkv)):
-        if t.dtype != gt or gt not in (torch.float32, torch.bfloat16) or tuple(t.shape) != (B, n, H, D):
-            raise ValueError(f"{name} must be a [B, {'Nq' if t is dq else 'Nkv'}, H, D] tensor, dq, dk and dv of one "
-                             "type (fp32 or bf16)")
+    gt = next((g.dtype for g in (dq, dk, dv) if g is not None), grad_dtype)
+    device = q.device
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=gt, device=device)
+    elif dq.dtype != gt or gt not in _DTYPES or dq.shape != q.shape:
+        raise ValueError("dq must be a [B, Nq, H, D] tensor, dq, dk and dv of one type (fp32 or bf16)")
+    grads_kv = []
+    for name, t in (("dk", dk), ("dv", dv)):
+        if t is None:
+            t = torch.empty(k.shape, dtype=gt, device=device)
+        elif t.dtype != gt or gt not in _DTYPES or t.shape != k.shape:
+            raise ValueError(f"{name} must be a [B, Nkv, H, D] tensor, dq, dk and dv of one type (fp32 or bf16)")
+        grads_kv.append(t)
+    dk, dv = grads_kv
     if workspace is None:
         nbytes = attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, kvl, masked)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    st = AttnBwdStrides(*(_strides4(t) for t in (q, k, v, out, dout, dq, dk, dv)))
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    st = _BwdStrideWords(*q.stride(), *k.stride(), *v.stride(), *out.stride(), *dout.stride(), *dq.stride(), *dk.stride(),
+                         *dv.stride())       # AttnBwdStrides, filled in one go
     head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), DIT_F32 if out.dtype == torch.float32 else DIT_BF16,
             lse.data_ptr(), dout.data_ptr(), None if dlse is None else dlse.data_ptr(), ctypes.byref(st), B, Nq, Nkv, H, D,
             kvl)
@@ -636,9 +647,6 @@ def _rows4(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
-_DTYPES = {torch.bfloat16: DIT_BF16, torch.float32: DIT_F32}
-
-
 def _norm_params(B, C, params):
     """param_batches of weight / bias tensors ([C] or [B, C]), all of one shape."""
     shape = None
@@ -669,13 +677,15 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     if x.dtype not in _DTYPES or not x.is_cuda:
         raise TypeError("x must be a bf16 or fp32 CUDA tensor")
     groups = _norm_params(B, C, (("weight", weight), ("bias", bias)))
+    device = x.device
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype not in _DTYPES:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=device)
+    if out.dtype not in _DTYPES or out.shape != x.shape:
         raise ValueError("out must have x's shape, bf16 or fp32")
     o4 = _rows4(out)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if center else None
+    rows = x.shape[:-1]
+    rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    mean = torch.empty(rows, dtype=torch.float32, device=device) if center else None
     rc = _lib.dit_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x4)), B, N, H, C,
                                  None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
                                  groups, float(eps), 1 if center else 0, out.data_ptr(), _DTYPES[out.dtype],
@@ -772,26 +782,28 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions: torch.Tensor | None
         raise ValueError("inv_freq must be a contiguous one-dimensional fp64 CPU tensor")
     if layout not in ("interleaved", "half"):
         raise ValueError('layout must be "interleaved" or "half"')
-    pairs = (inv_freq.numel(),) if axis_pairs is None else tuple(int(p) for p in axis_pairs)
+    n_pairs = inv_freq.numel()
+    pairs = (n_pairs,) if axis_pairs is None else tuple(axis_pairs)
     axes = len(pairs)
-    if sum(pairs) != inv_freq.numel():
+    if sum(pairs) != n_pairs:
         raise ValueError("axis_pairs must sum to the number of pairs")
     pos_sb = 0
     if positions is not None:
         if positions.dtype != torch.int32 or not positions.is_cuda:
             raise TypeError("positions must be an int32 CUDA tensor")
-        if positions.dim() == 1 and axes == 1:
-            positions = positions[None, :, None]
-        if positions.dim() != 3 or positions.shape[0] not in (1, B) or tuple(positions.shape[1:]) != (N, axes):
+        shape, step = positions.shape, positions.stride()
+        if len(shape) == 1 and axes == 1:
+            shape, step = (1, shape[0], 1), (0, step[0], 1)
+        if len(shape) != 3 or shape[0] not in (1, B) or shape[1] != N or shape[2] != axes:
             raise ValueError("positions must be [N] (one axis) or [B or 1, N, axes]")
-        if positions.numel() and not positions[0].is_contiguous():
+        if (N > 1 and step[1] != axes) or (axes > 1 and step[2] != 1):
             raise ValueError("each batch entry's positions must be contiguous")
-        pos_sb = 0 if positions.shape[0] == 1 else positions.stride(0)
+        pos_sb = 0 if shape[0] == 1 else step[0]
     if out is None:
         out = torch.empty((B, N, H, D), dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype:
+    elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and type")
-    rc = _lib.dit_rope(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x)), B, N, H, D, 2 * inv_freq.numel(),
+    rc = _lib.dit_rope(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x)), B, N, H, D, 2 * n_pairs,
                        DIT_ROPE_HALF if layout == "half" else DIT_ROPE_INTERLEAVED, inv_freq.data_ptr(),
                        (ctypes.c_int * axes)(*pairs), axes, None if positions is None else positions.data_ptr(), pos_sb,
                        int(offset), float(mscale), 1 if inverse else 0, out.data_ptr(), ctypes.byref(_strides4(out)),

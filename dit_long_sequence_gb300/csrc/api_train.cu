@@ -223,6 +223,9 @@ void norm_fill(NormArgs& a, int B, int N, int H, int C, int param_batches, bool 
     a.rows_per_group = a.rows / a.groups;
     a.div_nh = FastDiv(static_cast<uint32_t>(N) * static_cast<uint32_t>(H));
     a.div_h = FastDiv(static_cast<uint32_t>(H));
+    a.B = B;
+    a.N = N;
+    a.H = H;
     a.C = C;
     a.center = center;
     a.inv_c = 1.f / static_cast<float>(C);

@@ -85,44 +85,143 @@ struct Row {   // VEC elements as loaded
     }
 };
 
-// The threads of one row: `tpr` of them (a power of two), warp-aligned when
+// A thread's own ring of P staged rows in shared memory, filled by asynchronous
+// copies of its channels (no other thread reads them, so waiting for its own
+// copies is all the synchronisation there is).  Loads of single bf16 channels
+// are below the smallest asynchronous copy: those are loaded when their row is
+// due (a depth of one).
+template <typename T, int VEC, int NV>
+struct Ring {
+    using R = Row<T, VEC>;
+    static constexpr bool kAsync = R::kBytes >= 4;
+    static constexpr int kChunk = R::kBytes < 16 ? R::kBytes : 16;    // bytes of one copy
+    static constexpr int kChunks = kAsync ? R::kBytes / kChunk : 1;
+    static constexpr int kStageBytes = NV * R::kBytes;                // per thread
+    uint32_t base;              // this thread's first chunk; chunks lie blockDim.x apart
+    R reg[kAsync ? 1 : NV];
+    __device__ __forceinline__ uint32_t slot(int stage, int i, int c) const {
+        return base + static_cast<uint32_t>(((stage * NV + i) * kChunks + c) * blockDim.x) * kChunk;
+    }
+    __device__ __forceinline__ void init(void* smem) {
+        base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kChunk;
+    }
+    __device__ __forceinline__ void fetch(int stage, int i, const T* p) {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const char* src = reinterpret_cast<const char*>(p) + c * kChunk;
+                if constexpr (kChunk == 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot(stage, i, c)), "l"(src) : "memory");
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(slot(stage, i, c)), "l"(src), "n"(kChunk) : "memory");
+            }
+        } else {
+            reg[i].load(p);
+        }
+    }
+    __device__ __forceinline__ R take(int stage, int i) const {
+        if constexpr (kAsync) {
+            R r;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if constexpr (kChunk == 16)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(r.w[4 * c]), "=r"(r.w[4 * c + 1]), "=r"(r.w[4 * c + 2]), "=r"(r.w[4 * c + 3])
+                                 : "r"(slot(stage, i, c)) : "memory");
+                else if constexpr (kChunk == 8)
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(slot(stage, i, c)) : "memory");
+                else
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.w[0]) : "r"(slot(stage, i, c)) : "memory");
+            }
+            return r;
+        } else {
+            return reg[i];
+        }
+    }
+};
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Rows staged ahead: as many as keep some 64 bytes a thread and direction in
+// flight without holding more than half an SM's shared memory per 512 threads.
+#ifndef DIT_NORM_STAGE_BYTES
+#define DIT_NORM_STAGE_BYTES 128
+#endif
+__host__ __device__ constexpr int ring_depth(int stage_bytes, bool async) {
+    if (!async) return 1;
+    const int p = DIT_NORM_STAGE_BYTES / stage_bytes;
+    return p < 2 ? 2 : (p > 6 ? 6 : p);
+}
+
+// Packed pairs of fp32 operations: the kernels are bound by instructions as
+// much as by memory, and these halve the arithmetic.
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+// The threads of one row: `tpr` of them (a power of two), whole warps when
 // tpr > 32.  Sums over the row reach every thread in the same order.
 struct RowGroup {
     int tpr, t, id;             // threads per row, index in the row, row slot of the block
+    int warps;                  // warps of a row (1 when tpr <= 32)
     float2* buf;                // [2][kMaxThreads / 32] cross-warp partials
     int flip;
-    __device__ RowGroup(int tpr_, float2* b) : tpr(tpr_), t(threadIdx.x & (tpr_ - 1)), id(threadIdx.x / tpr_), buf(b), flip(0) {}
-    __device__ __forceinline__ float2 sum(float2 v) {
-        const int lim = tpr < 32 ? tpr : 32;
-        // lanes of one warp may belong to row slots that have run out of rows:
-        // every lane of a block takes part in every sum
-        for (int o = lim >> 1; o >= 1; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    __device__ RowGroup(int tpr_, float2* b)
+        : tpr(tpr_), t(threadIdx.x & (tpr_ - 1)), id(threadIdx.x / tpr_), warps(tpr_ > 32 ? tpr_ >> 5 : 1), buf(b), flip(0) {}
+    // Sum over the row's lanes of this warp.  Lanes of one warp may belong to
+    // row slots that have run out of rows: every lane takes part in every sum.
+    __device__ __forceinline__ float lanes(float v) const {
+        if (tpr >= 32) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        } else {
+            for (int o = tpr >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         }
-        if (tpr > 32) {
-            float2* const b = buf + flip * (kMaxThreads / 32);
-            flip ^= 1;
-            if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-            __syncthreads();
-            const int w0 = id * (tpr >> 5);
-            v = b[w0];
-            for (int w = 1; w < (tpr >> 5); ++w) {
-                const float2 o = b[w0 + w];
-                v.x += o.x;
-                v.y += o.y;
-            }
-        }
+        return v;
+    }
+    // Each warp's pair to the row's other warps: lane l gets that of warp
+    // l mod warps.  One barrier among the row's threads; the other buffer is
+    // written next, so a second is not needed.
+    __device__ __forceinline__ float2 exchange(float2 v) {
+        float2* const b = buf + flip * (kMaxThreads / 32);
+        flip ^= 1;
+        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(tpr) : "memory");
+        return b[id * warps + (threadIdx.x & (warps - 1))];
+    }
+    // Sum of what exchange() handed out, over the row's warps.
+    __device__ __forceinline__ float across(float v) const {
+        for (int o = warps >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
 };
 
-__device__ __forceinline__ int64_t row_offset(const NormArgs& a, const dit_strides4_t& s, uint32_t row) {
-    uint32_t nh, h;
-    const uint32_t b = a.div_nh.divmod(row, nh);
-    const uint32_t n = a.div_h.divmod(nh, h);
-    return b * s.b + n * s.n + h * s.h;
-}
+// Element offset of row (b, n, h); rows that follow one another at one distance
+// (the common case) take a multiply.
+struct RowAt {
+    dit_strides4_t s;
+    bool flat;
+    __device__ __forceinline__ int64_t operator()(const NormArgs& a, uint32_t row) const {
+        if (flat) return static_cast<int64_t>(row) * (a.H == 1 ? s.n : s.h);
+        uint32_t nh, h;
+        const uint32_t b = a.div_nh.divmod(row, nh);
+        const uint32_t n = a.div_h.divmod(nh, h);
+        return b * s.b + n * s.n + h * s.h;
+    }
+    __device__ RowAt(const NormArgs& a, const dit_strides4_t& st) : s(st) {
+        flat = (a.H == 1 || st.n == a.H * st.h) && (a.B == 1 || st.b == a.N * st.n);
+    }
+};
 
 template <int VEC>
 __device__ __forceinline__ void load_params(const float* p, float (&v)[VEC]) {
@@ -141,69 +240,135 @@ __device__ __forceinline__ void load_params(const float* p, float (&v)[VEC]) {
 // rounds; a row slot past its last row runs along on zeros.
 template <typename TX, typename TY, int VEC, int NV>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormArgs a, int tpr) {
+    using RX = Ring<TX, VEC, NV>;
+    constexpr int P = ring_depth(RX::kStageBytes, RX::kAsync);
     __shared__ float2 buf[2 * kMaxThreads / 32];
+    extern __shared__ __align__(16) uint8_t ring_mem[];
     RowGroup g(tpr, buf);
+    RX ring;
+    ring.init(ring_mem);
+    const RowAt x_at(a, a.sx), y_at(a, a.sy);
     const uint32_t slots = blockDim.x / tpr;
     const uint32_t step = gridDim.x * slots;
     const uint32_t row0 = blockIdx.y * a.rows_per_group;
-    const uint32_t rounds = (a.rows_per_group - blockIdx.x * slots + step - 1) / step;   // >= 1: blocks * slots <= rows
-    float w[NV][VEC], bi[NV][VEC];
+    const uint32_t rounds = (a.rows_per_group - blockIdx.x * slots + step - 1) / step;   // >= 1: (blocks - 1) * slots < rows
+    const uint32_t first = blockIdx.x * slots + g.id;
     bool live[NV];
     int col[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         col[i] = (i * tpr + g.t) * VEC;
         live[i] = col[i] < a.C;
+    }
+    auto fetch = [&](uint32_t k) {
+        const uint32_t r = first + k * step;
+        if (k < rounds && r < a.rows_per_group) {
+            const TX* p = static_cast<const TX*>(a.x) + x_at(a, row0 + r);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (live[i]) ring.fetch(k % P, i, p + col[i]);
+        }
+        ring_commit();
+    };
+    for (int k = 0; k < P - 1; ++k) fetch(k);
+    float w[NV][VEC], bi[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) { w[i][e] = 1.f; bi[i][e] = 0.f; }
         if (live[i] && a.weight) load_params<VEC>(a.weight + static_cast<int64_t>(blockIdx.y) * a.C + col[i], w[i]);
         if (live[i] && a.bias) load_params<VEC>(a.bias + static_cast<int64_t>(blockIdx.y) * a.C + col[i], bi[i]);
     }
-    Row<TX, VEC> nx[NV];
-    auto load = [&](uint32_t r) {
+    // Channels held by warp v of a row, 1 / that (0 for none): by this thread's
+    // own warp, and by the warp whose pair exchange() hands this lane.
+    auto held = [&](int v) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) n += min(max(a.C - (i * tpr + 32 * v) * VEC, 0), 32 * VEC);
+        return static_cast<float>(n);
+    };
+    const float own_n = tpr > 32 ? held(g.t >> 5) : static_cast<float>(a.C);
+    const float own_inv = own_n > 0.f ? 1.f / own_n : 0.f;
+    const float got_n = tpr > 32 ? held(threadIdx.x & (g.warps - 1)) : 0.f;
+    const float got_inv = got_n > 0.f ? 1.f / got_n : 0.f;
+
+    uint32_t r = first;
+    for (uint32_t k = 0; k < rounds; ++k, r += step) {
+        fetch(k + P - 1);
+        ring_wait<P - 1>();
         const bool ok = r < a.rows_per_group;
-        const TX* p = static_cast<const TX*>(a.x) + (ok ? row_offset(a, a.sx, row0 + r) : 0);
+        float x[NV][VEC];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (ok && live[i]) nx[i].load(p + col[i]);
-            else nx[i].zero();
-        }
-    };
-    uint32_t r = blockIdx.x * slots + g.id;
-    load(r);
-    for (uint32_t k = 0; k < rounds; ++k, r += step) {
-        Row<TX, VEC> x[NV];
+            if (ok && live[i]) {
+                const Row<TX, VEC> v = ring.take(k % P, i);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x[i] = nx[i];
-        if (k + 1 < rounds) load(r + step);
-        float mean = 0.f;
+                for (int e = 0; e < VEC; ++e) x[i][e] = v.get(e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
+            }
+        }
+        // This warp's mean and sum of squared deviations from it, then the row's
+        // from all its warps': sum of (their deviations + n (their mean - mean)^2).
+        float mean = 0.f, s = 0.f;
         if (a.center) {
-            float s = 0.f;
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                if constexpr (VEC == 1) s0 += x[i][0];
+                else
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s += x[i].get(e);
-            mean = g.sum(make_float2(s, 0.f)).x * a.inv_c;
+                    for (int e = 0; e < VEC; e += 2) add2(s0, s1, s0, s1, x[i][e], x[i][e + 1]);
+            }
+            s = g.lanes(s0 + s1);
+            mean = s * own_inv;
         }
-        float q = 0.f;
+        float q0 = 0.f, q1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (live[i])
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (VEC == 1) {
+                x[i][0] = live[i] ? x[i][0] - mean : 0.f;
+                q0 = fmaf(x[i][0], x[i][0], q0);
+            } else if (live[i]) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = x[i].get(e) - mean;
-                    q = fmaf(d, d, q);
+                for (int e = 0; e < VEC; e += 2) {
+                    add2(x[i][e], x[i][e + 1], x[i][e], x[i][e + 1], -mean, -mean);
+                    fma2(q0, q1, x[i][e], x[i][e + 1], x[i][e], x[i][e + 1], q0, q1);
                 }
-        const float var = g.sum(make_float2(q, 0.f)).x * a.inv_c;
-        const float rstd = 1.f / sqrtf(var + a.eps);
-        if (r < a.rows_per_group) {
-            TY* const p = static_cast<TY*>(a.y) + row_offset(a, a.sy, row0 + r);
+            }
+        }
+        float q = g.lanes(q0 + q1);
+        float shift = 0.f;          // this warp's mean - the row's, still in x
+        if (tpr > 32) {
+            const float2 p = g.exchange(make_float2(s, q));
+            q = p.y;
+            if (a.center) {
+                const float row_mean = g.across(p.x) * a.inv_c;
+                const float d = fmaf(p.x, got_inv, -row_mean);
+                q = fmaf(got_n * d, d, q);
+                shift = mean - row_mean;
+                mean = row_mean;
+            }
+            q = g.across(q);
+        }
+        const float rstd = 1.f / sqrtf(q * a.inv_c + a.eps);
+        if (ok) {
+            TY* const p = static_cast<TY*>(a.y) + y_at(a, row0 + r);
+            const float sr = shift * rstd;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live[i]) {
                     float v[VEC];
+                    if constexpr (VEC == 1) {
+                        v[0] = fmaf(fmaf(x[i][0], rstd, sr), w[i][0], bi[i][0]);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[e] = fmaf((x[i].get(e) - mean) * rstd, w[i][e], bi[i][e]);
+                        for (int e = 0; e < VEC; e += 2) {
+                            fma2(v[e], v[e + 1], x[i][e], x[i][e + 1], rstd, rstd, sr, sr);
+                            fma2(v[e], v[e + 1], v[e], v[e + 1], w[i][e], w[i][e + 1], bi[i][e], bi[i][e + 1]);
+                        }
+                    }
                     Row<TY, VEC>::store(p + col[i], v);
                 }
             if (g.t == 0) {
@@ -216,77 +381,126 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
 
 template <typename TX, typename TY, int VEC, int NV>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormArgs a, int tpr) {
+    using RX = Ring<TX, VEC, NV>;
+    using RD = Ring<TY, VEC, NV>;
+    constexpr int P = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
     __shared__ float2 buf[2 * kMaxThreads / 32];
-    extern __shared__ float acc[];      // [slots][tpr * NV * VEC], several row slots only
+    extern __shared__ __align__(16) uint8_t ring_mem[];   // the rings; after the rows, [slots][tpr * NV * VEC] sums
+    float* const acc = reinterpret_cast<float*>(ring_mem);
     RowGroup g(tpr, buf);
+    RX rx;
+    RD rd;
+    rx.init(ring_mem);
+    rd.init(ring_mem + (RX::kAsync ? P * RX::kStageBytes * blockDim.x : 0));
+    const RowAt x_at(a, a.sx), d_at(a, a.sdy), y_at(a, a.sy);
     const uint32_t slots = blockDim.x / tpr;
     const uint32_t step = gridDim.x * slots;
     const uint32_t row0 = blockIdx.y * a.rows_per_group;
     const uint32_t rounds = (a.rows_per_group - blockIdx.x * slots + step - 1) / step;
-    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    const uint32_t first = blockIdx.x * slots + g.id;
     bool live[NV];
     int col[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         col[i] = (i * tpr + g.t) * VEC;
         live[i] = col[i] < a.C;
+    }
+    float nmean = 0.f, nrstd = 0.f;
+    auto stats = [&](uint32_t k) {       // of round k, read one round ahead
+        const uint32_t r = first + k * step;
+        const bool ok = k < rounds && r < a.rows_per_group;
+        nmean = ok && a.center ? __ldg(a.mean + row0 + r) : 0.f;
+        nrstd = ok ? __ldg(a.rstd + row0 + r) : 0.f;
+    };
+    auto fetch = [&](uint32_t k) {
+        const uint32_t r = first + k * step;
+        if (k < rounds && r < a.rows_per_group) {
+            const TX* p = static_cast<const TX*>(a.x) + x_at(a, row0 + r);
+            const TY* d = static_cast<const TY*>(a.dy) + d_at(a, row0 + r);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (live[i]) {
+                    rx.fetch(k % P, i, p + col[i]);
+                    rd.fetch(k % P, i, d + col[i]);
+                }
+        }
+        ring_commit();
+    };
+    for (int k = 0; k < P - 1; ++k) fetch(k);
+    stats(0);
+    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) { w[i][e] = 1.f; dw[i][e] = 0.f; db[i][e] = 0.f; }
         if (live[i] && a.weight) load_params<VEC>(a.weight + static_cast<int64_t>(blockIdx.y) * a.C + col[i], w[i]);
     }
-    Row<TX, VEC> nx[NV];
-    Row<TY, VEC> nd[NV];
-    float nmean = 0.f, nrstd = 0.f;
-    auto load = [&](uint32_t r) {
+    uint32_t r = first;
+    for (uint32_t k = 0; k < rounds; ++k, r += step) {
+        fetch(k + P - 1);
+        ring_wait<P - 1>();
         const bool ok = r < a.rows_per_group;
-        const TX* p = static_cast<const TX*>(a.x) + (ok ? row_offset(a, a.sx, row0 + r) : 0);
-        const TY* d = static_cast<const TY*>(a.dy) + (ok ? row_offset(a, a.sdy, row0 + r) : 0);
+        const float rstd = nrstd, mr = -nmean * nrstd;
+        stats(k + 1);
+        float xh[NV][VEC], gr[NV][VEC];      // xh and g, kept for dx
+        float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (ok && live[i]) { nx[i].load(p + col[i]); nd[i].load(d + col[i]); }
-            else { nx[i].zero(); nd[i].zero(); }
-        }
-        nmean = ok && a.center ? __ldg(a.mean + row0 + r) : 0.f;
-        nrstd = ok ? __ldg(a.rstd + row0 + r) : 0.f;
-    };
-    uint32_t r = blockIdx.x * slots + g.id;
-    load(r);
-    for (uint32_t k = 0; k < rounds; ++k, r += step) {
-        Row<TX, VEC> x[NV];
-        Row<TY, VEC> d[NV];
+            Row<TX, VEC> x;
+            Row<TY, VEC> d;
+            x.zero();
+            d.zero();
+            if (ok && live[i]) { x = rx.take(k % P, i); d = rd.take(k % P, i); }
+            if constexpr (VEC == 1) {
+                const float dy = d.get(0);
+                xh[i][0] = fmaf(x.get(0), rstd, mr);
+                gr[i][0] = dy * w[i][0];
+                s0 += gr[i][0];
+                t0 = fmaf(gr[i][0], xh[i][0], t0);
+                dw[i][0] = fmaf(dy, xh[i][0], dw[i][0]);
+                db[i][0] += dy;
+            } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) { x[i] = nx[i]; d[i] = nd[i]; }
-        const float mean = nmean, rstd = nrstd;
-        if (k + 1 < rounds) load(r + step);
-        float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float xh = (x[i].get(e) - mean) * rstd, dy = d[i].get(e);
-                const float gg = dy * w[i][e];
-                s.x += gg;
-                s.y = fmaf(gg, xh, s.y);
-                dw[i][e] = fmaf(dy, xh, dw[i][e]);
-                db[i][e] += dy;
+                for (int e = 0; e < VEC; e += 2) {
+                    const float d0 = d.get(e), d1 = d.get(e + 1);
+                    fma2(xh[i][e], xh[i][e + 1], x.get(e), x.get(e + 1), rstd, rstd, mr, mr);
+                    mul2(gr[i][e], gr[i][e + 1], d0, d1, w[i][e], w[i][e + 1]);
+                    add2(s0, s1, s0, s1, gr[i][e], gr[i][e + 1]);
+                    fma2(t0, t1, gr[i][e], gr[i][e + 1], xh[i][e], xh[i][e + 1], t0, t1);
+                    fma2(dw[i][e], dw[i][e + 1], d0, d1, xh[i][e], xh[i][e + 1], dw[i][e], dw[i][e + 1]);
+                    add2(db[i][e], db[i][e + 1], db[i][e], db[i][e + 1], d0, d1);
+                }
             }
-        s = g.sum(s);
-        const float c1 = a.center ? s.x * a.inv_c : 0.f, c2 = s.y * a.inv_c;
-        if (r < a.rows_per_group) {
-            TX* const p = static_cast<TX*>(a.y) + row_offset(a, a.sy, row0 + r);
+        }
+        float sg = a.center ? g.lanes(s0 + s1) : 0.f;
+        float st = g.lanes(t0 + t1);
+        if (tpr > 32) {
+            const float2 p = g.exchange(make_float2(sg, st));
+            if (a.center) sg = g.across(p.x);
+            st = g.across(p.y);
+        }
+        // dx = rstd g - rstd c1 - xh (rstd c2)
+        const float n1 = -sg * a.inv_c * rstd, n2 = -st * a.inv_c * rstd;
+        if (ok) {
+            TX* const p = static_cast<TX*>(a.y) + y_at(a, row0 + r);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live[i]) {
                     float v[VEC];
+                    if constexpr (VEC == 1) {
+                        v[0] = fmaf(gr[i][0], rstd, fmaf(xh[i][0], n2, n1));
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float xh = (x[i].get(e) - mean) * rstd;
-                        v[e] = rstd * (fmaf(-xh, c2, d[i].get(e) * w[i][e]) - c1);
+                        for (int e = 0; e < VEC; e += 2) {
+                            fma2(v[e], v[e + 1], xh[i][e], xh[i][e + 1], n2, n2, n1, n1);
+                            fma2(v[e], v[e + 1], gr[i][e], gr[i][e + 1], rstd, rstd, v[e], v[e + 1]);
+                        }
                     }
                     Row<TX, VEC>::store(p + col[i], v);
                 }
         }
     }
+    ring_wait<0>();
     // The block's sums: row slots added in order, then one partial per block
     // (the gradient itself when the group has one block).
     const int width = tpr * NV * VEC;
@@ -301,7 +515,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
                     for (int e = 0; e < VEC; ++e) out[col[i] + e] = v[i][e];
             return;
         }
-        __syncthreads();
+        __syncthreads();     // the rings (or the last sums) have been read
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -340,14 +554,31 @@ __global__ void __launch_bounds__(256) layer_norm_param_sum_kernel(const NormArg
 
 template <typename TX, typename TY, int VEC, int NV>
 cudaError_t fwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-    layer_norm_fwd_kernel<TX, TY, VEC, NV><<<dim3(p.blocks, a.groups), p.threads, 0, s>>>(a, p.tpr);
+    using RX = Ring<TX, VEC, NV>;
+    const int smem = RX::kAsync ? ring_depth(RX::kStageBytes, true) * RX::kStageBytes * p.threads : 0;
+    auto kern = layer_norm_fwd_kernel<TX, TY, VEC, NV>;
+    if (smem > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<dim3(p.blocks, a.groups), p.threads, smem, s>>>(a, p.tpr);
     return cudaGetLastError();
 }
 
 template <typename TX, typename TY, int VEC, int NV>
 cudaError_t bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-    const size_t smem = p.threads > p.tpr ? static_cast<size_t>(p.threads) * NV * VEC * sizeof(float) : 0;
-    layer_norm_bwd_kernel<TX, TY, VEC, NV><<<dim3(p.blocks, a.groups), p.threads, smem, s>>>(a, p.tpr);
+    using RX = Ring<TX, VEC, NV>;
+    using RD = Ring<TY, VEC, NV>;
+    const int depth = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
+    const int rings = ((RX::kAsync ? RX::kStageBytes : 0) + (RD::kAsync ? RD::kStageBytes : 0)) * depth * p.threads;
+    const int sums = p.threads > p.tpr ? p.threads * NV * VEC * static_cast<int>(sizeof(float)) : 0;
+    const int smem = rings > sums ? rings : sums;
+    auto kern = layer_norm_bwd_kernel<TX, TY, VEC, NV>;
+    if (smem > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<dim3(p.blocks, a.groups), p.threads, smem, s>>>(a, p.tpr);
     cudaError_t e = cudaGetLastError();
     const int wants = (a.want_w ? 1 : 0) + (a.want_b ? 1 : 0);
     if (e != cudaSuccess || p.blocks == 1 || wants == 0) return e;
@@ -361,6 +592,7 @@ cudaError_t pick(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
     if (p.vec == V && p.nv == N) return BWD ? bwd<TX, TY, V, N>(a, p, s) : fwd<TX, TY, V, N>(a, p, s);
     DIT_NORM_CASE(8, 1)
     DIT_NORM_CASE(8, 2)
+    DIT_NORM_CASE(8, 4)
     DIT_NORM_CASE(2, 4)
     DIT_NORM_CASE(2, 8)
     DIT_NORM_CASE(1, 8)
@@ -377,25 +609,30 @@ cudaError_t pick_types(const NormArgs& a, const NormPlan& p, bool x_f32, bool y_
 
 }  // namespace
 
+// Channels a thread: forward 32 (16 without 16-byte loads), so that a row of
+// 4,096 is four warps' and one of 1,024 a single warp's, without a barrier:
+// 70 us for 24,576 x 4,096 bf16 against 101 with 16 a thread and 167 with 8; halved
+// while rows are so few that the SMs would not get 512 threads each.  Backward
+// 16: its sums over rows hold two registers a channel (120 us there; 32 spill).
+// 512 threads an SM either way: forward in blocks of 128 (a row's threads when
+// those are more), backward in one block, which leaves one partial (1,024 threads
+// an SM measured 127 us, for its partials).
 NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max, int sms, bool backward) {
     NormPlan p;
     p.vec = vec_max;
-    // 8 channels a thread while a row then fits one block's 512 threads, else 16
-    int per = C <= 8 * kMaxThreads ? 8 : 16;
+    int per = backward || vec_max < 8 ? 16 : 32;
+    const uint64_t rows = static_cast<uint64_t>(groups) * rows_per_group;
+    while (per > 8 && rows * ((C + per - 1) / per) < static_cast<uint64_t>(sms) * 512 && C <= per / 2 * kMaxThreads) per /= 2;
     p.nv = per / p.vec;
     p.tpr = 1;
     while (p.tpr * per < C) p.tpr *= 2;
-    // Blocks of several rows (256 threads; 512 when one row needs them), never
-    // more row slots than rows.
-    p.threads = p.tpr > 256 ? p.tpr : 256;
+    p.threads = backward ? kMaxThreads : 128;
+    if (p.threads < p.tpr) p.threads = p.tpr;
+    // never more row slots than rows
     while (p.threads > 32 && p.threads > p.tpr && static_cast<uint32_t>(p.threads / p.tpr) > rows_per_group) p.threads /= 2;
-    if (p.threads < 32) p.threads = 32;
     const uint32_t slots = static_cast<uint32_t>(p.threads / p.tpr);
     const uint64_t need = (rows_per_group + slots - 1) / slots;
-    // Backward: a block leaves a partial of C sums, so few, long-lived blocks;
-    // forward: as many as are resident.
-    const uint64_t resident = static_cast<uint64_t>(sms) * (backward ? 1024 : 2048) / p.threads;
-    uint64_t blocks = (resident + groups - 1) / groups;
+    uint64_t blocks = (static_cast<uint64_t>(sms) * 512 / p.threads + groups - 1) / groups;
     if (blocks > need) blocks = need;
     p.blocks = static_cast<int>(blocks < 1 ? 1 : blocks);
     return p;

@@ -45,6 +45,7 @@ struct NormArgs {
     uint32_t groups;            // parameter sets: B with per-batch parameters, else 1
     uint32_t rows_per_group;    // rows / groups
     FastDiv div_nh, div_h;      // row -> b, (n, h)
+    int64_t B, N, H;
     int C;
     bool center;
     float eps, inv_c;
