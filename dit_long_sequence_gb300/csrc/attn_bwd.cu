@@ -65,7 +65,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum BwdSite : uint32_t {
     SITE_FIX_FULL = 11, SITE_X_FULL = 12, SITE_X_EMPTY = 13, SITE_T0_FULL = 14, SITE_T1_FULL = 15, SITE_P_READY = 16,
-    SITE_DS_READY = 17, SITE_T1_READ = 18, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21
+    SITE_DS_READY = 17, SITE_T1_READ = 18, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21,
+    SITE_NO_ROOM = 22
 };
 constexpr uint32_t ROLE_MASK = 4;
 
@@ -100,14 +101,19 @@ __device__ __forceinline__ void fadd2_mul2(float& d0, float& d1, float a0, float
         : "f"(a0), "f"(a1), "f"(c0), "f"(c1), "f"(b0), "f"(b1));
 }
 
-template <int D>
+// MASK: a key CTA also stages mask words, which leaves D = 128 one slot less.
+template <int D, bool MASK>
 struct Cfg {
     static constexpr int kTile = kT * D * 2;
-    static constexpr int kStages = D == 128 ? 4 : 8;     // ring slots (X0, X1 alternating)
-    static constexpr int kPairs = kStages / 2;
+    // Ring slots (X0, X1 alternating).  X0(j) is held until the last product of
+    // tile j and X0(j+2) is wanted two products later, which is less than a copy
+    // takes: with four slots both kinds of CTA ran at 1.6 us a tile pair whatever
+    // their products, waiting for it.
+    static constexpr int kStages = D == 128 ? (MASK ? 4 : 5) : 8;
+    static constexpr int kPairs = kStages / 2;           // statistics (mask words) of this many tiles
     static constexpr int kBlock = kT * 128;              // 128 rows x 64 bf16 (one swizzle column)
     static constexpr int kStatBytes = 2 * kT * 4;        // -lse2[128], -delta[128]
-    static constexpr int kMaskBytes = kT * 16;           // 4 words x 128 rows
+    static constexpr int kMaskBytes = MASK ? kT * 16 : 0;   // 4 words x 128 rows
     // barriers
     static constexpr int kFixFull = 0;
     static constexpr int kXFull = 1;
@@ -124,8 +130,10 @@ struct Cfg {
     static constexpr int kStatOffset = (2 + kStages) * kTile;
     static constexpr int kMaskOffset = kStatOffset + kPairs * kStatBytes;
     static constexpr int kBarOffset = kMaskOffset + kPairs * kMaskBytes;
-    static constexpr int kSmemBytes = 1024 + kBarOffset + kNumBars * 8 + 16;
-    static_assert(kSmemBytes <= 232448, "shared memory");
+    static constexpr int kUsedBytes = kBarOffset + kNumBars * 8 + 16;
+    // with room to start on a 1,024-byte boundary where the buffer does not
+    static constexpr int kSmemBytes = kUsedBytes + 1024 <= 232448 ? kUsedBytes + 1024 : 232448;
+    static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStages % 2 == 0), "shared memory");
     // TMEM columns
     static constexpr int kColT0 = 0, kColT1 = 128, kColAcc0 = 256, kColAcc1 = 256 + D;
     static_assert(kColAcc1 + 128 <= 512, "TMEM");
@@ -162,13 +170,19 @@ struct Stream {
 template <int D, bool KEY, bool OUT_BF16, bool MASK>
 __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtensorMap& tm_f1, const CUtensorMap& tm_x0,
                                          const CUtensorMap& tm_x1, const AttnBwdArgs& a, int slot) {
-    using C = Cfg<D>;
+    using C = Cfg<D, MASK>;
     constexpr int S = C::kStages;
     constexpr int TILE = C::kTile;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_base = smem_u32(smem);
+    // Dynamic shared memory starts on a 1,024-byte boundary when a kernel has no
+    // other; the whole grid would give up alike if it ever did not fit.
+    if (s_base + C::kUsedBytes > smem_u32(smem_raw) + C::kSmemBytes) {
+        if (threadIdx.x == 0 && atomicCAS(a.status, 0u, 5u) == 0u) atomicExch(a.status + 3, static_cast<unsigned>(SITE_NO_ROOM));
+        return;
+    }
     const uint32_t sF0 = s_base, sF1 = s_base + TILE, sRing = s_base + 2 * TILE;
     const uint32_t sStat = s_base + C::kStatOffset;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
@@ -285,15 +299,16 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                 const uint32_t ph = static_cast<uint32_t>(i / S) & 1u;
                 if (!wait_bounded(bar(C::kXEmpty + s), ph ^ 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
                 issued = i + 1;
-                // a key CTA's X0 brings the rows' statistics along
-                const bool with_stat = KEY && (i & 1) == 0;
+                // A key CTA's X1 brings the rows' statistics along: by then X0 of
+                // kPairs tiles ago has been released, and its statistics with it.
+                const bool with_stat = KEY && (i & 1) == 1;
                 mbar_arrive_expect_tx(bar(C::kXFull + s), TILE + (with_stat ? C::kStatBytes : 0));
                 const CUtensorMap* tm = (i & 1) ? &tm_x1 : &tm_x0;
                 const uint32_t dst = sRing + s * TILE;
                 for (int c = 0; c < D / 64; ++c)
                     tma_load_4d(dst + c * C::kBlock, tm, bar(C::kXFull + s), c * 64, x_row, h, b);
                 if (with_stat) {
-                    const uint32_t sd = sStat + (s / 2) * C::kStatBytes;
+                    const uint32_t sd = sStat + (i / 2 % C::kPairs) * C::kStatBytes;
                     bulk_load(sd, stat + x_row, kT * 4, bar(C::kXFull + s));
                     bulk_load(sd + kT * 4, stat + static_cast<int64_t>(a.q_tiles) * kT + x_row, kT * 4, bar(C::kXFull + s));
                 }
@@ -426,8 +441,10 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
         bool row_masked = false;
         const uint32_t* mrow = nullptr;
         if constexpr (!KEY) {
-            nlse = __ldg(stat + row);
-            ndelta = __ldg(stat + static_cast<int64_t>(a.q_tiles) * kT + row);
+            if (n_tiles > 0) {      // without keys there are no statistics
+                nlse = __ldg(stat + row);
+                ndelta = __ldg(stat + static_cast<int64_t>(a.q_tiles) * kT + row);
+            }
             if (MASK) {
                 row_masked = row < a.mask_rows;
                 mrow = a.mask + b * a.mask_sb + (row_masked ? row : 0) * a.mask_si;
@@ -454,7 +471,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
             ok = KEY ? wait_bounded(bar(C::kT0Full), ph, wd, ROLE_SOFTMAX, SITE_T0_FULL)
                      : wait_bounded(bar(C::kT0Full + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_SOFTMAX, SITE_T0_FULL);
             // the statistics (and mask words) of this stage have landed
-            if (KEY) ok = ok && wait_bounded(bar(C::kXFull + 2 * st), st_ph, wd, ROLE_SOFTMAX, SITE_X_FULL);
+            if (KEY) ok = ok && wait_bounded(bar(C::kXFull + (2 * j + 1) % S), static_cast<uint32_t>((2 * j + 1) / S) & 1u, wd, ROLE_SOFTMAX, SITE_X_FULL);
             if (KEY && MASK) ok = ok && wait_bounded(bar(C::kMaskFull + st), st_ph, wd, ROLE_SOFTMAX, SITE_MASK_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -711,9 +728,9 @@ template <int D, bool OUT_BF16, bool MASK>
 cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                         const AttnBwdArgs& a, cudaStream_t s) {
     auto kern = attn_bwd_kernel<D, OUT_BF16, MASK>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, MASK>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.n_kv_ctas + a.n_q_ctas, kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
+    kern<<<a.n_kv_ctas + a.n_q_ctas, kThreads, Cfg<D, MASK>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
     return cudaGetLastError();
 }
 
