@@ -77,6 +77,31 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// 16 lanes x 64 32-bit columns: r[4k + i] is lane t / 4 + 8 (i / 2), column
+// 8k + 2 (t mod 4) + (i mod 2) for thread t of the warp.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// 16 lanes x 32 32-bit columns: r[2k + i] goes to lane t / 4 + 8 i, column
+// 4k + t mod 4.  Two neighbouring values of the load above, packed, land on the
+// columns of their pair.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // (d0, d1) = (a0*b + c0, a1*b + c1), one packed FMA.
 __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
     asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
@@ -105,35 +130,38 @@ __device__ __forceinline__ void fadd2_mul2(float& d0, float& d1, float a0, float
 template <int D, bool MASK>
 struct Cfg {
     static constexpr int kTile = kT * D * 2;
-    // Ring slots (X0, X1 alternating).  X0(j) is held until the last product of
-    // tile j and X0(j+2) is wanted two products later, which is less than a copy
-    // takes: with four slots both kinds of CTA ran at 1.6 us a tile pair whatever
-    // their products, waiting for it.
-    static constexpr int kStages = D == 128 ? (MASK ? 4 : 5) : 8;
-    static constexpr int kPairs = kStages / 2;           // statistics (mask words) of this many tiles
+    // Ring slots of X0 and of X1.  X0(j) is held until the last product of tile j,
+    // so three of it keep the next copy three products ahead of its use; with
+    // two and two, both kinds of CTA ran at 1.6 us a tile pair whatever their
+    // products, waiting for copies.
+    static constexpr int kR0 = D == 128 ? (MASK ? 2 : 3) : 4;
+    static constexpr int kR1 = D == 128 ? 2 : 4;
+    static constexpr int kStats = kR1;                   // statistics (and mask words) of this many tiles
     static constexpr int kBlock = kT * 128;              // 128 rows x 64 bf16 (one swizzle column)
     static constexpr int kStatBytes = 2 * kT * 4;        // -lse2[128], -delta[128]
     static constexpr int kMaskBytes = MASK ? kT * 16 : 0;   // 4 words x 128 rows
     // barriers
     static constexpr int kFixFull = 0;
-    static constexpr int kXFull = 1;
-    static constexpr int kXEmpty = kXFull + kStages;
-    static constexpr int kT0Full = kXEmpty + kStages;    // two (query CTA's two T0)
+    static constexpr int kX0Full = 1;
+    static constexpr int kX0Empty = kX0Full + kR0;
+    static constexpr int kX1Full = kX0Empty + kR0;
+    static constexpr int kX1Empty = kX1Full + kR1;
+    static constexpr int kT0Full = kX1Empty + kR1;       // two (query CTA's two T0)
     static constexpr int kT1Full = kT0Full + 2;
     static constexpr int kP = kT1Full + 1;
     static constexpr int kDS = kP + 1;
     static constexpr int kT1Read = kDS + 1;
     static constexpr int kAccFinal = kT1Read + 1;
     static constexpr int kMaskFull = kAccFinal + 1;
-    static constexpr int kDrain = kMaskFull + kPairs;
+    static constexpr int kDrain = kMaskFull + kStats;
     static constexpr int kNumBars = kDrain + 1;
-    static constexpr int kStatOffset = (2 + kStages) * kTile;
-    static constexpr int kMaskOffset = kStatOffset + kPairs * kStatBytes;
-    static constexpr int kBarOffset = kMaskOffset + kPairs * kMaskBytes;
+    static constexpr int kStatOffset = (2 + kR0 + kR1) * kTile;
+    static constexpr int kMaskOffset = kStatOffset + kStats * kStatBytes;
+    static constexpr int kBarOffset = kMaskOffset + kStats * kMaskBytes;
     static constexpr int kUsedBytes = kBarOffset + kNumBars * 8 + 16;
     // with room to start on a 1,024-byte boundary where the buffer does not
     static constexpr int kSmemBytes = kUsedBytes + 1024 <= 232448 ? kUsedBytes + 1024 : 232448;
-    static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStages % 2 == 0), "shared memory");
+    static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStats == kR0), "shared memory");
     // TMEM columns
     static constexpr int kColT0 = 0, kColT1 = 128, kColAcc0 = 256, kColAcc1 = 256 + D;
     static_assert(kColAcc1 + 128 <= 512, "TMEM");
@@ -171,7 +199,7 @@ template <int D, bool KEY, bool OUT_BF16, bool MASK>
 __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtensorMap& tm_f1, const CUtensorMap& tm_x0,
                                          const CUtensorMap& tm_x1, const AttnBwdArgs& a, int slot) {
     using C = Cfg<D, MASK>;
-    constexpr int S = C::kStages;
+    constexpr int R0 = C::kR0, R1 = C::kR1;
     constexpr int TILE = C::kTile;
 
     extern __shared__ uint8_t smem_raw[];
@@ -183,7 +211,8 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
         if (threadIdx.x == 0 && atomicCAS(a.status, 0u, 5u) == 0u) atomicExch(a.status + 3, static_cast<unsigned>(SITE_NO_ROOM));
         return;
     }
-    const uint32_t sF0 = s_base, sF1 = s_base + TILE, sRing = s_base + 2 * TILE;
+    const uint32_t sF0 = s_base, sF1 = s_base + TILE;
+    const uint32_t sX0 = s_base + 2 * TILE, sX1 = sX0 + R0 * TILE;
     const uint32_t sStat = s_base + C::kStatOffset;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
@@ -217,9 +246,13 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
 
     if (threadIdx.x == 0) {
         mbar_init(bar(C::kFixFull), 1);
-        for (int s = 0; s < S; ++s) {
-            mbar_init(bar(C::kXFull + s), 1);
-            mbar_init(bar(C::kXEmpty + s), 1);
+        for (int s = 0; s < R0; ++s) {
+            mbar_init(bar(C::kX0Full + s), 1);
+            mbar_init(bar(C::kX0Empty + s), 1);
+        }
+        for (int s = 0; s < R1; ++s) {
+            mbar_init(bar(C::kX1Full + s), 1);
+            mbar_init(bar(C::kX1Empty + s), 1);
         }
         mbar_init(bar(C::kT0Full), 1);
         mbar_init(bar(C::kT0Full + 1), 1);
@@ -228,7 +261,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
         mbar_init(bar(C::kDS), 256);
         mbar_init(bar(C::kT1Read), 256);
         mbar_init(bar(C::kAccFinal), 1);
-        for (int s = 0; s < C::kPairs; ++s) mbar_init(bar(C::kMaskFull + s), 32);
+        for (int s = 0; s < C::kStats; ++s) mbar_init(bar(C::kMaskFull + s), 32);
         mbar_init(bar(C::kDrain), 1);
         *abort_flag = 0;
         *never_flag = 0;
@@ -256,9 +289,9 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
             Stream<KEY> cur = stream;
             for (int j = 0; j < n_tiles; ++j) {
                 const int tile = cur.next();
-                const int st = j % C::kPairs;
-                const uint32_t ph = static_cast<uint32_t>(j / C::kPairs) & 1u;
-                if (!wait_bounded_warp(bar(C::kXEmpty + 2 * st), ph ^ 1u, wd, ROLE_MASK, SITE_X_EMPTY)) break;
+                const int st = j % C::kStats;
+                const uint32_t ph = static_cast<uint32_t>(j / C::kStats) & 1u;
+                if (!wait_bounded_warp(bar(C::kX0Empty + st), ph ^ 1u, wd, ROLE_MASK, SITE_X_EMPTY)) break;
                 uint32_t* dst = reinterpret_cast<uint32_t*>(smem + C::kMaskOffset + st * C::kMaskBytes);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -288,36 +321,42 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                 tma_load_4d(sF0 + c * C::kBlock, &tm_f0, bar(C::kFixFull), c * 64, row0, h, b);
                 tma_load_4d(sF1 + c * C::kBlock, &tm_f1, bar(C::kFixFull), c * 64, row0, h, b);
             }
-            const int total = 2 * n_tiles;
-            int issued = 0;
+            int issued0 = 0, issued1 = 0;
             Stream<KEY> cur = stream;
-            int x_row = 0;
-            for (int i = 0; i < total; ++i) {
-                if ((i & 1) == 0) x_row = cur.next() * kT;
-                if (!in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len), a.status, ROLE_LOAD, BND_KEY)) break;
-                const int s = i % S;
-                const uint32_t ph = static_cast<uint32_t>(i / S) & 1u;
-                if (!wait_bounded(bar(C::kXEmpty + s), ph ^ 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
-                issued = i + 1;
-                // A key CTA's X1 brings the rows' statistics along: by then X0 of
-                // kPairs tiles ago has been released, and its statistics with it.
-                const bool with_stat = KEY && (i & 1) == 1;
-                mbar_arrive_expect_tx(bar(C::kXFull + s), TILE + (with_stat ? C::kStatBytes : 0));
-                const CUtensorMap* tm = (i & 1) ? &tm_x1 : &tm_x0;
-                const uint32_t dst = sRing + s * TILE;
+            auto copy = [&](const CUtensorMap* tm, uint32_t dst, int full, int x_row) {
                 for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(dst + c * C::kBlock, tm, bar(C::kXFull + s), c * 64, x_row, h, b);
-                if (with_stat) {
-                    const uint32_t sd = sStat + (i / 2 % C::kPairs) * C::kStatBytes;
-                    bulk_load(sd, stat + x_row, kT * 4, bar(C::kXFull + s));
-                    bulk_load(sd + kT * 4, stat + static_cast<int64_t>(a.q_tiles) * kT + x_row, kT * 4, bar(C::kXFull + s));
+                    tma_load_4d(dst + c * C::kBlock, tm, bar(full), c * 64, x_row, h, b);
+            };
+            for (int j = 0; j < n_tiles; ++j) {
+                const int x_row = cur.next() * kT;
+                if (!in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len), a.status, ROLE_LOAD, BND_KEY)) break;
+                if (!wait_bounded(bar(C::kX0Empty + j % R0), (static_cast<uint32_t>(j / R0) & 1u) ^ 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
+                mbar_arrive_expect_tx(bar(C::kX0Full + j % R0), TILE);
+                copy(&tm_x0, sX0 + j % R0 * TILE, C::kX0Full + j % R0, x_row);
+                issued0 = j + 1;
+                if (!wait_bounded(bar(C::kX1Empty + j % R1), (static_cast<uint32_t>(j / R1) & 1u) ^ 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
+                if constexpr (KEY) {
+                    // The rows' statistics come with X1; their stage is free when X0
+                    // of kStats tiles ago has been released.
+                    const int o = j - C::kStats;
+                    if (R0 > C::kStats && o >= 0 &&
+                        !wait_bounded(bar(C::kX0Empty + o % R0), static_cast<uint32_t>(o / R0) & 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
                 }
+                mbar_arrive_expect_tx(bar(C::kX1Full + j % R1), TILE + (KEY ? C::kStatBytes : 0));
+                copy(&tm_x1, sX1 + j % R1 * TILE, C::kX1Full + j % R1, x_row);
+                if constexpr (KEY) {
+                    const uint32_t sd = sStat + j % C::kStats * C::kStatBytes;
+                    bulk_load(sd, stat + x_row, kT * 4, bar(C::kX1Full + j % R1));
+                    bulk_load(sd + kT * 4, stat + static_cast<int64_t>(a.q_tiles) * kT + x_row, kT * 4, bar(C::kX1Full + j % R1));
+                }
+                issued1 = j + 1;
             }
-            if (issued < total || *abort_flag) {
+            if (issued1 < n_tiles || *abort_flag) {
                 // Winding down: wait (bounded) until every copy issued has landed.
-                for (int i = (issued > S ? issued - S : 0); i < issued; ++i)
-                    wait_bounded(bar(C::kXFull + i % S), static_cast<uint32_t>(i / S) & 1u, wd_drain, ROLE_LOAD,
-                                 SITE_LOAD_DRAIN);
+                for (int j = (issued0 > R0 ? issued0 - R0 : 0); j < issued0; ++j)
+                    wait_bounded(bar(C::kX0Full + j % R0), static_cast<uint32_t>(j / R0) & 1u, wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN);
+                for (int j = (issued1 > R1 ? issued1 - R1 : 0); j < issued1; ++j)
+                    wait_bounded(bar(C::kX1Full + j % R1), static_cast<uint32_t>(j / R1) & 1u, wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN);
                 wait_bounded(bar(C::kFixFull), 0, wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN);
             }
         }
@@ -349,72 +388,75 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                                                       (accumulate || kk.value > 0) ? 1u : 0u);
                 });
             };
-            auto x_full = [&](int i) {
-                return wait_bounded_warp(bar(C::kXFull + i % S), static_cast<uint32_t>(i / S) & 1u, wd, ROLE_MMA, SITE_X_FULL);
+            auto x0_full = [&](int j) {
+                return wait_bounded_warp(bar(C::kX0Full + j % R0), static_cast<uint32_t>(j / R0) & 1u, wd, ROLE_MMA, SITE_X_FULL);
             };
-            auto x_addr = [&](int i) { return sRing + (i % S) * TILE; };
+            auto x1_full = [&](int j) {
+                return wait_bounded_warp(bar(C::kX1Full + j % R1), static_cast<uint32_t>(j / R1) & 1u, wd, ROLE_MMA, SITE_X_FULL);
+            };
+            auto x0 = [&](int j) { return sX0 + j % R0 * TILE; };
+            auto x1 = [&](int j) { return sX1 + j % R1 * TILE; };
 
-            bool ok = wait_bounded_warp(bar(C::kFixFull), 0, wd, ROLE_MMA, SITE_FIX_FULL) && x_full(0);
+            bool ok = wait_bounded_warp(bar(C::kFixFull), 0, wd, ROLE_MMA, SITE_FIX_FULL) && x0_full(0);
             if (ok) {
                 tc_fence_after();
-                issue_t(tT0, sF0, x_addr(0));
+                issue_t(tT0, sF0, x0(0));
                 umma_commit_warp(bar(C::kT0Full));
-                ok = x_full(1);
+                ok = x1_full(0);
             }
             if (ok) {
                 tc_fence_after();
-                issue_t(tT1, sF1, x_addr(1));
+                issue_t(tT1, sF1, x1(0));
                 umma_commit_warp(bar(C::kT1Full));
-                if (!KEY) umma_commit_warp(bar(C::kXEmpty + 1));
+                if (!KEY) umma_commit_warp(bar(C::kX1Empty));
             }
             for (int j = 0; ok && j < n_tiles; ++j) {
-                const int i0 = 2 * j, i1 = 2 * j + 1, n0 = 2 * j + 2, n1 = 2 * j + 3;
                 const bool more = j + 1 < n_tiles;
                 const uint32_t ph = static_cast<uint32_t>(j) & 1u;
                 if constexpr (KEY) {
                     ok = wait_bounded_warp(bar(C::kP), ph, wd, ROLE_MMA, SITE_P_READY);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_acc(tA1, tT0, x_addr(i1), j > 0);
-                    umma_commit_warp(bar(C::kXEmpty + i1 % S));
+                    issue_acc(tA1, tT0, x1(j), j > 0);
+                    umma_commit_warp(bar(C::kX1Empty + j % R1));
                     if (more) {
-                        ok = x_full(n0);
+                        ok = x0_full(j + 1);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_t(tT0, sF0, x_addr(n0));
+                        issue_t(tT0, sF0, x0(j + 1));
                         umma_commit_warp(bar(C::kT0Full));
                     }
                     ok = wait_bounded_warp(bar(C::kDS), ph, wd, ROLE_MMA, SITE_DS_READY);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_acc(tA0, tT1, x_addr(i0), j > 0);
-                    umma_commit_warp(bar(C::kXEmpty + i0 % S));
+                    issue_acc(tA0, tT1, x0(j), j > 0);
+                    umma_commit_warp(bar(C::kX0Empty + j % R0));
                     if (more) {
-                        ok = x_full(n1);
+                        ok = x1_full(j + 1);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_t(tT1, sF1, x_addr(n1));
+                        issue_t(tT1, sF1, x1(j + 1));
                         umma_commit_warp(bar(C::kT1Full));
                     }
                 } else {
                     if (more) {
-                        ok = x_full(n0);
+                        ok = x0_full(j + 1);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_t((j & 1) ? tT0 : tT0b, sF0, x_addr(n0));
+                        issue_t((j & 1) ? tT0 : tT0b, sF0, x0(j + 1));
                         umma_commit_warp(bar(C::kT0Full + ((j + 1) & 1)));
-                        ok = x_full(n1) && wait_bounded_warp(bar(C::kT1Read), ph, wd, ROLE_MMA, SITE_T1_READ);
+                        ok = x1_full(j + 1) && wait_bounded_warp(bar(C::kT1Read), ph, wd, ROLE_MMA, SITE_T1_READ);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_t(tT1, sF1, x_addr(n1));
+                        issue_t(tT1, sF1, x1(j + 1));
                         umma_commit_warp(bar(C::kT1Full));
-                        umma_commit_warp(bar(C::kXEmpty + n1 % S));
+                        umma_commit_warp(bar(C::kX1Empty + (j + 1) % R1));
                     }
                     ok = wait_bounded_warp(bar(C::kDS), ph, wd, ROLE_MMA, SITE_DS_READY);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_acc(tA0, (j & 1) ? tT0b : tT0, x_addr(i0), j > 0);
-                    umma_commit_warp(bar(C::kXEmpty + i0 % S));
+                    issue_acc(tA0, (j & 1) ? tT0b : tT0, x0(j), j > 0);
+                    umma_commit_warp(bar(C::kX0Empty + j % R0));
                 }
                 if (!more) umma_commit_warp(bar(C::kAccFinal));
             }
@@ -450,61 +492,81 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                 mrow = a.mask + b * a.mask_sb + (row_masked ? row : 0) * a.mask_si;
             }
         }
-        // 64 values -> 32 columns of bf16 pairs at t
+        // 64 values -> 32 columns of bf16 pairs at t, in the layout they were read
+        // (key CTA: the second half of the values are lanes 16-31)
         auto store_bf16 = [&](const float* v, uint32_t t) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]);
-                tmem_st16(t + c * 16, pk);
+                if constexpr (KEY) tmem_st_16x128b_x8(t + (static_cast<uint32_t>(16 * c) << 16), pk);
+                else tmem_st16(t + c * 16, pk);
             }
         };
 
         for (int j = 0; j < n_tiles; ++j) {
             const int tile = cur.next();
             const uint32_t ph = static_cast<uint32_t>(j) & 1u;
-            const int st = j % C::kPairs;
-            const uint32_t st_ph = static_cast<uint32_t>(j / C::kPairs) & 1u;
+            const int st = j % C::kStats;
+            const uint32_t st_ph = static_cast<uint32_t>(j / C::kStats) & 1u;
             uint2 mw = make_uint2(~0u, ~0u);
             if (!KEY && MASK && row_masked) mw = __ldg(reinterpret_cast<const uint2*>(mrow + 4 * tile) + g);
             ok = KEY ? wait_bounded(bar(C::kT0Full), ph, wd, ROLE_SOFTMAX, SITE_T0_FULL)
                      : wait_bounded(bar(C::kT0Full + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_SOFTMAX, SITE_T0_FULL);
             // the statistics (and mask words) of this stage have landed
-            if (KEY) ok = ok && wait_bounded(bar(C::kXFull + (2 * j + 1) % S), static_cast<uint32_t>((2 * j + 1) / S) & 1u, wd, ROLE_SOFTMAX, SITE_X_FULL);
+            if (KEY) ok = ok && wait_bounded(bar(C::kX1Full + j % R1), static_cast<uint32_t>(j / R1) & 1u, wd, ROLE_SOFTMAX, SITE_X_FULL);
             if (KEY && MASK) ok = ok && wait_bounded(bar(C::kMaskFull + st), st_ph, wd, ROLE_SOFTMAX, SITE_MASK_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             const uint32_t tS = (KEY || !(j & 1)) ? tT0 : tT0b;
-            const float4* sl = reinterpret_cast<const float4*>(smem + C::kStatOffset + st * C::kStatBytes) + 16 * g;
+            // P, then dS: 64 values a thread.  A query CTA's thread holds one row (its
+            // statistics in registers) and 64 columns.  A key CTA's statistics go by
+            // column: its thread holds four rows, lane / 4 + 8 i, and of every 8
+            // columns the pair 2 (lane mod 4), so that it reads a quarter of them --
+            // with a row a thread, broadcasting them from shared memory took half
+            // of its bandwidth from the products (1.50 ms of key CTAs against 1.20).
             float p[64];
+            const float2* nl = reinterpret_cast<const float2*>(smem + C::kStatOffset + st * C::kStatBytes) + 32 * g + (lane & 3);
             {
                 uint32_t s0[32], s1[32];
-                tmem_ld32(tS, s0);
-                tmem_ld32(tS + 32, s1);
+                if constexpr (KEY) {
+                    tmem_ld_16x256b_x8(tS, s0);
+                    tmem_ld_16x256b_x8(tS + (16u << 16), s1);
+                } else {
+                    tmem_ld32(tS, s0);
+                    tmem_ld32(tS + 32, s1);
+                }
                 tmem_ld_wait_dep(s0);
                 reg_dep(s1);
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    const float4 n = KEY ? sl[c / 4] : make_float4(nlse, nlse, nlse, nlse);
-                    const uint32_t* s = c < 32 ? s0 + c : s1 + (c - 32);
-                    ffma2(p[c], p[c + 1], __uint_as_float(s[0]), __uint_as_float(s[1]), sl2, n.x, n.y);
-                    ffma2(p[c + 2], p[c + 3], __uint_as_float(s[2]), __uint_as_float(s[3]), sl2, n.z, n.w);
+                for (int c = 0; c < 32; c += 4) {
+                    const float2 n = KEY ? nl[c] : make_float2(nlse, nlse);    // columns 2c .. 2c + 7 of this half
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        ffma2(p[c + i], p[c + i + 1], __uint_as_float(s0[c + i]), __uint_as_float(s0[c + i + 1]), sl2, n.x, n.y);
+                        ffma2(p[32 + c + i], p[32 + c + i + 1], __uint_as_float(s1[c + i]), __uint_as_float(s1[c + i + 1]), sl2, n.x, n.y);
+                    }
                 }
             }
 #pragma unroll
             for (int c = 0; c < 64; ++c) p[c] = ex2_approx(p[c]);
             if constexpr (MASK) {
                 if constexpr (KEY) {
-                    const uint4* m = reinterpret_cast<const uint4*>(smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 4) + 16 * g;
+                    const uint2* m = reinterpret_cast<const uint2*>(smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 2) + 32 * g + (lane & 3);
+                    const int r = lane >> 2;
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const uint4 w = m[c / 4];
-                        if (!((w.x >> lane) & 1u)) p[c] = 0.f;
-                        if (!((w.y >> lane) & 1u)) p[c + 1] = 0.f;
-                        if (!((w.z >> lane) & 1u)) p[c + 2] = 0.f;
-                        if (!((w.w >> lane) & 1u)) p[c + 3] = 0.f;
+                    for (int c = 0; c < 32; c += 4) {
+                        const uint2 w = m[c];
+                        if (!((w.x >> r) & 1u)) p[c] = 0.f;
+                        if (!((w.y >> r) & 1u)) p[c + 1] = 0.f;
+                        if (!((w.x >> (r + 8)) & 1u)) p[c + 2] = 0.f;
+                        if (!((w.y >> (r + 8)) & 1u)) p[c + 3] = 0.f;
+                        if (!((w.x >> (r + 16)) & 1u)) p[32 + c] = 0.f;
+                        if (!((w.y >> (r + 16)) & 1u)) p[32 + c + 1] = 0.f;
+                        if (!((w.x >> (r + 24)) & 1u)) p[32 + c + 2] = 0.f;
+                        if (!((w.y >> (r + 24)) & 1u)) p[32 + c + 3] = 0.f;
                     }
                 } else {
 #pragma unroll
@@ -533,21 +595,27 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
             tc_fence_after();
             {
                 uint32_t s0[32], s1[32];
-                tmem_ld32(tT1, s0);
-                tmem_ld32(tT1 + 32, s1);
+                if constexpr (KEY) {
+                    tmem_ld_16x256b_x8(tT1, s0);
+                    tmem_ld_16x256b_x8(tT1 + (16u << 16), s1);
+                } else {
+                    tmem_ld32(tT1, s0);
+                    tmem_ld32(tT1 + 32, s1);
+                }
                 tmem_ld_wait_dep(s0);
                 reg_dep(s1);
                 if constexpr (!KEY) {
                     tc_fence_before();
                     mbar_arrive(bar(C::kT1Read));
                 }
-                const float4* sd = sl + kT / 4;
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    const float4 n = KEY ? sd[c / 4] : make_float4(ndelta, ndelta, ndelta, ndelta);
-                    const uint32_t* s = c < 32 ? s0 + c : s1 + (c - 32);
-                    fadd2_mul2(p[c], p[c + 1], __uint_as_float(s[0]), __uint_as_float(s[1]), n.x, n.y, p[c], p[c + 1]);
-                    fadd2_mul2(p[c + 2], p[c + 3], __uint_as_float(s[2]), __uint_as_float(s[3]), n.z, n.w, p[c + 2], p[c + 3]);
+                for (int c = 0; c < 32; c += 4) {
+                    const float2 n = KEY ? nl[kT / 2 + c] : make_float2(ndelta, ndelta);
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        fadd2_mul2(p[c + i], p[c + i + 1], __uint_as_float(s0[c + i]), __uint_as_float(s0[c + i + 1]), n.x, n.y, p[c + i], p[c + i + 1]);
+                        fadd2_mul2(p[32 + c + i], p[32 + c + i + 1], __uint_as_float(s1[c + i]), __uint_as_float(s1[c + i + 1]), n.x, n.y, p[32 + c + i], p[32 + c + i + 1]);
+                    }
                 }
             }
             store_bf16(p, KEY ? tT1 : tS);
