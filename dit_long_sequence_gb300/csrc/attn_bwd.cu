@@ -149,8 +149,11 @@ struct Cfg {
     static constexpr int kT0Full = kX1Empty + kR1;       // two (query CTA's two T0)
     static constexpr int kT1Full = kT0Full + 2;
     static constexpr int kP = kT1Full + 1;
+    // Two, by the tile's parity: a query CTA's softmax warps may finish dS(j+1)
+    // before the MMA warp has looked for dS(j), and one barrier would then be a
+    // phase past the one it waits for.  (dS(j+2) needs T1(j+2), issued after that.)
     static constexpr int kDS = kP + 1;
-    static constexpr int kT1Read = kDS + 1;
+    static constexpr int kT1Read = kDS + 2;
     static constexpr int kAccFinal = kT1Read + 1;
     static constexpr int kMaskFull = kAccFinal + 1;
     static constexpr int kDrain = kMaskFull + kStats;
@@ -259,6 +262,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
         mbar_init(bar(C::kT1Full), 1);
         mbar_init(bar(C::kP), 256);
         mbar_init(bar(C::kDS), 256);
+        mbar_init(bar(C::kDS + 1), 256);
         mbar_init(bar(C::kT1Read), 256);
         mbar_init(bar(C::kAccFinal), 1);
         for (int s = 0; s < C::kStats; ++s) mbar_init(bar(C::kMaskFull + s), 32);
@@ -426,7 +430,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                         issue_t(tT0, sF0, x0(j + 1));
                         umma_commit_warp(bar(C::kT0Full));
                     }
-                    ok = wait_bounded_warp(bar(C::kDS), ph, wd, ROLE_MMA, SITE_DS_READY);
+                    ok = wait_bounded_warp(bar(C::kDS + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_MMA, SITE_DS_READY);
                     if (!ok) break;
                     tc_fence_after();
                     issue_acc(tA0, tT1, x0(j), j > 0);
@@ -452,7 +456,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                         umma_commit_warp(bar(C::kT1Full));
                         umma_commit_warp(bar(C::kX1Empty + (j + 1) % R1));
                     }
-                    ok = wait_bounded_warp(bar(C::kDS), ph, wd, ROLE_MMA, SITE_DS_READY);
+                    ok = wait_bounded_warp(bar(C::kDS + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_MMA, SITE_DS_READY);
                     if (!ok) break;
                     tc_fence_after();
                     issue_acc(tA0, (j & 1) ? tT0b : tT0, x0(j), j > 0);
@@ -621,7 +625,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
             store_bf16(p, KEY ? tT1 : tS);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(bar(C::kDS));
+            mbar_arrive(bar(C::kDS + (j & 1)));
         }
 
         // ---------------------------------------------------------------- epilogue

@@ -20,6 +20,13 @@ def dl():
     return m
 
 
+@pytest.fixture(autouse=True)
+def no_wait_ran_out(dl):
+    yield
+    rc, info = dl.check_watchdog()
+    assert rc == 0, info
+
+
 def _inputs(B, Nq, Nkv, H, D, seed, scale_q=1.5):
     g = wl.generator(DEV, seed)
 
@@ -67,8 +74,6 @@ def test_matches_the_formulas(dl, B, Nq, Nkv, H, D, out_dtype, grad_dtype):
         torch.cuda.synchronize()
         _check(grads, q, k, v, out, lse, dout, scale, allow)
         assert (grads[1][:, kvl:] == 0).all() and (grads[2][:, kvl:] == 0).all()
-    rc, info = dl.check_watchdog()
-    assert rc == 0, info
 
 
 def _mask(kind, B, R, Nk, g):
@@ -106,8 +111,6 @@ def test_masked_matches_the_formulas(dl, kind, B, Nq, Nkv, H, D, rows, kvl):
     _check(grads, q, k, v, out, lse, dout, scale, allow)
     empty = ~allow[:, 0].any(-1)
     assert (grads[0][empty] == 0).all()
-    rc, info = dl.check_watchdog()
-    assert rc == 0, info
 
 
 def test_shared_mask_and_no_mask_rows(dl):
