@@ -97,8 +97,8 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     if (cudaGetDevice(&dev) != cudaSuccess) return DIT_ERR_CUDA;
     const BwdPlan p = plan_attn_bwd(B, Nq, Nkv, H, D, any_keys ? key_valid_len : 0, device_sm_count(dev));
     const bool with_mask = mask != nullptr && mask->rows > 0 && any_keys;
-    // CTAs and partial tiles are counted in 32-bit ints on the device.
-    if (p.key_items * p.f_kv + p.query_items * p.f_q > 0x7fffffffLL ||
+    // Items and partial tiles are counted in 32-bit ints on the device.
+    if (p.key_items * p.f_kv + p.query_items * p.f_q > 0x7ffffff0LL - device_sm_count(dev) ||
         static_cast<int64_t>(B) * H * 128 * (p.q_tiles > p.kv_out_tiles ? p.q_tiles : p.kv_out_tiles) > (int64_t(1) << 37))
         return DIT_ERR_UNSUPPORTED;
     const int64_t need = p.stat_bytes + p.part_kv_bytes + p.part_q_bytes + (with_mask ? occ_bytes(B, p) : 0);
@@ -143,8 +143,12 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     a.sdv = st->dv;
     a.f_kv = p.f_kv;
     a.f_q = p.f_q;
-    a.n_kv_ctas = static_cast<int>(p.key_items * p.f_kv);
-    a.n_q_ctas = static_cast<int>(p.query_items * p.f_q);
+    a.n_kv_items = static_cast<int>(p.key_items * p.f_kv);
+    a.n_q_items = static_cast<int>(p.query_items * p.f_q);
+    a.grid = std::min(device_sm_count(dev), a.n_kv_items + a.n_q_items);
+    const int64_t wide = grad_dtype == DIT_F32 ? 8 : 16;
+    a.wide = (Nq == 0 || (multiple(st->dq, wide) && on(dq, 32))) &&
+             (Nkv == 0 || (multiple(st->dk, wide) && multiple(st->dv, wide) && on(dk, 32) && on(dv, 32)));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool grad_bf16 = grad_dtype == DIT_BF16;
     if (any_keys) {

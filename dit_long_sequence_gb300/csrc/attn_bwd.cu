@@ -7,20 +7,26 @@
 //     dS = P o (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q:
 // the probabilities are recomputed tile by tile, never stored.
 //
-// Two kinds of CTA in one grid, so that no gradient is summed through memory
-// and every result repeats bit for bit (no atomics):
-//   key CTA    one 128-key tile of a (b, h); streams the 128-row query tiles,
-//              S^T = K Q^T and dP^T = V dO^T (rows are keys), then
-//              dV += P^T dO and dK += dS^T Q;
-//   query CTA  one 128-row query tile; streams the key tiles,
-//              S = Q K^T and dP = dO V^T, then dQ += dS K.
+// Two kinds of work item, so that no gradient is summed through memory and
+// every result repeats bit for bit (no atomics):
+//   key item    one 128-key tile of a (b, h); streams the 128-row query tiles,
+//               S^T = K Q^T and dP^T = V dO^T (rows are keys), then
+//               dV += P^T dO and dK += dS^T Q;
+//   query item  one 128-row query tile; streams the key tiles,
+//               S = Q K^T and dP = dO V^T, then dQ += dS K.
 // Seven products a tile pair instead of five: the two recomputed ones cost
 // 40% more tensor work, against fp32 atomics of 64 KB a tile pair into L2 (or a
-// serial order of CTAs) for one kind of CTA that also adds into dQ.
+// serial order of CTAs) for one kind of item that also adds into dQ.
+//
+// One CTA per SM takes its share of the key items, then of the query items
+// (starting where the key items left off, so that shares differ by an item at
+// most).  Its roles run on through the items without meeting: while the softmax
+// warps write one item's gradient, the next one's fixed tiles are on their way
+// and its first products run.
 //
 // In both, the streamed tiles come in pairs (X0, X1) = (Q, dO) or (K, V), the
 // fixed ones are (F0, F1) = (K, V) or (Q, dO), and
-//   T0 = F0 X0^T, T1 = F1 X1^T, ACC1 += P X1 (key CTA), ACC0 += dS X0,
+//   T0 = F0 X0^T, T1 = F1 X1^T, ACC1 += P X1 (key item), ACC0 += dS X0,
 // with P and dS the TMEM A operands, written by the softmax warps in bf16 over
 // their own half of T0 / T1.
 //
@@ -30,20 +36,20 @@
 //   warp 8          tcgen05.mma issuer (warp-wide, one elected lane issues);
 //                   owns the TMEM allocation
 //   warp 9          TMA producer (one thread)
-//   warp 10         stages mask words (key CTAs with a mask)
+//   warp 10         stages mask words (key items with a mask)
 // Registers: 168 at launch; softmax 208, the rest 88 (as the forward kernel).
 // TMEM (512 columns): T0 [0,128) T1 [128,256) ACC0 [256,256+D)
 // ACC1 or the second T0 [256+D, ...).
 //
-// Order of products.  Key CTA, per tile j: dV(j) when P(j) is ready, S(j+1),
+// Order of products.  Key item, per tile j: dV(j) when P(j) is ready, S(j+1),
 // dK(j) when dS(j) is ready, dP(j+1); the softmax warps form P(j+1) while dK(j)
-// and dP(j+1) run and dS(j) while dV(j) and S(j+1) run.  Query CTA: S(j+1) into
+// and dP(j+1) run and dS(j) while dV(j) and S(j+1) run.  Query item: S(j+1) into
 // the other T0, dP(j+1) once dP(j) is in registers, dQ(j) when dS(j) (written
 // over S(j)) is ready.
 //
 // Rows without an allowed key have LSE = -inf; they, and the rows past Nq, get
 // P = 0 through a stored -LSE of -inf.  Keys past kv_len are zero-filled by the
-// tensor maps and masked (query CTA) or not stored (key CTA: their gradients
+// tensor maps and masked (query item) or not stored (key item: their gradients
 // are written as zeros).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -66,7 +72,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum BwdSite : uint32_t {
     SITE_FIX_FULL = 11, SITE_X_FULL = 12, SITE_X_EMPTY = 13, SITE_T0_FULL = 14, SITE_T1_FULL = 15, SITE_P_READY = 16,
     SITE_DS_READY = 17, SITE_T1_READ = 18, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21,
-    SITE_NO_ROOM = 22
+    SITE_NO_ROOM = 22, SITE_FIX_EMPTY = 23, SITE_ACC_FREE = 24
 };
 constexpr uint32_t ROLE_MASK = 4;
 
@@ -142,10 +148,9 @@ struct Cfg {
     static constexpr int kMaskBytes = MASK ? kT * 16 : 0;   // 4 words x 128 rows
     // barriers
     static constexpr int kFixFull = 0;
-    static constexpr int kX0Full = 1;
-    static constexpr int kX0Empty = kX0Full + kR0;
-    static constexpr int kX1Full = kX0Empty + kR0;
-    static constexpr int kX1Empty = kX1Full + kR1;
+    static constexpr int kXFull = 1;                     // X0 and X1 of a tile (by X0's slot)
+    static constexpr int kX0Empty = kXFull + kR0;
+    static constexpr int kX1Empty = kX0Empty + kR0;
     static constexpr int kT0Full = kX1Empty + kR1;       // two (query CTA's two T0)
     static constexpr int kT1Full = kT0Full + 2;
     static constexpr int kP = kT1Full + 1;
@@ -155,13 +160,16 @@ struct Cfg {
     static constexpr int kDS = kP + 1;
     static constexpr int kT1Read = kDS + 2;
     static constexpr int kAccFinal = kT1Read + 1;
-    static constexpr int kMaskFull = kAccFinal + 1;
+    static constexpr int kAccFree = kAccFinal + 1;       // the accumulators have been read
+    static constexpr int kFixEmpty = kAccFree + 1;       // the last T0, T1 of an item are done
+    static constexpr int kMaskFull = kFixEmpty + 1;
     static constexpr int kDrain = kMaskFull + kStats;
     static constexpr int kNumBars = kDrain + 1;
     static constexpr int kStatOffset = (2 + kR0 + kR1) * kTile;
     static constexpr int kMaskOffset = kStatOffset + kStats * kStatBytes;
     static constexpr int kBarOffset = kMaskOffset + kStats * kMaskBytes;
-    static constexpr int kUsedBytes = kBarOffset + kNumBars * 8 + 16;
+    // two sets of barriers: key items', query items'
+    static constexpr int kUsedBytes = kBarOffset + 2 * kNumBars * 8 + 16;
     // with room to start on a 1,024-byte boundary where the buffer does not
     static constexpr int kSmemBytes = kUsedBytes + 1024 <= 232448 ? kUsedBytes + 1024 : 232448;
     static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStats == kR0), "shared memory");
@@ -170,369 +178,456 @@ struct Cfg {
     static_assert(kColAcc1 + 128 <= 512, "TMEM");
 };
 
-// The streamed tiles of a CTA in order: all of [begin, end), or those whose
-// occupancy bit is set -- for a key CTA the bit of its key tile in each query
-// block's words, for a query CTA the set bits of its block's words.
+// One item: its fixed tile, and the streamed tiles [begin, end) of its piece.
 template <bool KEY>
-struct Stream {
-    const uint32_t* occ;      // nullptr: all.  KEY: batch's words; else: this block's words
-    int words, fixed, t, end;
-    __device__ Stream(const uint32_t* o, int w, int f, int begin, int e) : occ(o), words(w), fixed(f), t(begin), end(e) {}
-    __device__ bool hit(int i) const {
-        if (occ == nullptr) return true;
-        if (KEY) return (occ[static_cast<int64_t>(i >> 1) * words + (fixed >> 5)] >> (fixed & 31)) & 1u;
-        return (occ[i >> 5] >> (i & 31)) & 1u;
-    }
-    __device__ int next() {
-        while (t < end) {
-            const int i = t++;
-            if (hit(i)) return i;
-        }
-        return -1;
-    }
-    __device__ int count() const {
-        if (occ == nullptr) return end - t;
-        int c = 0;
-        for (int i = t; i < end; ++i) c += hit(i) ? 1 : 0;
-        return c;
-    }
+struct Item {
+    int b, h, fixed, begin, end;
+    int64_t part_tile;          // its place among the partials
 };
 
-template <int D, bool KEY, bool OUT_BF16, bool MASK>
-__device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtensorMap& tm_f1, const CUtensorMap& tm_x0,
-                                         const CUtensorMap& tm_x1, const AttnBwdArgs& a, int slot) {
-    using C = Cfg<D, MASK>;
-    constexpr int R0 = C::kR0, R1 = C::kR1;
-    constexpr int TILE = C::kTile;
+// The items of this CTA: every gridDim.x-th, the query items beginning behind
+// the CTA that took the last key item.
+template <bool KEY>
+__device__ __forceinline__ int first_item(const AttnBwdArgs& a) {
+    const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    return KEY ? c : (c + g - a.n_kv_items % g) % g;
+}
+template <bool KEY>
+__device__ __forceinline__ int item_count(const AttnBwdArgs& a) { return KEY ? a.n_kv_items : a.n_q_items; }
 
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t s_base = smem_u32(smem);
-    // Dynamic shared memory starts on a 1,024-byte boundary when a kernel has no
-    // other; the whole grid would give up alike if it ever did not fit.
-    if (s_base + C::kUsedBytes > smem_u32(smem_raw) + C::kSmemBytes) {
-        if (threadIdx.x == 0 && atomicCAS(a.status, 0u, 5u) == 0u) atomicExch(a.status + 3, static_cast<unsigned>(SITE_NO_ROOM));
-        return;
-    }
-    const uint32_t sF0 = s_base, sF1 = s_base + TILE;
-    const uint32_t sX0 = s_base + 2 * TILE, sX1 = sX0 + R0 * TILE;
-    const uint32_t sStat = s_base + C::kStatOffset;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* never_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
-    auto bar = [&](int i) -> uint32_t { return smem_u32(bars + i); };
-
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-
-    // The item (b, h, fixed tile) and its range of streamed tiles.
+// Items count pieces fastest, then tiles, then heads, so that the CTAs at work
+// share a few heads' tiles in L2; with a mask heads before tiles, since masks
+// tend to load some tiles of every head (the first frame's, the first keys')
+// more than others, and those then begin together.
+template <bool KEY, bool MASK>
+__device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int slot) {
+    Item<KEY> it;
     const int f = KEY ? a.f_kv : a.f_q;
     const int tiles = KEY ? a.kv_out_tiles : a.q_tiles;
     const int piece = slot % f;
     const int item = slot / f;
-    const int fixed = item % tiles;
-    const int h = (item / tiles) % a.H;
-    const int b = item / tiles / a.H;
-    const int row0 = fixed * kT;
+    const int bhs = a.B * a.H;
+    it.fixed = MASK ? item / bhs : item % tiles;
+    const int bh = MASK ? item % bhs : item / tiles;
+    it.h = bh % a.H;
+    it.b = bh / a.H;
+    it.part_tile = (static_cast<int64_t>(bh) * tiles + it.fixed) * f + piece;
     // a key tile wholly past kv_len has nothing to stream: its gradient is zero
-    const int x_tiles = KEY ? (fixed < a.kv_tiles ? a.q_tiles : 0) : a.kv_tiles;
-    const int begin = static_cast<int>(static_cast<int64_t>(piece) * x_tiles / f);
-    const int end = static_cast<int>(static_cast<int64_t>(piece + 1) * x_tiles / f);
-    if (!in_bounds(b < a.B && fixed < tiles && begin >= 0 && end <= x_tiles, a.status, 0, BND_ITEM)) return;
-    const uint32_t* occ = nullptr;
-    if (MASK && a.occ != nullptr)
-        occ = a.occ + (static_cast<int64_t>(b) * a.occ_blocks + (KEY ? 0 : fixed >> 1)) * a.occ_words;
-    const Stream<KEY> stream(occ, a.occ_words, fixed, begin, end);
-    const int n_tiles = stream.count();
-    const float* const stat = a.stat + (static_cast<int64_t>(b) * a.H + h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
+    const int x_tiles = KEY ? (it.fixed < a.kv_tiles ? a.q_tiles : 0) : a.kv_tiles;
+    it.begin = static_cast<int>(static_cast<int64_t>(piece) * x_tiles / f);
+    it.end = static_cast<int>(static_cast<int64_t>(piece + 1) * x_tiles / f);
+    return it;
+}
 
-    if (threadIdx.x == 0) {
-        mbar_init(bar(C::kFixFull), 1);
-        for (int s = 0; s < R0; ++s) {
-            mbar_init(bar(C::kX0Full + s), 1);
-            mbar_init(bar(C::kX0Empty + s), 1);
+// The streamed tiles of an item in order: all of [begin, end), or with an
+// occupancy map those whose bit is set -- a key item's the bit of its key tile
+// in each 256-row query block's words, a query item's the bits of its block's
+// words.  A warp holds the bits in its lanes (lane w: bits 32 w ..), 1,024 of
+// them; items beyond that many blocks (key) or key tiles (query) are streamed
+// whole.  Every call is made by a whole, converged warp.
+template <bool KEY, bool MASK>
+struct Stream {
+    int t, end;
+    uint32_t bits;
+    bool whole;
+    __device__ Stream(const AttnBwdArgs& a, const Item<KEY>& it) : t(it.begin), end(it.end), bits(0u), whole(true) {
+        if constexpr (MASK) {
+            const int n = KEY ? (a.q_tiles + 1) >> 1 : a.kv_tiles;
+            if (a.occ == nullptr || n > 1024 || t >= end) return;
+            whole = false;
+            const int lane = static_cast<int>(lane_id());
+            const uint32_t* occ = a.occ + static_cast<int64_t>(it.b) * a.occ_blocks * a.occ_words;
+            if constexpr (KEY) {
+                for (int w = 0; w * 32 < n; ++w) {
+                    const int blk = w * 32 + lane;
+                    const bool on = blk < n && ((occ[static_cast<int64_t>(blk) * a.occ_words + (it.fixed >> 5)] >> (it.fixed & 31)) & 1u);
+                    const uint32_t all = __ballot_sync(0xffffffffu, on);
+                    if (lane == w) bits = all;
+                }
+            } else {
+                if (lane < a.occ_words) bits = occ[static_cast<int64_t>(it.fixed >> 1) * a.occ_words + lane];
+            }
         }
-        for (int s = 0; s < R1; ++s) {
-            mbar_init(bar(C::kX1Full + s), 1);
-            mbar_init(bar(C::kX1Empty + s), 1);
+    }
+    // the next tile, or -1
+    __device__ __forceinline__ int next() {
+        if constexpr (MASK) {
+            while (!whole && t < end) {
+                const int i = KEY ? t >> 1 : t;
+                const uint32_t w = __shfl_sync(0xffffffffu, bits, i >> 5) >> (i & 31);
+                if (w & 1u) break;
+                const int skip = w != 0u ? __ffs(static_cast<int>(w)) - 1 : 32 - (i & 31);
+                t = KEY ? (i + skip) * 2 : i + skip;
+            }
         }
-        mbar_init(bar(C::kT0Full), 1);
-        mbar_init(bar(C::kT0Full + 1), 1);
-        mbar_init(bar(C::kT1Full), 1);
-        mbar_init(bar(C::kP), 256);
-        mbar_init(bar(C::kDS), 256);
-        mbar_init(bar(C::kDS + 1), 256);
-        mbar_init(bar(C::kT1Read), 256);
-        mbar_init(bar(C::kAccFinal), 1);
-        for (int s = 0; s < C::kStats; ++s) mbar_init(bar(C::kMaskFull + s), 32);
-        mbar_init(bar(C::kDrain), 1);
-        *abort_flag = 0;
-        *never_flag = 0;
-        fence_mbar_init();
+        return t < end ? t++ : -1;
     }
-    if (warp == 8) {
-        tmem_alloc(smem_u32(tmem_slot), 512);
-        tmem_relinquish();
+    __device__ __forceinline__ int count() const {
+        if constexpr (MASK) {
+            if (!whole) {
+                Stream c = *this;
+                int n = 0;
+                while (c.next() >= 0) ++n;
+                return n;
+            }
+        }
+        return end - t;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const Watchdog wd{a.status, a.timeout_ns, abort_flag};
-    const Watchdog wd_drain{a.status, a.timeout_ns, never_flag};   // ignores the abort flag: work already in flight
+};
 
-    if (warp == 11) {
-        regs_decrease<kOtherRegs>();
-    } else if (warp == 10) {
-        regs_decrease<kOtherRegs>();
-        // ------------------------------------- mask words of the streamed query rows
-        // Stage j holds word w (keys 32w .. of the fixed tile) of row r at [w][r];
-        // a stage is free again when its X0 slot is (dK of that tile is done).
-        if (KEY && MASK) {
-            Stream<KEY> cur = stream;
-            for (int j = 0; j < n_tiles; ++j) {
-                const int tile = cur.next();
-                const int st = j % C::kStats;
-                const uint32_t ph = static_cast<uint32_t>(j / C::kStats) & 1u;
-                if (!wait_bounded_warp(bar(C::kX0Empty + st), ph ^ 1u, wd, ROLE_MASK, SITE_X_EMPTY)) break;
-                uint32_t* dst = reinterpret_cast<uint32_t*>(smem + C::kMaskOffset + st * C::kMaskBytes);
+// What the roles of a CTA share.
+template <int D, bool MASK>
+struct Cta {
+    using C = Cfg<D, MASK>;
+    uint8_t* smem;
+    uint32_t base, bars, tmem;
+    Watchdog wd, wd_drain;      // wd_drain ignores the abort flag: it waits for work already in flight
+    template <bool KEY>
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + ((KEY ? 0 : C::kNumBars) + i) * 8; }
+    __device__ __forceinline__ uint32_t f0() const { return base; }
+    __device__ __forceinline__ uint32_t f1() const { return base + C::kTile; }
+    __device__ __forceinline__ uint32_t x0(int j) const { return base + (2 + j % C::kR0) * C::kTile; }
+    __device__ __forceinline__ uint32_t x1(int j) const { return base + (2 + C::kR0 + j % C::kR1) * C::kTile; }
+};
+// The parity of use n of a slot of r.
+__device__ __forceinline__ uint32_t turn(int n, int r) { return static_cast<uint32_t>(n / r) & 1u; }
+
+// ------------------------------------------------------------ TMA producer (a warp; lane 0 issues)
+template <int D, bool KEY, bool MASK>
+__device__ __forceinline__ void produce(const Cta<D, MASK>& s, const CUtensorMap& tm_f0, const CUtensorMap& tm_f1,
+                                        const CUtensorMap& tm_x0, const CUtensorMap& tm_x1, const AttnBwdArgs& a) {
+    using C = Cfg<D, MASK>;
+    constexpr int R0 = C::kR0, R1 = C::kR1;
+    const bool leader = lane_id() == 0;
+    auto bar = [&](int i) { return s.template bar<KEY>(i); };
+    auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded_warp(bar(i), parity, s.wd, ROLE_LOAD, site); };
+    auto copy = [&](const CUtensorMap* tm, uint32_t dst, int full, int row, int h, int b) {
+        for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * C::kBlock, tm, bar(full), c * 64, row, h, b);
+    };
+    int J = 0, I = 0;                   // tiles and items so far
+    int done = 0;                       // tiles copied
+    int half = -1;                      // a tile whose X0 alone was copied
+    bool ok = true;
+    for (int slot = first_item<KEY>(a); ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
+        const Item<KEY> it = decode<KEY, MASK>(a, slot);
+        Stream<KEY, MASK> stream(a, it);
+        const int n = stream.count();
+        if (n == 0) continue;
+        ok = wait(C::kFixEmpty, (I & 1) ^ 1u, SITE_FIX_EMPTY);
+        if (!ok) break;
+        if (leader) {
+            mbar_arrive_expect_tx(bar(C::kFixFull), 2 * C::kTile);
+            copy(&tm_f0, s.f0(), C::kFixFull, it.fixed * kT, it.h, it.b);
+            copy(&tm_f1, s.f1(), C::kFixFull, it.fixed * kT, it.h, it.b);
+        }
+        ++I;
+        const float* const stat = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
+        for (int j = 0; j < n; ++j, ++J) {
+            const int x_row = stream.next() * kT;
+            ok = in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len), a.status, ROLE_LOAD, BND_KEY) &&
+                 wait(C::kX0Empty + J % R0, turn(J, R0) ^ 1u, SITE_X_EMPTY);
+            if (!ok) break;
+            const int full = C::kXFull + J % R0;
+            if (leader) {
+                mbar_arrive_expect_tx(bar(full), 2 * C::kTile + (KEY ? C::kStatBytes : 0));
+                copy(&tm_x0, s.x0(J), full, x_row, it.h, it.b);
+            }
+            half = J;
+            ok = wait(C::kX1Empty + J % R1, turn(J, R1) ^ 1u, SITE_X_EMPTY);
+            if constexpr (KEY && R0 > C::kStats) {
+                // The rows' statistics come with X1; their stage is free when X0 of
+                // kStats tiles ago has been released.
+                const int o = J - C::kStats;
+                if (o >= 0) ok = ok && wait(C::kX0Empty + o % R0, turn(o, R0), SITE_X_EMPTY);
+            }
+            if (!ok) break;
+            if (leader) {
+                copy(&tm_x1, s.x1(J), full, x_row, it.h, it.b);
+                if constexpr (KEY) {
+                    const uint32_t sd = s.base + C::kStatOffset + J % C::kStats * C::kStatBytes;
+                    bulk_load(sd, stat + x_row, kT * 4, bar(full));
+                    bulk_load(sd + kT * 4, stat + static_cast<int64_t>(a.q_tiles) * kT + x_row, kT * 4, bar(full));
+                }
+            }
+            done = J + 1;
+            half = -1;
+        }
+    }
+    // Every slot released: the query items' copies may follow the key items'.
+    for (int j = J > R0 ? J - R0 : 0; ok && j < J; ++j) ok = wait(C::kX0Empty + j % R0, turn(j, R0), SITE_X_EMPTY);
+    for (int j = J > R1 ? J - R1 : 0; ok && j < J; ++j) ok = wait(C::kX1Empty + j % R1, turn(j, R1), SITE_X_EMPTY);
+    if (ok && I > 0) ok = wait(C::kFixEmpty, (I - 1) & 1, SITE_FIX_EMPTY);
+    if (!ok) {
+        // Winding down: wait (bounded) until every copy issued has landed.
+        auto land = [&](int i, uint32_t parity) { wait_bounded_warp(bar(i), parity, s.wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN); };
+        // (an X0 copied alone: account for its X1 and statistics, so that its barrier completes)
+        if (half >= 0 && leader)
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar(C::kXFull + half % R0)),
+                         "r"(C::kTile + (KEY ? C::kStatBytes : 0)) : "memory");
+        if (half >= 0) done = half + 1;
+        for (int j = done > R0 ? done - R0 : 0; j < done; ++j) land(C::kXFull + j % R0, turn(j, R0));
+        if (I > 0) land(C::kFixFull, (I - 1) & 1);
+    }
+}
+
+// ------------------------------------------- mask words of the streamed query rows (key items; a warp)
+// Stage j holds word w (keys 32w .. of the fixed tile) of row r at [w][r]; a
+// stage is free again when its X0 slot is (dK of that tile is done).
+template <int D, bool MASK>
+__device__ __forceinline__ void stage_mask(const Cta<D, MASK>& s, const AttnBwdArgs& a) {
+    using C = Cfg<D, MASK>;
+    const int lane = static_cast<int>(lane_id());
+    int J = 0;
+    for (int slot = first_item<true>(a); slot < item_count<true>(a); slot += static_cast<int>(gridDim.x)) {
+        const Item<true> it = decode<true, MASK>(a, slot);
+        Stream<true, MASK> stream(a, it);
+        for (int tile = stream.next(); tile >= 0; tile = stream.next(), ++J) {
+            const int st = J % C::kStats;
+            if (!wait_bounded_warp(s.template bar<true>(C::kX0Empty + st), turn(J, C::kStats) ^ 1u, s.wd, ROLE_MASK, SITE_X_EMPTY)) return;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(s.smem + C::kMaskOffset + st * C::kMaskBytes);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i * 32 + lane, row = tile * kT + r;
-                    uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
-                    if (row < a.mask_rows)
-                        w = __ldg(reinterpret_cast<const uint4*>(a.mask + b * a.mask_sb + row * a.mask_si) + fixed);
-                    dst[r] = w.x;
-                    dst[kT + r] = w.y;
-                    dst[2 * kT + r] = w.z;
-                    dst[3 * kT + r] = w.w;
-                }
-                mbar_arrive(bar(C::kMaskFull + st));
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 32 + lane, row = tile * kT + r;
+                uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (row < a.mask_rows)
+                    w = __ldg(reinterpret_cast<const uint4*>(a.mask + it.b * a.mask_sb + row * a.mask_si) + it.fixed);
+                dst[r] = w.x;
+                dst[kT + r] = w.y;
+                dst[2 * kT + r] = w.z;
+                dst[3 * kT + r] = w.w;
             }
+            mbar_arrive(s.template bar<true>(C::kMaskFull + st));
         }
-        __syncwarp();
-    } else if (warp == 9) {
-        regs_decrease<kOtherRegs>();
-        // ------------------------------------------------------------ TMA producer
-        if (lane == 0 && n_tiles > 0) {
-            tma_prefetch_desc(&tm_f0);
-            tma_prefetch_desc(&tm_f1);
-            tma_prefetch_desc(&tm_x0);
-            tma_prefetch_desc(&tm_x1);
-            mbar_arrive_expect_tx(bar(C::kFixFull), 2 * TILE);
-            for (int c = 0; c < D / 64; ++c) {
-                tma_load_4d(sF0 + c * C::kBlock, &tm_f0, bar(C::kFixFull), c * 64, row0, h, b);
-                tma_load_4d(sF1 + c * C::kBlock, &tm_f1, bar(C::kFixFull), c * 64, row0, h, b);
-            }
-            int issued0 = 0, issued1 = 0;
-            Stream<KEY> cur = stream;
-            auto copy = [&](const CUtensorMap* tm, uint32_t dst, int full, int x_row) {
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(dst + c * C::kBlock, tm, bar(full), c * 64, x_row, h, b);
-            };
-            for (int j = 0; j < n_tiles; ++j) {
-                const int x_row = cur.next() * kT;
-                if (!in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len), a.status, ROLE_LOAD, BND_KEY)) break;
-                if (!wait_bounded(bar(C::kX0Empty + j % R0), (static_cast<uint32_t>(j / R0) & 1u) ^ 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
-                mbar_arrive_expect_tx(bar(C::kX0Full + j % R0), TILE);
-                copy(&tm_x0, sX0 + j % R0 * TILE, C::kX0Full + j % R0, x_row);
-                issued0 = j + 1;
-                if (!wait_bounded(bar(C::kX1Empty + j % R1), (static_cast<uint32_t>(j / R1) & 1u) ^ 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
-                if constexpr (KEY) {
-                    // The rows' statistics come with X1; their stage is free when X0
-                    // of kStats tiles ago has been released.
-                    const int o = j - C::kStats;
-                    if (R0 > C::kStats && o >= 0 &&
-                        !wait_bounded(bar(C::kX0Empty + o % R0), static_cast<uint32_t>(o / R0) & 1u, wd, ROLE_LOAD, SITE_X_EMPTY)) break;
-                }
-                mbar_arrive_expect_tx(bar(C::kX1Full + j % R1), TILE + (KEY ? C::kStatBytes : 0));
-                copy(&tm_x1, sX1 + j % R1 * TILE, C::kX1Full + j % R1, x_row);
-                if constexpr (KEY) {
-                    const uint32_t sd = sStat + j % C::kStats * C::kStatBytes;
-                    bulk_load(sd, stat + x_row, kT * 4, bar(C::kX1Full + j % R1));
-                    bulk_load(sd + kT * 4, stat + static_cast<int64_t>(a.q_tiles) * kT + x_row, kT * 4, bar(C::kX1Full + j % R1));
-                }
-                issued1 = j + 1;
-            }
-            if (issued1 < n_tiles || *abort_flag) {
-                // Winding down: wait (bounded) until every copy issued has landed.
-                for (int j = (issued0 > R0 ? issued0 - R0 : 0); j < issued0; ++j)
-                    wait_bounded(bar(C::kX0Full + j % R0), static_cast<uint32_t>(j / R0) & 1u, wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN);
-                for (int j = (issued1 > R1 ? issued1 - R1 : 0); j < issued1; ++j)
-                    wait_bounded(bar(C::kX1Full + j % R1), static_cast<uint32_t>(j / R1) & 1u, wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN);
-                wait_bounded(bar(C::kFixFull), 0, wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        regs_decrease<kOtherRegs>();
-        // ------------------------------------------------------------- MMA issuer
-        if (n_tiles > 0) {
-            constexpr uint32_t kIdescT = idesc_bf16_f32(kT, kT, false);
-            constexpr uint32_t kIdescAcc = idesc_bf16_f32(kT, D, true);
-            const uint32_t tT0 = tmem + C::kColT0, tT1 = tmem + C::kColT1;
-            const uint32_t tT0b = tmem + C::kColAcc1;      // query CTA: the second T0
-            const uint32_t tA0 = tmem + C::kColAcc0, tA1 = tmem + C::kColAcc1;
+    }
+}
 
-            // T = F X^T, both K-major, K = D channels.
-            auto issue_t = [&](uint32_t tT, uint32_t f_addr, uint32_t x_addr) {
-                const uint64_t df = sdesc_sw128(f_addr, 16, 1024), dx = sdesc_sw128(x_addr, 16, 1024);
-                static_for<D / 16>([&](auto kk) {
-                    constexpr uint32_t off = (kk.value >> 2) * C::kBlock + (kk.value & 3) * 32;
-                    umma_ss_warp<off>(tT, df, dx, kIdescT, kk.value > 0 ? 1u : 0u);
-                });
-            };
-            // ACC (+)= A X, A = bf16 pairs in TMEM (K columns 0-63 in the first 32
-            // columns of T's first half, 64-127 in those of its second), X MN-major.
-            auto issue_acc = [&](uint32_t tA, uint32_t tOp, uint32_t x_addr, bool accumulate) {
-                const uint64_t dx = sdesc_sw128(x_addr, C::kBlock, 1024);
-                static_for<kT / 16>([&](auto kk) {
-                    umma_ts_warp<kk.value * 16 * 128>(tA, tOp + (kk.value >> 2) * 64 + (kk.value & 3) * 8, dx, kIdescAcc,
-                                                      (accumulate || kk.value > 0) ? 1u : 0u);
-                });
-            };
-            auto x0_full = [&](int j) {
-                return wait_bounded_warp(bar(C::kX0Full + j % R0), static_cast<uint32_t>(j / R0) & 1u, wd, ROLE_MMA, SITE_X_FULL);
-            };
-            auto x1_full = [&](int j) {
-                return wait_bounded_warp(bar(C::kX1Full + j % R1), static_cast<uint32_t>(j / R1) & 1u, wd, ROLE_MMA, SITE_X_FULL);
-            };
-            auto x0 = [&](int j) { return sX0 + j % R0 * TILE; };
-            auto x1 = [&](int j) { return sX1 + j % R1 * TILE; };
-
-            bool ok = wait_bounded_warp(bar(C::kFixFull), 0, wd, ROLE_MMA, SITE_FIX_FULL) && x0_full(0);
-            if (ok) {
-                tc_fence_after();
-                issue_t(tT0, sF0, x0(0));
-                umma_commit_warp(bar(C::kT0Full));
-                ok = x1_full(0);
-            }
-            if (ok) {
-                tc_fence_after();
-                issue_t(tT1, sF1, x1(0));
-                umma_commit_warp(bar(C::kT1Full));
-                if (!KEY) umma_commit_warp(bar(C::kX1Empty));
-            }
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                const bool more = j + 1 < n_tiles;
-                const uint32_t ph = static_cast<uint32_t>(j) & 1u;
-                if constexpr (KEY) {
-                    ok = wait_bounded_warp(bar(C::kP), ph, wd, ROLE_MMA, SITE_P_READY);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_acc(tA1, tT0, x1(j), j > 0);
-                    umma_commit_warp(bar(C::kX1Empty + j % R1));
-                    if (more) {
-                        ok = x0_full(j + 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_t(tT0, sF0, x0(j + 1));
-                        umma_commit_warp(bar(C::kT0Full));
-                    }
-                    ok = wait_bounded_warp(bar(C::kDS + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_MMA, SITE_DS_READY);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_acc(tA0, tT1, x0(j), j > 0);
-                    umma_commit_warp(bar(C::kX0Empty + j % R0));
-                    if (more) {
-                        ok = x1_full(j + 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_t(tT1, sF1, x1(j + 1));
-                        umma_commit_warp(bar(C::kT1Full));
-                    }
-                } else {
-                    if (more) {
-                        ok = x0_full(j + 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_t((j & 1) ? tT0 : tT0b, sF0, x0(j + 1));
-                        umma_commit_warp(bar(C::kT0Full + ((j + 1) & 1)));
-                        ok = x1_full(j + 1) && wait_bounded_warp(bar(C::kT1Read), ph, wd, ROLE_MMA, SITE_T1_READ);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_t(tT1, sF1, x1(j + 1));
-                        umma_commit_warp(bar(C::kT1Full));
-                        umma_commit_warp(bar(C::kX1Empty + (j + 1) % R1));
-                    }
-                    ok = wait_bounded_warp(bar(C::kDS + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_MMA, SITE_DS_READY);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_acc(tA0, (j & 1) ? tT0b : tT0, x0(j), j > 0);
-                    umma_commit_warp(bar(C::kX0Empty + j % R0));
-                }
-                if (!more) umma_commit_warp(bar(C::kAccFinal));
-            }
-            // Every product issued must finish before TMEM is released.
-            umma_commit_warp(bar(C::kDrain));
-            wait_bounded_warp(bar(C::kDrain), 0, wd_drain, ROLE_MMA, SITE_BWD_DRAIN);
+// ------------------------------------------------------------ MMA issuer (a warp)
+// A position in a ring: slot, the parity of its use, and the low word of its
+// tile's matrix descriptor (the start address field).  Stepped, not computed from
+// the tile's number: the issue loop is on the products' critical path.
+template <int R, int STEP>
+struct RingPos {
+    uint32_t slot = 0, parity = 0, addr;
+    __device__ explicit RingPos(uint32_t a) : addr(a) {}
+    __device__ __forceinline__ void step() {
+        if (slot == R - 1) {
+            slot = 0;
+            parity ^= 1u;
+            addr -= (R - 1) * STEP;
+        } else {
+            ++slot;
+            addr += STEP;
         }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------- softmax warps
-        regs_increase<kSoftmaxRegs>();
-        const int g = warp >> 2;    // column half
-        const int wq = warp & 3;    // TMEM lane quadrant
-        const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t tT0 = tmem + lane_off + C::kColT0 + 64 * g;
-        const uint32_t tT0b = tmem + lane_off + C::kColAcc1 + 64 * g;
-        const uint32_t tT1 = tmem + lane_off + C::kColT1 + 64 * g;
-        const float sl2 = a.scale_log2;
+    }
+};
+
+// Returns the items worked on; `before`: the key items this CTA worked on, whose
+// accumulators must have been read before the query items' products overwrite them.
+template <int D, bool KEY, bool MASK>
+__device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs& a, int before) {
+    using C = Cfg<D, MASK>;
+    constexpr uint32_t kIdescT = idesc_bf16_f32(kT, kT, false);
+    constexpr uint32_t kIdescAcc = idesc_bf16_f32(kT, D, true);
+    const uint32_t tT0 = s.tmem + C::kColT0, tT1 = s.tmem + C::kColT1;
+    const uint32_t tT0b = s.tmem + C::kColAcc1;      // query items: the second T0
+    const uint32_t tA0 = s.tmem + C::kColAcc0, tA1 = s.tmem + C::kColAcc1;
+    const uint32_t bars = s.template bar<KEY>(0);
+    auto wait = [&](uint32_t i, uint32_t parity, uint32_t site) { return wait_bounded_warp(bars + 8 * i, parity, s.wd, ROLE_MMA, site); };
+    auto commit = [&](uint32_t i) { umma_commit_warp(bars + 8 * i); };
+
+    // Descriptors: K-major operands of T, MN-major ones of ACC; only the start
+    // address (in the low word) differs between tiles.
+    const uint64_t dT = sdesc_sw128(0, 16, 1024), dAcc = sdesc_sw128(0, C::kBlock, 1024);
+    const uint64_t f0 = dT + (s.f0() >> 4), f1 = dT + (s.f1() >> 4);
+    constexpr uint32_t kStep = C::kTile >> 4;
+    // T = F X^T, both K-major, K = D channels.
+    auto issue_t = [&](uint32_t tT, uint64_t df, uint32_t x_addr) {
+        tc_fence_after();
+        const uint64_t dx = dT + x_addr;
+        static_for<D / 16>([&](auto kk) {
+            constexpr uint32_t off = (kk.value >> 2) * C::kBlock + (kk.value & 3) * 32;
+            umma_ss_warp<off>(tT, df, dx, kIdescT, kk.value > 0 ? 1u : 0u);
+        });
+    };
+    // ACC (+)= A X, A = bf16 pairs in TMEM (K columns 0-63 in the first 32
+    // columns of T's first half, 64-127 in those of its second), X MN-major.
+    auto issue_acc = [&](uint32_t tA, uint32_t tOp, uint32_t x_addr, bool accumulate) {
+        tc_fence_after();
+        const uint64_t dx = dAcc + x_addr;
+        static_for<kT / 16>([&](auto kk) {
+            umma_ts_warp<kk.value * 16 * 128>(tA, tOp + (kk.value >> 2) * 64 + (kk.value & 3) * 8, dx, kIdescAcc,
+                                              (accumulate || kk.value > 0) ? 1u : 0u);
+        });
+    };
+    // The next tile for T0 and T1, and the tile whose P, dS are due.
+    RingPos<C::kR0, kStep> n0(s.x0(0) >> 4), c0(s.x0(0) >> 4);
+    RingPos<C::kR1, kStep> n1(s.x1(0) >> 4), c1(s.x1(0) >> 4);
+
+    bool ok = true;
+    if (!KEY && before > 0)
+        ok = wait_bounded_warp(s.template bar<true>(C::kAccFree), (before - 1) & 1, s.wd, ROLE_MMA, SITE_ACC_FREE);
+    uint32_t J = 0;
+    int I = 0;
+    for (int slot = first_item<KEY>(a); ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
+        const int n = Stream<KEY, MASK>(a, decode<KEY, MASK>(a, slot)).count();
+        if (n == 0) continue;
+        // the item's first T0, T1 (the previous item's last products are done with them: in order)
+        ok = wait(C::kFixFull, I & 1, SITE_FIX_FULL) && wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
+        if (!ok) break;
+        issue_t(!KEY && (J & 1) ? tT0b : tT0, f0, n0.addr);
+        commit(C::kT0Full + (KEY ? 0 : J & 1));
+        if (!KEY && J > 0) {
+            ok = wait(C::kT1Read, (J - 1) & 1, SITE_T1_READ);
+            if (!ok) break;
+        }
+        issue_t(tT1, f1, n1.addr);
+        commit(C::kT1Full);
+        if (!KEY) commit(C::kX1Empty + n1.slot);
+        if (n == 1) commit(C::kFixEmpty);
+        n0.step();
+        n1.step();
+        for (int j = 0; j < n; ++j, ++J) {
+            const bool more = j + 1 < n;
+            if constexpr (KEY) {
+                ok = wait(C::kP, J & 1, SITE_P_READY) && (j > 0 || I == 0 || wait(C::kAccFree, (I - 1) & 1, SITE_ACC_FREE));
+                if (!ok) break;
+                issue_acc(tA1, tT0, c1.addr, j > 0);
+                commit(C::kX1Empty + c1.slot);
+                if (more) {
+                    ok = wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
+                    if (!ok) break;
+                    issue_t(tT0, f0, n0.addr);
+                    commit(C::kT0Full);
+                }
+                ok = wait(C::kDS + (J & 1), (J >> 1) & 1, SITE_DS_READY);
+                if (!ok) break;
+                issue_acc(tA0, tT1, c0.addr, j > 0);
+                commit(C::kX0Empty + c0.slot);
+                if (more) {
+                    issue_t(tT1, f1, n1.addr);
+                    commit(C::kT1Full);
+                }
+            } else {
+                if (more) {
+                    ok = wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
+                    if (!ok) break;
+                    issue_t((J & 1) ? tT0 : tT0b, f0, n0.addr);
+                    commit(C::kT0Full + ((J + 1) & 1));
+                    ok = wait(C::kT1Read, J & 1, SITE_T1_READ);
+                    if (!ok) break;
+                    issue_t(tT1, f1, n1.addr);
+                    commit(C::kT1Full);
+                    commit(C::kX1Empty + n1.slot);
+                }
+                ok = wait(C::kDS + (J & 1), (J >> 1) & 1, SITE_DS_READY) &&
+                     (j > 0 || I == 0 || wait(C::kAccFree, (I - 1) & 1, SITE_ACC_FREE));
+                if (!ok) break;
+                issue_acc(tA0, (J & 1) ? tT0b : tT0, c0.addr, j > 0);
+                commit(C::kX0Empty + c0.slot);
+            }
+            if (more) {
+                n0.step();
+                n1.step();
+            }
+            c0.step();
+            c1.step();
+            if (j + 2 == n) commit(C::kFixEmpty);     // the item's last T0 and T1 have been issued
+        }
+        if (!ok) break;
+        commit(C::kAccFinal);
+        ++I;
+    }
+    // Every product issued must finish before TMEM is released.
+    commit(C::kDrain);
+    wait_bounded_warp(bars + 8 * C::kDrain, 0, s.wd_drain, ROLE_MMA, SITE_BWD_DRAIN);
+    return I;
+}
+
+// ------------------------------------------------------- softmax warps (0-7)
+// 8 consecutive 32-bit words (32-byte aligned, or as two 16-byte halves).
+__device__ __forceinline__ void store8(void* p, const uint32_t (&v)[8], bool wide) {
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+template <int D, bool KEY, bool OUT_BF16, bool MASK>
+__device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs& a) {
+    using C = Cfg<D, MASK>;
+    constexpr int R0 = C::kR0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = warp >> 2;    // column half
+    const int wq = warp & 3;    // TMEM lane quadrant
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tT0 = s.tmem + lane_off + C::kColT0 + 64 * g;
+    const uint32_t tT0b = s.tmem + lane_off + C::kColAcc1 + 64 * g;
+    const uint32_t tT1 = s.tmem + lane_off + C::kColT1 + 64 * g;
+    const float sl2 = a.scale_log2;
+    auto bar = [&](int i) { return s.template bar<KEY>(i); };
+    auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded(bar(i), parity, s.wd, ROLE_SOFTMAX, site); };
+    // 64 values -> 32 columns of bf16 pairs at t, in the layout they were read
+    // (key item: the second half of the values are lanes 16-31)
+    auto store_bf16 = [&](const float* v, uint32_t t) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]);
+            if constexpr (KEY) tmem_st_16x128b_x8(t + (static_cast<uint32_t>(16 * c) << 16), pk);
+            else tmem_st16(t + c * 16, pk);
+        }
+    };
+    // A query item's row statistics, asked for one item ahead.
+    float next_nlse = 0.f, next_ndelta = 0.f;
+    auto ask = [&](int slot) {
+        if (KEY || slot >= item_count<KEY>(a) || a.stat == nullptr) return;    // (without keys there are no statistics)
+        const Item<KEY> it = decode<KEY, MASK>(a, slot);
+        const float* p = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT) + it.fixed * kT + wq * 32 + lane;
+        next_nlse = __ldg(p);
+        next_ndelta = __ldg(p + static_cast<int64_t>(a.q_tiles) * kT);
+    };
+
+    int J = 0, I = 0;
+    bool ok = true;
+    int slot = first_item<KEY>(a);
+    ask(slot);
+    for (; ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
+        const Item<KEY> it = decode<KEY, MASK>(a, slot);
+        const int row0 = it.fixed * kT;
         const int row = row0 + wq * 32 + lane;      // this thread's row of the fixed tile
-        bool ok = true;
-        Stream<KEY> cur = stream;
-        // query CTA: this row's statistics and mask words
-        float nlse = 0.f, ndelta = 0.f;
-        bool row_masked = false;
-        const uint32_t* mrow = nullptr;
-        if constexpr (!KEY) {
-            if (n_tiles > 0) {      // without keys there are no statistics
-                nlse = __ldg(stat + row);
-                ndelta = __ldg(stat + static_cast<int64_t>(a.q_tiles) * kT + row);
-            }
-            if (MASK) {
-                row_masked = row < a.mask_rows;
-                mrow = a.mask + b * a.mask_sb + (row_masked ? row : 0) * a.mask_si;
-            }
-        }
-        // 64 values -> 32 columns of bf16 pairs at t, in the layout they were read
-        // (key CTA: the second half of the values are lanes 16-31)
-        auto store_bf16 = [&](const float* v, uint32_t t) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]);
-                if constexpr (KEY) tmem_st_16x128b_x8(t + (static_cast<uint32_t>(16 * c) << 16), pk);
-                else tmem_st16(t + c * 16, pk);
-            }
-        };
+        Stream<KEY, MASK> stream(a, it);
+        const int n_tiles = stream.count();
+        const float nlse = next_nlse, ndelta = next_ndelta;
+        ask(slot + static_cast<int>(gridDim.x));
+        const bool row_masked = !KEY && MASK && row < a.mask_rows;
+        const uint32_t* mrow = row_masked ? a.mask + it.b * a.mask_sb + row * a.mask_si : nullptr;
 
-        for (int j = 0; j < n_tiles; ++j) {
-            const int tile = cur.next();
-            const uint32_t ph = static_cast<uint32_t>(j) & 1u;
-            const int st = j % C::kStats;
-            const uint32_t st_ph = static_cast<uint32_t>(j / C::kStats) & 1u;
+        for (int j = 0; j < n_tiles; ++j, ++J) {
+            const int tile = stream.next();
+            const int st = J % C::kStats;
             uint2 mw = make_uint2(~0u, ~0u);
-            if (!KEY && MASK && row_masked) mw = __ldg(reinterpret_cast<const uint2*>(mrow + 4 * tile) + g);
-            ok = KEY ? wait_bounded(bar(C::kT0Full), ph, wd, ROLE_SOFTMAX, SITE_T0_FULL)
-                     : wait_bounded(bar(C::kT0Full + (j & 1)), static_cast<uint32_t>(j >> 1) & 1u, wd, ROLE_SOFTMAX, SITE_T0_FULL);
+            if (row_masked) mw = __ldg(reinterpret_cast<const uint2*>(mrow + 4 * tile) + g);
+            ok = KEY ? wait(C::kT0Full, J & 1, SITE_T0_FULL) : wait(C::kT0Full + (J & 1), turn(J, 2), SITE_T0_FULL);
             // the statistics (and mask words) of this stage have landed
-            if (KEY) ok = ok && wait_bounded(bar(C::kX1Full + j % R1), static_cast<uint32_t>(j / R1) & 1u, wd, ROLE_SOFTMAX, SITE_X_FULL);
-            if (KEY && MASK) ok = ok && wait_bounded(bar(C::kMaskFull + st), st_ph, wd, ROLE_SOFTMAX, SITE_MASK_FULL);
+            if (KEY) ok = ok && wait(C::kXFull + J % R0, turn(J, R0), SITE_X_FULL);
+            if (KEY && MASK) ok = ok && wait(C::kMaskFull + st, turn(J, C::kStats), SITE_MASK_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tS = (KEY || !(j & 1)) ? tT0 : tT0b;
-            // P, then dS: 64 values a thread.  A query CTA's thread holds one row (its
-            // statistics in registers) and 64 columns.  A key CTA's statistics go by
+            const uint32_t tS = (KEY || !(J & 1)) ? tT0 : tT0b;
+            // P, then dS: 64 values a thread.  A query item's thread holds one row (its
+            // statistics in registers) and 64 columns.  A key item's statistics go by
             // column: its thread holds four rows, lane / 4 + 8 i, and of every 8
             // columns the pair 2 (lane mod 4), so that it reads a quarter of them --
             // with a row a thread, broadcasting them from shared memory took half
-            // of its bandwidth from the products (1.50 ms of key CTAs against 1.20).
+            // of its bandwidth from the products (1.50 ms of key items against 1.20).
             float p[64];
-            const float2* nl = reinterpret_cast<const float2*>(smem + C::kStatOffset + st * C::kStatBytes) + 32 * g + (lane & 3);
+            const float2* nl = reinterpret_cast<const float2*>(s.smem + C::kStatOffset + st * C::kStatBytes) + 32 * g + (lane & 3);
             {
                 uint32_t s0[32], s1[32];
                 if constexpr (KEY) {
@@ -558,7 +653,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
             for (int c = 0; c < 64; ++c) p[c] = ex2_approx(p[c]);
             if constexpr (MASK) {
                 if constexpr (KEY) {
-                    const uint2* m = reinterpret_cast<const uint2*>(smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 2) + 32 * g + (lane & 3);
+                    const uint2* m = reinterpret_cast<const uint2*>(s.smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 2) + 32 * g + (lane & 3);
                     const int r = lane >> 2;
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
@@ -593,7 +688,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
                 mbar_arrive(bar(C::kP));
             }
             // dS = P o (dP - delta), from the fp32 P
-            ok = wait_bounded(bar(C::kT1Full), ph, wd, ROLE_SOFTMAX, SITE_T1_FULL);
+            ok = wait(C::kT1Full, J & 1, SITE_T1_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -625,78 +720,71 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tm_f0, const CUtenso
             store_bf16(p, KEY ? tT1 : tS);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(bar(C::kDS + (j & 1)));
+            mbar_arrive(bar(C::kDS + (J & 1)));
         }
 
-        // ---------------------------------------------------------------- epilogue
+        // The gradient: key item, warps 0-3 write dV and warps 4-7 dK, all D
+        // channels; query item, each half of the warps half of dQ's channels.  A
+        // thread writes its row, 32 bytes (a sector) at a time.
         if (ok && n_tiles > 0) {
-            ok = wait_bounded(bar(C::kAccFinal), 0, wd, ROLE_SOFTMAX, SITE_ACC_FINAL);
+            ok = wait(C::kAccFinal, I & 1, SITE_ACC_FINAL);
             ok = __all_sync(0xffffffffu, ok);
-            if (ok) tc_fence_after();
         }
-        if (ok) {
-            // Key CTA: warps 0-3 write dV, warps 4-7 dK, all D channels; query CTA:
-            // each half of the warps writes half of dQ's channels.  32-channel
-            // chunks go through this warp's 4 KB of the idle fixed tiles, so that
-            // stores leave as whole 128-byte lines.
+        if (!ok) break;
+        {
+            tc_fence_after();
+            // the item decoded anew: nothing of it is held across the tiles but its number
+            int again = slot;
+            asm volatile("" : "+r"(again));
+            const Item<KEY> it = decode<KEY, MASK>(a, again);
+            const int row0 = it.fixed * kT;
+            const int row = row0 + wq * 32 + lane;
             constexpr int kChunks = KEY ? D / 32 : D / 64;
             const int c0 = KEY ? 0 : g * kChunks;
-            const uint32_t tA = tmem + lane_off + (KEY && g == 0 ? C::kColAcc1 : C::kColAcc0);
-            const bool split = f > 1;
+            const uint32_t tA = s.tmem + lane_off + (KEY && g == 0 ? C::kColAcc1 : C::kColAcc0);
+            const bool split = (KEY ? a.f_kv : a.f_q) > 1;
             const float mult = split ? 1.f : (KEY && g == 0 ? 1.f : a.scale);
-            const int rows_valid = KEY ? a.kv_len : a.Nq;     // rows past it are zeros (key CTA)
-            const int rows_out = KEY ? a.Nkv : a.Nq;
+            const bool zero_row = n_tiles == 0 || row >= (KEY ? a.kv_len : a.Nq);    // (key item: rows past kv_len are zeros)
+            const bool store = split || row < (KEY ? a.Nkv : a.Nq);
+            const dit_strides4_t& so = KEY ? (g == 0 ? a.sdv : a.sdk) : a.sdq;
             void* const out = KEY ? (g == 0 ? a.dv : a.dk) : a.dq;
-            const dit_strides4_t so = KEY ? (g == 0 ? a.sdv : a.sdk) : a.sdq;
-            float* const part = KEY ? a.part_kv + (static_cast<int64_t>(slot) * 2 + g) * kT * D
-                                    : a.part_q + static_cast<int64_t>(slot) * kT * D;
-            float4* stg = reinterpret_cast<float4*>(smem + warp * 4096);
-            const int k4 = lane & 7, r_sub = lane >> 3;
+            const int64_t off = it.b * so.b + static_cast<int64_t>(row) * so.n + it.h * so.h;
+            float* const part = (KEY ? a.part_kv + (it.part_tile * 2 + g) * kT * D : a.part_q + it.part_tile * kT * D) + (row - row0) * D;
 #pragma unroll 1
             for (int cc = c0; cc < c0 + kChunks; ++cc) {
                 uint32_t o[32];
                 if (n_tiles > 0) {
                     tmem_ld32(tA + cc * 32, o);
                     tmem_ld_wait_dep(o);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = zero_row ? 0u : __float_as_uint(__uint_as_float(o[i]) * mult);
+                if (!store) continue;
+                if (!OUT_BF16 || split) {
+                    float* dst = (split ? part : static_cast<float*>(out) + off) + cc * 32;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        const uint32_t v[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
+                        store8(dst + i, v, split || a.wide);
+                    }
                 } else {
+                    uint16_t* dst = static_cast<uint16_t*>(out) + off + cc * 32;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                const bool zero_row = row >= rows_valid;
+                    for (int i = 0; i < 32; i += 16) {
+                        uint32_t v[8];
 #pragma unroll
-                for (int v4 = 0; v4 < 8; ++v4) {
-                    float4 v = make_float4(__uint_as_float(o[4 * v4 + 0]) * mult, __uint_as_float(o[4 * v4 + 1]) * mult,
-                                           __uint_as_float(o[4 * v4 + 2]) * mult, __uint_as_float(o[4 * v4 + 3]) * mult);
-                    if (zero_row) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    stg[lane * 8 + (v4 ^ (lane & 7))] = v;
-                }
-                __syncwarp();
-#pragma unroll
-                for (int it = 0; it < 8; ++it) {
-                    const int r = it * 4 + r_sub;
-                    const float4 v = stg[r * 8 + (k4 ^ (r & 7))];
-                    const int tr = wq * 32 + r;
-                    if (split) {
-                        *reinterpret_cast<float4*>(part + tr * D + cc * 32 + 4 * k4) = v;
-                    } else if (row0 + tr < rows_out) {
-                        const int64_t off = b * so.b + static_cast<int64_t>(row0 + tr) * so.n + h * so.h + cc * 32 + 4 * k4;
-                        if constexpr (OUT_BF16)
-                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + off) =
-                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                        else
-                            *reinterpret_cast<float4*>(static_cast<float*>(out) + off) = v;
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = pack_bf16x2(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
+                        store8(dst + i, v, a.wide);
                     }
                 }
-                __syncwarp();
             }
         }
-    }
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 8) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if (n_tiles > 0) {
+            tc_fence_before();
+            mbar_arrive(bar(C::kAccFree));
+            ++I;
+        }
     }
 }
 
@@ -705,9 +793,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ AttnBwdArgs a) {
-    const int slot = static_cast<int>(blockIdx.x);
-    if (slot < a.n_kv_ctas) bwd_body<D, true, OUT_BF16, MASK>(tm_k, tm_v, tm_q, tm_do, a, slot);
-    else bwd_body<D, false, OUT_BF16, MASK>(tm_q, tm_do, tm_k, tm_v, a, slot - a.n_kv_ctas);
+    using C = Cfg<D, MASK>;
+    extern __shared__ uint8_t smem_raw[];
+    Cta<D, MASK> s;
+    s.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    s.base = smem_u32(s.smem);
+    // Dynamic shared memory starts on a 1,024-byte boundary when a kernel has no
+    // other; the whole grid would give up alike if it ever did not fit.
+    if (s.base + C::kUsedBytes > smem_u32(smem_raw) + C::kSmemBytes) {
+        if (threadIdx.x == 0 && atomicCAS(a.status, 0u, 5u) == 0u) atomicExch(a.status + 3, static_cast<unsigned>(SITE_NO_ROOM));
+        return;
+    }
+    s.bars = s.base + C::kBarOffset;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s.smem + C::kBarOffset + 2 * C::kNumBars * 8);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* const never_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    s.wd = Watchdog{a.status, a.timeout_ns, abort_flag};
+    s.wd_drain = Watchdog{a.status, a.timeout_ns, never_flag};
+    const int warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * C::kNumBars; ++i) {
+            const int k = i % C::kNumBars;
+            const bool all = k == C::kP || k == C::kDS || k == C::kDS + 1 || k == C::kT1Read || k == C::kAccFree;
+            const bool warp_wide = k >= C::kMaskFull && k < C::kMaskFull + C::kStats;
+            mbar_init(s.bars + i * 8, all ? 256 : (warp_wide ? 32 : 1));
+        }
+        *abort_flag = 0;
+        *never_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    s.tmem = *tmem_slot;
+
+    // Each role runs through the key items, then the query items.  Nothing but
+    // its barriers holds one back; a role that gave up leaves the others to.
+    if (warp >= 8) {
+        regs_decrease<kOtherRegs>();
+        if (warp == 8) {
+            const int worked = multiply<D, true, MASK>(s, a, 0);
+            __syncwarp();
+            if (!__any_sync(0xffffffffu, *abort_flag)) multiply<D, false, MASK>(s, a, worked);
+        } else if (warp == 9) {
+            if (lane_id() == 0) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+                tma_prefetch_desc(&tm_do);
+            }
+            produce<D, true, MASK>(s, tm_k, tm_v, tm_q, tm_do, a);
+            __syncwarp();
+            if (!__any_sync(0xffffffffu, *abort_flag)) produce<D, false, MASK>(s, tm_q, tm_do, tm_k, tm_v, a);
+        } else if (MASK && warp == 10) {
+            stage_mask<D, MASK>(s, a);
+        }
+        __syncwarp();
+    } else {
+        regs_increase<kSoftmaxRegs>();
+        soften<D, true, OUT_BF16, MASK>(s, a);
+        __syncwarp();
+        if (!__any_sync(0xffffffffu, *abort_flag)) soften<D, false, OUT_BF16, MASK>(s, a);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(s.tmem, 512);
+    }
 }
 
 // stat[b*H + h][0][i] = -lse * log2(e) (-inf for rows without a key and rows
@@ -802,7 +961,7 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     auto kern = attn_bwd_kernel<D, OUT_BF16, MASK>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, MASK>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.n_kv_ctas + a.n_q_ctas, kThreads, Cfg<D, MASK>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
+    kern<<<a.grid, kThreads, Cfg<D, MASK>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
     return cudaGetLastError();
 }
 

@@ -106,13 +106,15 @@ struct AttnBwdArgs {
     int occ_words, occ_blocks;  // words per 256-row block, blocks per batch entry
     void *dq, *dk, *dv;
     dit_strides4_t sdq, sdk, sdv;
-    // One CTA per piece.  Key items (b, h, 128-key tile) come first, each cut
-    // into f_kv ranges of query tiles; then query items (b, h, 128-row tile),
-    // each cut into f_q ranges of key tiles.  f > 1: pieces write fp32 partials
-    // ([slot][2][128][D] for dv, dk; [slot][128][D] for dq) that a second
-    // kernel sums in slot order.
+    // Key items (b, h, 128-key tile), each cut into f_kv ranges of query tiles,
+    // and query items (b, h, 128-row tile), each cut into f_q ranges of key
+    // tiles, over `grid` CTAs.  f > 1: pieces write fp32 partials
+    // ([tile][piece][2][128][D] for dv, dk; [tile][piece][128][D] for dq) that a
+    // second kernel sums in piece order.
     int f_kv, f_q;
-    int n_kv_ctas, n_q_ctas;
+    int n_kv_items, n_q_items;  // pieces counted
+    int grid;
+    bool wide;                  // gradients may be stored 32 bytes at a time
     float *part_kv, *part_q;
     unsigned int* status;
     unsigned long long timeout_ns;
