@@ -39,13 +39,18 @@
 //   warp 10         stages mask words (key items with a mask)
 // Registers: 168 at launch; softmax 208, the rest 88 (as the forward kernel).
 // TMEM (512 columns): T0 [0,128) T1 [128,256) ACC0 [256,256+D)
-// ACC1 or the second T0 [256+D, ...).
+// ACC1 [256+D,256+2D) (key items), a second T0 [384,512) (query items; D = 64).
 //
-// Order of products.  Key item, per tile j: dV(j) when P(j) is ready, S(j+1),
-// dK(j) when dS(j) is ready, dP(j+1); the softmax warps form P(j+1) while dK(j)
-// and dP(j+1) run and dS(j) while dV(j) and S(j+1) run.  Query item: S(j+1) into
-// the other T0, dP(j+1) once dP(j) is in registers, dQ(j) when dS(j) (written
-// over S(j)) is ready.
+// Order of products.  An issue that finds the tensor pipe busy waits for it, so
+// every wait of the MMA warp on a barrier (some 100 cycles when it is met) is
+// idle time of the pipe, and the loop makes as few as it can.
+//   query items: T0 one tile ahead of T1; once dS(j) is ready (so dP(j) has been
+//     read) dP(j+1), dQ(j), S(j+2): one wait a tile for dS(j) and X(j+2) together.
+//   key items, D = 64: the same with P: dV(j), S(j+2) behind P(j); dK(j), dP(j+1)
+//     behind dS(j).
+//   key items, D = 128 (one T0): dV(j), S(j+1) behind P(j); dK(j), dP(j+1) behind
+//     dS(j).  (P handed over in two halves, so that dV(j) begins with the first,
+//     measured 1.5% on the key items: another wait eats most of it.)
 //
 // Rows without an allowed key have LSE = -inf; they, and the rows past Nq, get
 // P = 0 through a stored -LSE of -inf.  Keys past kv_len are zero-filled by the
@@ -59,6 +64,7 @@
 #include "ptx.cuh"
 #include "train.h"
 
+
 namespace dit {
 namespace {
 
@@ -71,7 +77,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum BwdSite : uint32_t {
     SITE_FIX_FULL = 11, SITE_X_FULL = 12, SITE_X_EMPTY = 13, SITE_T0_FULL = 14, SITE_T1_FULL = 15, SITE_P_READY = 16,
-    SITE_DS_READY = 17, SITE_T1_READ = 18, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21,
+    SITE_DS_READY = 17, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21,
     SITE_NO_ROOM = 22, SITE_FIX_EMPTY = 23, SITE_ACC_FREE = 24
 };
 constexpr uint32_t ROLE_MASK = 4;
@@ -83,29 +89,31 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// 16 lanes x 64 32-bit columns: r[4k + i] is lane t / 4 + 8 (i / 2), column
-// 8k + 2 (t mod 4) + (i mod 2) for thread t of the warp.
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
+// 32 lanes x 32 32-bit columns: r[16 u + 4k + i] is lane 16 u + t / 4 + 8 (i / 2),
+// column 8k + 2 (t mod 4) + (i mod 2) for thread t of the warp.
+__device__ __forceinline__ void tmem_ld_16x256b_x4x2(uint32_t taddr, uint32_t (&r)[32]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[16 * u]), "=r"(r[16 * u + 1]), "=r"(r[16 * u + 2]), "=r"(r[16 * u + 3]), "=r"(r[16 * u + 4]),
+              "=r"(r[16 * u + 5]), "=r"(r[16 * u + 6]), "=r"(r[16 * u + 7]), "=r"(r[16 * u + 8]), "=r"(r[16 * u + 9]),
+              "=r"(r[16 * u + 10]), "=r"(r[16 * u + 11]), "=r"(r[16 * u + 12]), "=r"(r[16 * u + 13]),
+              "=r"(r[16 * u + 14]), "=r"(r[16 * u + 15])
+            : "r"(taddr + (static_cast<uint32_t>(16 * u) << 16)));
 }
-// 16 lanes x 32 32-bit columns: r[2k + i] goes to lane t / 4 + 8 i, column
-// 4k + t mod 4.  Two neighbouring values of the load above, packed, land on the
-// columns of their pair.
-__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+// 32 lanes x 16 32-bit columns: r[8 u + 2k + i] goes to lane 16 u + t / 4 + 8 i,
+// column 4k + t mod 4.  Two neighbouring values of the load above, packed, land
+// on the columns of their pair.
+__device__ __forceinline__ void tmem_st_16x128b_x4x2(uint32_t taddr, const uint32_t (&r)[16]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                         taddr + (static_cast<uint32_t>(16 * u) << 16)),
+                     "r"(r[8 * u]), "r"(r[8 * u + 1]), "r"(r[8 * u + 2]), "r"(r[8 * u + 3]), "r"(r[8 * u + 4]),
+                     "r"(r[8 * u + 5]), "r"(r[8 * u + 6]), "r"(r[8 * u + 7])
+                     : "memory");
 }
 
 // (d0, d1) = (a0*b + c0, a1*b + c1), one packed FMA.
@@ -153,13 +161,13 @@ struct Cfg {
     static constexpr int kX1Empty = kX0Empty + kR0;
     static constexpr int kT0Full = kX1Empty + kR1;       // two (query CTA's two T0)
     static constexpr int kT1Full = kT0Full + 2;
+    // P ready; two by the tile's parity where key items have two T0 (D = 64): with
+    // S issued ahead the softmax warps may finish P(j+1) before the MMA warp has
+    // looked for P(j), and one barrier would be a phase past the one it waits for.
+    // (dS(j+1) needs dP(j+1), issued after the wait for dS(j): one barrier.)
     static constexpr int kP = kT1Full + 1;
-    // Two, by the tile's parity: a query CTA's softmax warps may finish dS(j+1)
-    // before the MMA warp has looked for dS(j), and one barrier would then be a
-    // phase past the one it waits for.  (dS(j+2) needs T1(j+2), issued after that.)
-    static constexpr int kDS = kP + 1;
-    static constexpr int kT1Read = kDS + 2;
-    static constexpr int kAccFinal = kT1Read + 1;
+    static constexpr int kDS = kP + 2;
+    static constexpr int kAccFinal = kDS + 1;
     static constexpr int kAccFree = kAccFinal + 1;       // the accumulators have been read
     static constexpr int kFixEmpty = kAccFree + 1;       // the last T0, T1 of an item are done
     static constexpr int kMaskFull = kFixEmpty + 1;
@@ -174,8 +182,10 @@ struct Cfg {
     static constexpr int kSmemBytes = kUsedBytes + 1024 <= 232448 ? kUsedBytes + 1024 : 232448;
     static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStats == kR0), "shared memory");
     // TMEM columns
-    static constexpr int kColT0 = 0, kColT1 = 128, kColAcc0 = 256, kColAcc1 = 256 + D;
-    static_assert(kColAcc1 + 128 <= 512, "TMEM");
+    static constexpr int kColT0 = 0, kColT1 = 128, kColAcc0 = 256, kColAcc1 = 256 + D, kColT0b = 384;
+    static constexpr bool kKeyDouble = kColAcc1 + D <= kColT0b;     // key items have a second T0
+    // Query items' S(j+2) is issued while X0(j) is still held: three slots.
+    static constexpr bool kAhead = kR0 >= 3;
 };
 
 // One item: its fixed tile, and the streamed tiles [begin, end) of its piece.
@@ -428,11 +438,18 @@ __device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs
     using C = Cfg<D, MASK>;
     constexpr uint32_t kIdescT = idesc_bf16_f32(kT, kT, false);
     constexpr uint32_t kIdescAcc = idesc_bf16_f32(kT, D, true);
-    const uint32_t tT0 = s.tmem + C::kColT0, tT1 = s.tmem + C::kColT1;
-    const uint32_t tT0b = s.tmem + C::kColAcc1;      // query items: the second T0
+    constexpr bool kDouble = !KEY || C::kKeyDouble;              // two T0
+    constexpr bool kTwoAhead = kDouble && C::kAhead;             // S(j+2) issued at tile j
+    const uint32_t tT0 = s.tmem + C::kColT0, tT1 = s.tmem + C::kColT1, tT0b = s.tmem + C::kColT0b;
     const uint32_t tA0 = s.tmem + C::kColAcc0, tA1 = s.tmem + C::kColAcc1;
     const uint32_t bars = s.template bar<KEY>(0);
     auto wait = [&](uint32_t i, uint32_t parity, uint32_t site) { return wait_bounded_warp(bars + 8 * i, parity, s.wd, ROLE_MMA, site); };
+    // two barriers at once: one vote when both are met
+    auto wait2 = [&](uint32_t i, uint32_t pi, uint32_t site_i, uint32_t k, uint32_t pk, uint32_t site_k) {
+        const bool a0 = mbar_try_wait(bars + 8 * i, pi), b0 = mbar_try_wait(bars + 8 * k, pk);
+        if (__all_sync(0xffffffffu, a0 && b0)) return true;
+        return wait(i, pi, site_i) && wait(k, pk, site_k);
+    };
     auto commit = [&](uint32_t i) { umma_commit_warp(bars + 8 * i); };
 
     // Descriptors: K-major operands of T, MN-major ones of ACC; only the start
@@ -459,9 +476,24 @@ __device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs
                                               (accumulate || kk.value > 0) ? 1u : 0u);
         });
     };
-    // The next tile for T0 and T1, and the tile whose P, dS are due.
+    // The next tile of T0, the next of T1 and the tile whose P, dS are due; with
+    // the parity of T0's next tile.
     RingPos<C::kR0, kStep> n0(s.x0(0) >> 4), c0(s.x0(0) >> 4);
     RingPos<C::kR1, kStep> n1(s.x1(0) >> 4), c1(s.x1(0) >> 4);
+    uint32_t odd = 0;
+    auto next_t0 = [&]() {
+        issue_t(kDouble && odd ? tT0b : tT0, f0, n0.addr);
+        commit(C::kT0Full + (kDouble ? odd : 0));
+        if (kDouble) odd ^= 1u;
+        n0.step();
+    };
+    auto next_t1 = [&](bool last) {
+        issue_t(tT1, f1, n1.addr);
+        commit(C::kT1Full);
+        if (!KEY) commit(C::kX1Empty + n1.slot);
+        if (last) commit(C::kFixEmpty);      // the item's last T0 has been issued before
+        n1.step();
+    };
 
     bool ok = true;
     if (!KEY && before > 0)
@@ -471,67 +503,66 @@ __device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs
     for (int slot = first_item<KEY>(a); ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
         const int n = Stream<KEY, MASK>(a, decode<KEY, MASK>(a, slot)).count();
         if (n == 0) continue;
-        // the item's first T0, T1 (the previous item's last products are done with them: in order)
+        // the item's first T0, T1 (the previous item's last products are done with
+        // T0, and its dS(last) was written after dP(last) had been read: in order)
         ok = wait(C::kFixFull, I & 1, SITE_FIX_FULL) && wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
         if (!ok) break;
-        issue_t(!KEY && (J & 1) ? tT0b : tT0, f0, n0.addr);
-        commit(C::kT0Full + (KEY ? 0 : J & 1));
-        if (!KEY && J > 0) {
-            ok = wait(C::kT1Read, (J - 1) & 1, SITE_T1_READ);
+        next_t0();
+        next_t1(n == 1);
+        if (kTwoAhead && n > 1) {
+            ok = wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
             if (!ok) break;
+            next_t0();
         }
-        issue_t(tT1, f1, n1.addr);
-        commit(C::kT1Full);
-        if (!KEY) commit(C::kX1Empty + n1.slot);
-        if (n == 1) commit(C::kFixEmpty);
-        n0.step();
-        n1.step();
         for (int j = 0; j < n; ++j, ++J) {
             const bool more = j + 1 < n;
-            if constexpr (KEY) {
-                ok = wait(C::kP, J & 1, SITE_P_READY) && (j > 0 || I == 0 || wait(C::kAccFree, (I - 1) & 1, SITE_ACC_FREE));
+            const bool t0_due = j + (kTwoAhead ? 2 : 1) < n;     // T0 has a tile to issue at this one
+            const bool first = j == 0 && I > 0;                  // the accumulators must have been read
+            // With four slots X(j+2) has long been on its way and is awaited together
+            // with P or dS; with three it is needed two products later, and awaited
+            // then (together: query items of D = 128 1.31 ms against 0.95).
+            constexpr bool kTogether = kTwoAhead && C::kR0 >= 4;
+            auto x_due = [&]() { return wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL); };
+            if (kDouble && !kTwoAhead && t0_due) {
+                ok = x_due();
                 if (!ok) break;
-                issue_acc(tA1, tT0, c1.addr, j > 0);
+                next_t0();
+            }
+            if constexpr (KEY) {
+                const uint32_t p = C::kP + (kDouble ? (J & 1) : 0), pp = kDouble ? (J >> 1) & 1 : J & 1;
+                ok = kTogether && t0_due ? wait2(p, pp, SITE_P_READY, C::kXFull + n0.slot, n0.parity, SITE_X_FULL)
+                                         : wait(p, pp, SITE_P_READY);
+                if (ok && first) ok = wait(C::kAccFree, (I - 1) & 1, SITE_ACC_FREE);
+                if (!ok) break;
+                issue_acc(tA1, kDouble && (J & 1) ? tT0b : tT0, c1.addr, j > 0);
                 commit(C::kX1Empty + c1.slot);
-                if (more) {
-                    ok = wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
+                if (t0_due) {
+                    if (!kTogether) ok = x_due();
                     if (!ok) break;
-                    issue_t(tT0, f0, n0.addr);
-                    commit(C::kT0Full);
+                    next_t0();
                 }
-                ok = wait(C::kDS + (J & 1), (J >> 1) & 1, SITE_DS_READY);
+                ok = wait(C::kDS, J & 1, SITE_DS_READY);
                 if (!ok) break;
                 issue_acc(tA0, tT1, c0.addr, j > 0);
                 commit(C::kX0Empty + c0.slot);
-                if (more) {
-                    issue_t(tT1, f1, n1.addr);
-                    commit(C::kT1Full);
-                }
+                if (more) next_t1(j + 2 == n);
             } else {
-                if (more) {
-                    ok = wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
-                    if (!ok) break;
-                    issue_t((J & 1) ? tT0 : tT0b, f0, n0.addr);
-                    commit(C::kT0Full + ((J + 1) & 1));
-                    ok = wait(C::kT1Read, J & 1, SITE_T1_READ);
-                    if (!ok) break;
-                    issue_t(tT1, f1, n1.addr);
-                    commit(C::kT1Full);
-                    commit(C::kX1Empty + n1.slot);
-                }
-                ok = wait(C::kDS + (J & 1), (J >> 1) & 1, SITE_DS_READY) &&
-                     (j > 0 || I == 0 || wait(C::kAccFree, (I - 1) & 1, SITE_ACC_FREE));
+                ok = kTogether && t0_due ? wait2(C::kDS, J & 1, SITE_DS_READY, C::kXFull + n0.slot, n0.parity, SITE_X_FULL)
+                                         : wait(C::kDS, J & 1, SITE_DS_READY);
+                if (!ok) break;
+                if (more) next_t1(j + 2 == n);
+                if (first) ok = wait(C::kAccFree, (I - 1) & 1, SITE_ACC_FREE);
                 if (!ok) break;
                 issue_acc(tA0, (J & 1) ? tT0b : tT0, c0.addr, j > 0);
                 commit(C::kX0Empty + c0.slot);
-            }
-            if (more) {
-                n0.step();
-                n1.step();
+                if (kTwoAhead && t0_due) {
+                    if (!kTogether) ok = x_due();
+                    if (!ok) break;
+                    next_t0();
+                }
             }
             c0.step();
             c1.step();
-            if (j + 2 == n) commit(C::kFixEmpty);     // the item's last T0 and T1 have been issued
         }
         if (!ok) break;
         commit(C::kAccFinal);
@@ -565,22 +596,25 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
     const int wq = warp & 3;    // TMEM lane quadrant
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tT0 = s.tmem + lane_off + C::kColT0 + 64 * g;
-    const uint32_t tT0b = s.tmem + lane_off + C::kColAcc1 + 64 * g;
+    const uint32_t tT0b = s.tmem + lane_off + C::kColT0b + 64 * g;
     const uint32_t tT1 = s.tmem + lane_off + C::kColT1 + 64 * g;
+    constexpr bool kDouble = !KEY || C::kKeyDouble;
     const float sl2 = a.scale_log2;
     auto bar = [&](int i) { return s.template bar<KEY>(i); };
     auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded(bar(i), parity, s.wd, ROLE_SOFTMAX, site); };
-    // 64 values -> 32 columns of bf16 pairs at t, in the layout they were read
-    // (key item: the second half of the values are lanes 16-31)
-    auto store_bf16 = [&](const float* v, uint32_t t) {
+    // 32 columns of T (half `hf` of this warp's 64) to 32 registers and, packed to
+    // bf16 pairs, back to 16 columns.  Query item: a row a thread.  Key item: four
+    // rows, lane / 4 + 8 i, and of every 8 columns the pair 2 (lane mod 4).
+    auto load = [&](uint32_t t, int hf, uint32_t (&r)[32]) {
+        if constexpr (KEY) tmem_ld_16x256b_x4x2(t + 32 * hf, r);
+        else tmem_ld32(t + 32 * hf, r);
+    };
+    auto store = [&](uint32_t t, int hf, const float* v) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]);
-            if constexpr (KEY) tmem_st_16x128b_x8(t + (static_cast<uint32_t>(16 * c) << 16), pk);
-            else tmem_st16(t + c * 16, pk);
-        }
+        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        if constexpr (KEY) tmem_st_16x128b_x4x2(t + 16 * hf, pk);
+        else tmem_st16(t + 16 * hf, pk);
     };
     // A query item's row statistics, asked for one item ahead.
     float next_nlse = 0.f, next_ndelta = 0.f;
@@ -612,115 +646,110 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
             const int st = J % C::kStats;
             uint2 mw = make_uint2(~0u, ~0u);
             if (row_masked) mw = __ldg(reinterpret_cast<const uint2*>(mrow + 4 * tile) + g);
-            ok = KEY ? wait(C::kT0Full, J & 1, SITE_T0_FULL) : wait(C::kT0Full + (J & 1), turn(J, 2), SITE_T0_FULL);
+            ok = kDouble ? wait(C::kT0Full + (J & 1), turn(J, 2), SITE_T0_FULL) : wait(C::kT0Full, J & 1, SITE_T0_FULL);
             // the statistics (and mask words) of this stage have landed
             if (KEY) ok = ok && wait(C::kXFull + J % R0, turn(J, R0), SITE_X_FULL);
             if (KEY && MASK) ok = ok && wait(C::kMaskFull + st, turn(J, C::kStats), SITE_MASK_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tS = (KEY || !(J & 1)) ? tT0 : tT0b;
-            // P, then dS: 64 values a thread.  A query item's thread holds one row (its
-            // statistics in registers) and 64 columns.  A key item's statistics go by
-            // column: its thread holds four rows, lane / 4 + 8 i, and of every 8
-            // columns the pair 2 (lane mod 4), so that it reads a quarter of them --
-            // with a row a thread, broadcasting them from shared memory took half
-            // of its bandwidth from the products (1.50 ms of key items against 1.20).
+            const uint32_t tS = (kDouble && (J & 1)) ? tT0b : tT0;
+            // P, then dS: 64 values a thread, half by half, the second half's load
+            // behind the first half's arithmetic.  A query item's statistics are its
+            // row's, in registers.  A key item's go by column: a thread reads those of
+            // a quarter of them -- with a row a thread, broadcasting them from shared
+            // memory took half of its bandwidth from the products (1.50 ms of key
+            // items against 1.20).
             float p[64];
             const float2* nl = reinterpret_cast<const float2*>(s.smem + C::kStatOffset + st * C::kStatBytes) + 32 * g + (lane & 3);
-            {
-                uint32_t s0[32], s1[32];
-                if constexpr (KEY) {
-                    tmem_ld_16x256b_x8(tS, s0);
-                    tmem_ld_16x256b_x8(tS + (16u << 16), s1);
-                } else {
-                    tmem_ld32(tS, s0);
-                    tmem_ld32(tS + 32, s1);
-                }
-                tmem_ld_wait_dep(s0);
-                reg_dep(s1);
+            uint32_t r0[32], r1[32];
+            // x = S scale log2(e) - LSE log2(e) of one half, then its power of two
+            auto power = [&](int hf, const uint32_t (&r)[32]) {
+                float* q = p + 32 * hf;
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float2 n = KEY ? nl[c] : make_float2(nlse, nlse);    // columns 2c .. 2c + 7 of this half
+                for (int c = 0; c < 16; c += 4) {
+                    const float2 n = KEY ? nl[16 * hf + c] : make_float2(nlse, nlse);
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
-                        ffma2(p[c + i], p[c + i + 1], __uint_as_float(s0[c + i]), __uint_as_float(s0[c + i + 1]), sl2, n.x, n.y);
-                        ffma2(p[32 + c + i], p[32 + c + i + 1], __uint_as_float(s1[c + i]), __uint_as_float(s1[c + i + 1]), sl2, n.x, n.y);
+                        ffma2(q[c + i], q[c + i + 1], __uint_as_float(r[c + i]), __uint_as_float(r[c + i + 1]), sl2, n.x, n.y);
+                        ffma2(q[16 + c + i], q[16 + c + i + 1], __uint_as_float(r[16 + c + i]), __uint_as_float(r[16 + c + i + 1]), sl2, n.x, n.y);
                     }
                 }
-            }
 #pragma unroll
-            for (int c = 0; c < 64; ++c) p[c] = ex2_approx(p[c]);
-            if constexpr (MASK) {
-                if constexpr (KEY) {
-                    const uint2* m = reinterpret_cast<const uint2*>(s.smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 2) + 32 * g + (lane & 3);
-                    const int r = lane >> 2;
+                for (int c = 0; c < 32; ++c) q[c] = ex2_approx(q[c]);
+                if constexpr (MASK && KEY) {
+                    const uint2* m = reinterpret_cast<const uint2*>(s.smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 2) + 32 * g + 16 * hf + (lane & 3);
+                    const int row4 = lane >> 2;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
+                    for (int c = 0; c < 16; c += 4) {
                         const uint2 w = m[c];
-                        if (!((w.x >> r) & 1u)) p[c] = 0.f;
-                        if (!((w.y >> r) & 1u)) p[c + 1] = 0.f;
-                        if (!((w.x >> (r + 8)) & 1u)) p[c + 2] = 0.f;
-                        if (!((w.y >> (r + 8)) & 1u)) p[c + 3] = 0.f;
-                        if (!((w.x >> (r + 16)) & 1u)) p[32 + c] = 0.f;
-                        if (!((w.y >> (r + 16)) & 1u)) p[32 + c + 1] = 0.f;
-                        if (!((w.x >> (r + 24)) & 1u)) p[32 + c + 2] = 0.f;
-                        if (!((w.y >> (r + 24)) & 1u)) p[32 + c + 3] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {       // rows lane / 4 + 8 i: values 16 (i / 2) + c + 2 (i mod 2)
+                            const int at = 16 * (i >> 1) + c + 2 * (i & 1);
+                            if (!((w.x >> (row4 + 8 * i)) & 1u)) q[at] = 0.f;
+                            if (!((w.y >> (row4 + 8 * i)) & 1u)) q[at + 1] = 0.f;
+                        }
                     }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (!(((c < 32 ? mw.x : mw.y) >> (c & 31)) & 1u)) p[c] = 0.f;
                 }
-            }
-            if constexpr (!KEY) {
-                const int valid = a.kv_len - tile * kT - 64 * g;   // keys left in this half
-                if (valid < 64) {
+                if constexpr (MASK && !KEY) {
+                    const uint32_t w = hf ? mw.y : mw.x;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c >= valid) p[c] = 0.f;
+                    for (int c = 0; c < 32; ++c)
+                        if (!((w >> c) & 1u)) q[c] = 0.f;
                 }
-            }
+                if constexpr (!KEY) {
+                    const int valid = a.kv_len - tile * kT - 64 * g - 32 * hf;   // keys left in this half
+                    if (valid < 32) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (c >= valid) q[c] = 0.f;
+                    }
+                }
+            };
+            load(tS, 0, r0);
+            tmem_ld_wait_dep(r0);
+            load(tS, 1, r1);
+            power(0, r0);
             if constexpr (KEY) {
-                store_bf16(p, tT0);
+                store(tS, 0, p);
+            }
+            tmem_ld_wait_dep(r1);
+            power(1, r1);
+            if constexpr (KEY) {
+                store(tS, 1, p + 32);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bar(C::kP));
+                mbar_arrive(bar(C::kP + (kDouble ? (J & 1) : 0)));
             }
             // dS = P o (dP - delta), from the fp32 P
             ok = wait(C::kT1Full, J & 1, SITE_T1_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            {
-                uint32_t s0[32], s1[32];
-                if constexpr (KEY) {
-                    tmem_ld_16x256b_x8(tT1, s0);
-                    tmem_ld_16x256b_x8(tT1 + (16u << 16), s1);
-                } else {
-                    tmem_ld32(tT1, s0);
-                    tmem_ld32(tT1 + 32, s1);
-                }
-                tmem_ld_wait_dep(s0);
-                reg_dep(s1);
-                if constexpr (!KEY) {
-                    tc_fence_before();
-                    mbar_arrive(bar(C::kT1Read));
-                }
+            auto differ = [&](int hf, const uint32_t (&r)[32]) {
+                float* q = p + 32 * hf;
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float2 n = KEY ? nl[kT / 2 + c] : make_float2(ndelta, ndelta);
+                for (int c = 0; c < 16; c += 4) {
+                    const float2 n = KEY ? nl[kT / 2 + 16 * hf + c] : make_float2(ndelta, ndelta);
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
-                        fadd2_mul2(p[c + i], p[c + i + 1], __uint_as_float(s0[c + i]), __uint_as_float(s0[c + i + 1]), n.x, n.y, p[c + i], p[c + i + 1]);
-                        fadd2_mul2(p[32 + c + i], p[32 + c + i + 1], __uint_as_float(s1[c + i]), __uint_as_float(s1[c + i + 1]), n.x, n.y, p[32 + c + i], p[32 + c + i + 1]);
+                        fadd2_mul2(q[c + i], q[c + i + 1], __uint_as_float(r[c + i]), __uint_as_float(r[c + i + 1]), n.x, n.y, q[c + i], q[c + i + 1]);
+                        fadd2_mul2(q[16 + c + i], q[16 + c + i + 1], __uint_as_float(r[16 + c + i]), __uint_as_float(r[16 + c + i + 1]), n.x, n.y, q[16 + c + i], q[16 + c + i + 1]);
                     }
                 }
-            }
-            store_bf16(p, KEY ? tT1 : tS);
+            };
+            const uint32_t tD = KEY ? tT1 : tS;
+            load(tT1, 0, r0);
+            tmem_ld_wait_dep(r0);
+            load(tT1, 1, r1);
+            differ(0, r0);
+            store(tD, 0, p);
+            tmem_ld_wait_dep(r1);
+            differ(1, r1);
+            store(tD, 1, p + 32);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(bar(C::kDS + (J & 1)));
+            mbar_arrive(bar(C::kDS));
         }
 
         // The gradient: key item, warps 0-3 write dV and warps 4-7 dK, all D
@@ -745,7 +774,7 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
             const bool split = (KEY ? a.f_kv : a.f_q) > 1;
             const float mult = split ? 1.f : (KEY && g == 0 ? 1.f : a.scale);
             const bool zero_row = n_tiles == 0 || row >= (KEY ? a.kv_len : a.Nq);    // (key item: rows past kv_len are zeros)
-            const bool store = split || row < (KEY ? a.Nkv : a.Nq);
+            const bool inside = split || row < (KEY ? a.Nkv : a.Nq);
             const dit_strides4_t& so = KEY ? (g == 0 ? a.sdv : a.sdk) : a.sdq;
             void* const out = KEY ? (g == 0 ? a.dv : a.dk) : a.dq;
             const int64_t off = it.b * so.b + static_cast<int64_t>(row) * so.n + it.h * so.h;
@@ -759,7 +788,7 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = zero_row ? 0u : __float_as_uint(__uint_as_float(o[i]) * mult);
-                if (!store) continue;
+                if (!inside) continue;
                 if (!OUT_BF16 || split) {
                     float* dst = (split ? part : static_cast<float*>(out) + off) + cc * 32;
 #pragma unroll
@@ -815,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * C::kNumBars; ++i) {
             const int k = i % C::kNumBars;
-            const bool all = k == C::kP || k == C::kDS || k == C::kDS + 1 || k == C::kT1Read || k == C::kAccFree;
+            const bool all = (k >= C::kP && k <= C::kDS) || k == C::kAccFree;
             const bool warp_wide = k >= C::kMaskFull && k < C::kMaskFull + C::kStats;
             mbar_init(s.bars + i * 8, all ? 256 : (warp_wide ? 32 : 1));
         }
