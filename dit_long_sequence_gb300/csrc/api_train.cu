@@ -145,6 +145,13 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     a.f_q = p.f_q;
     a.n_kv_items = static_cast<int>(p.key_items * p.f_kv);
     a.n_q_items = static_cast<int>(p.query_items * p.f_q);
+    auto div = [](int64_t d) { return FastDiv(static_cast<uint32_t>(d > 0 ? d : 1)); };
+    a.div_f_kv = div(p.f_kv);
+    a.div_f_q = div(p.f_q);
+    a.div_kv_tiles = div(p.kv_out_tiles);
+    a.div_q_tiles = div(p.q_tiles);
+    a.div_bh = div(static_cast<int64_t>(B) * H);
+    a.div_h = div(H);
     a.grid = std::min(device_sm_count(dev), a.n_kv_items + a.n_q_items);
     const int64_t wide = grad_dtype == DIT_F32 ? 8 : 16;
     a.wide = (Nq == 0 || (multiple(st->dq, wide) && on(dq, 32))) &&

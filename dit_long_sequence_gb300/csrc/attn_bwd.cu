@@ -212,20 +212,20 @@ __device__ __forceinline__ int item_count(const AttnBwdArgs& a) { return KEY ? a
 template <bool KEY, bool MASK>
 __device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int slot) {
     Item<KEY> it;
-    const int f = KEY ? a.f_kv : a.f_q;
+    const uint32_t f = static_cast<uint32_t>(KEY ? a.f_kv : a.f_q);
     const int tiles = KEY ? a.kv_out_tiles : a.q_tiles;
-    const int piece = slot % f;
-    const int item = slot / f;
-    const int bhs = a.B * a.H;
-    it.fixed = MASK ? item / bhs : item % tiles;
-    const int bh = MASK ? item % bhs : item / tiles;
-    it.h = bh % a.H;
-    it.b = bh / a.H;
+    uint32_t piece, inner, h;
+    const uint32_t item = (KEY ? a.div_f_kv : a.div_f_q).divmod(static_cast<uint32_t>(slot), piece);
+    const uint32_t outer = (MASK ? a.div_bh : (KEY ? a.div_kv_tiles : a.div_q_tiles)).divmod(item, inner);
+    const uint32_t bh = MASK ? inner : outer;
+    it.fixed = static_cast<int>(MASK ? outer : inner);
+    it.b = static_cast<int>(a.div_h.divmod(bh, h));
+    it.h = static_cast<int>(h);
     it.part_tile = (static_cast<int64_t>(bh) * tiles + it.fixed) * f + piece;
     // a key tile wholly past kv_len has nothing to stream: its gradient is zero
-    const int x_tiles = KEY ? (it.fixed < a.kv_tiles ? a.q_tiles : 0) : a.kv_tiles;
-    it.begin = static_cast<int>(static_cast<int64_t>(piece) * x_tiles / f);
-    it.end = static_cast<int>(static_cast<int64_t>(piece + 1) * x_tiles / f);
+    const uint32_t x_tiles = static_cast<uint32_t>(KEY ? (it.fixed < a.kv_tiles ? a.q_tiles : 0) : a.kv_tiles);
+    it.begin = static_cast<int>((KEY ? a.div_f_kv : a.div_f_q).div(piece * x_tiles));
+    it.end = static_cast<int>((KEY ? a.div_f_kv : a.div_f_q).div((piece + 1) * x_tiles));
     return it;
 }
 

@@ -6,9 +6,11 @@
 // valid key ("8 卡怎么分 token", "构造 padding mask": pad query rows see all
 // valid keys), so their blocks are fully occupied.  The attention kernel then
 // loads and multiplies only occupied tiles; for block-local masks most tiles
-// are empty.  Reads the mask once (HBM-bound): one warp per (b, block, 32
-// tiles), lane = tile, each lane reading its tile's four words of every row
-// (a warp's loads cover 512 consecutive bytes of a mask row).
+// are empty.  Reads the mask once (HBM-bound): one block of eight warps per (b,
+// block, 32 tiles), lane = tile, each lane reading its tile's four words of 32
+// rows (a warp's loads cover 512 consecutive bytes of a mask row), eight loads
+// in flight.  One warp walking all 256 rows took 62 us for the 4,000 x 4,000
+// mask of a two-entry batch, where there are 32 units to share among the SMs.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -20,13 +22,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsPerBlock = 256;   // query rows per attention CTA
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 8;
+constexpr int kWarps = kThreads / 32;
 
 __global__ void __launch_bounds__(kThreads) mask_occupancy_kernel(const OccArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t units = static_cast<int64_t>(a.B) * a.row_blocks * a.occ_words;
-    if (unit >= units) return;
+    __shared__ uint32_t words[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = blockIdx.x;
     const int g = static_cast<int>(unit % a.occ_words);
     const int64_t rest = unit / a.occ_words;
     const int rb = static_cast<int>(rest % a.row_blocks);
@@ -41,27 +43,35 @@ __global__ void __launch_bounds__(kThreads) mask_occupancy_kernel(const OccArgs 
         } else {
             const uint4* base = reinterpret_cast<const uint4*>(a.mask + static_cast<int64_t>(b) * a.mask_sb) + t;
             const int64_t row_step = a.mask_si / 4;  // uint4 per row
-            for (int r = r0; r < r1 && !occupied; r += kUnroll) {
+            const int end = min(r1, r0 + (warp + 1) * (kRowsPerBlock / kWarps));
+            for (int r = r0 + warp * (kRowsPerBlock / kWarps); r < end && !occupied; r += kUnroll) {
                 uint4 w[kUnroll];
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u)
-                    w[u] = (r + u < r1) ? __ldcs(base + static_cast<int64_t>(r + u) * row_step) : make_uint4(0u, 0u, 0u, 0u);
+                    w[u] = (r + u < end) ? __ldcs(base + static_cast<int64_t>(r + u) * row_step) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) occupied |= (w[u].x | w[u].y | w[u].z | w[u].w) != 0u;
             }
         }
     }
     const uint32_t word = __ballot_sync(0xffffffffu, occupied);
-    if (lane == 0) a.occ[(static_cast<int64_t>(b) * a.row_blocks + rb) * a.occ_words + g] = word;
+    if (lane == 0) words[warp] = word;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t all = 0u;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all |= words[w];
+        a.occ[(static_cast<int64_t>(b) * a.row_blocks + rb) * a.occ_words + g] = all;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_mask_occupancy(const OccArgs& a, cudaStream_t stream) {
     const int64_t units = static_cast<int64_t>(a.B) * a.row_blocks * a.occ_words;
-    const int64_t blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks <= 0) return cudaSuccess;
-    mask_occupancy_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+    if (units <= 0) return cudaSuccess;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    mask_occupancy_kernel<<<static_cast<unsigned>(units), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -113,6 +113,7 @@ struct AttnBwdArgs {
     // second kernel sums in piece order.
     int f_kv, f_q;
     int n_kv_items, n_q_items;  // pieces counted
+    FastDiv div_f_kv, div_f_q, div_kv_tiles, div_q_tiles, div_bh, div_h;   // item -> piece, tile, head
     int grid;
     bool wide;                  // gradients may be stored 32 bytes at a time
     float *part_kv, *part_q;
