@@ -173,6 +173,7 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
         s.rows_pad = p.q_tiles * 128;
         s.stat = reinterpret_cast<float*>(ws);
         a.stat = s.stat;
+        s.counter = a.counter = reinterpret_cast<unsigned int*>(ws + p.stat_bytes - 256);    // behind the statistics
         a.part_kv = reinterpret_cast<float*>(ws + p.stat_bytes);
         a.part_q = reinterpret_cast<float*>(ws + p.stat_bytes + p.part_kv_bytes);
         if (with_mask) {

@@ -18,11 +18,11 @@
 // 40% more tensor work, against fp32 atomics of 64 KB a tile pair into L2 (or a
 // serial order of CTAs) for one kind of item that also adds into dQ.
 //
-// One CTA per SM takes its share of the key items, then of the query items
-// (starting where the key items left off, so that shares differ by an item at
-// most).  Its roles run on through the items without meeting: while the softmax
-// warps write one item's gradient, the next one's fixed tiles are on their way
-// and its first products run.
+// One CTA per SM takes items from a common counter, the key items first, until
+// none is left (which CTA works on an item changes nothing in its result).  Its
+// roles run on through the items without meeting: while the softmax warps write
+// one item's gradient, the next one's fixed tiles are on their way and its first
+// products run.
 //
 // In both, the streamed tiles come in pairs (X0, X1) = (Q, dO) or (K, V), the
 // fixed ones are (F0, F1) = (K, V) or (Q, dO), and
@@ -78,7 +78,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum BwdSite : uint32_t {
     SITE_FIX_FULL = 11, SITE_X_FULL = 12, SITE_X_EMPTY = 13, SITE_T0_FULL = 14, SITE_T1_FULL = 15, SITE_P_READY = 16,
     SITE_DS_READY = 17, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21,
-    SITE_NO_ROOM = 22, SITE_FIX_EMPTY = 23, SITE_ACC_FREE = 24
+    SITE_NO_ROOM = 22, SITE_FIX_EMPTY = 23, SITE_ACC_FREE = 24,
+    SITE_ITEM = 25
 };
 constexpr uint32_t ROLE_MASK = 4;
 
@@ -176,8 +177,11 @@ struct Cfg {
     static constexpr int kStatOffset = (2 + kR0 + kR1) * kTile;
     static constexpr int kMaskOffset = kStatOffset + kStats * kStatBytes;
     static constexpr int kBarOffset = kMaskOffset + kStats * kMaskBytes;
-    // two sets of barriers: key items', query items'
-    static constexpr int kUsedBytes = kBarOffset + 2 * kNumBars * 8 + 16;
+    // two sets of barriers: key items', query items'; then the item queue's
+    static constexpr int kQueue = 4;                     // items published ahead at most
+    static constexpr int kItemFull = 2 * kNumBars, kItemEmpty = kItemFull + kQueue;
+    static constexpr int kItemOffset = kBarOffset + (kItemEmpty + kQueue) * 8;
+    static constexpr int kUsedBytes = kItemOffset + kQueue * 4 + 16;
     // with room to start on a 1,024-byte boundary where the buffer does not
     static constexpr int kSmemBytes = kUsedBytes + 1024 <= 232448 ? kUsedBytes + 1024 : 232448;
     static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStats == kR0), "shared memory");
@@ -195,23 +199,14 @@ struct Item {
     int64_t part_tile;          // its place among the partials
 };
 
-// The items of this CTA: every gridDim.x-th, the query items beginning behind
-// the CTA that took the last key item.
-template <bool KEY>
-__device__ __forceinline__ int first_item(const AttnBwdArgs& a) {
-    const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-    return KEY ? c : (c + g - a.n_kv_items % g) % g;
-}
-template <bool KEY>
-__device__ __forceinline__ int item_count(const AttnBwdArgs& a) { return KEY ? a.n_kv_items : a.n_q_items; }
-
 // Items count pieces fastest, then tiles, then heads, so that the CTAs at work
 // share a few heads' tiles in L2; with a mask heads before tiles, since masks
 // tend to load some tiles of every head (the first frame's, the first keys')
 // more than others, and those then begin together.
 template <bool KEY, bool MASK>
-__device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int slot) {
+__device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int id) {
     Item<KEY> it;
+    const int slot = KEY ? id : id - a.n_kv_items;
     const uint32_t f = static_cast<uint32_t>(KEY ? a.f_kv : a.f_q);
     const int tiles = KEY ? a.kv_out_tiles : a.q_tiles;
     uint32_t piece, inner, h;
@@ -299,13 +294,50 @@ struct Cta {
     __device__ __forceinline__ uint32_t x0(int j) const { return base + (2 + j % C::kR0) * C::kTile; }
     __device__ __forceinline__ uint32_t x1(int j) const { return base + (2 + C::kR0 + j % C::kR1) * C::kTile; }
 };
+// The items a CTA works on, in order: its producer takes them from the counter
+// and publishes them one ahead; every other role's warps take them from there.
+// Ids from n_kv_items on are query items, n_kv_items + n_q_items is the end.
+struct Queue {
+    uint32_t n = 0;
+};
+template <int D, bool MASK>
+__device__ __forceinline__ bool publish(const Cta<D, MASK>& s, Queue& q, int id) {
+    using C = Cfg<D, MASK>;
+    const uint32_t slot = q.n % C::kQueue;
+    const bool ok = wait_bounded_warp(s.bars + (C::kItemEmpty + slot) * 8, ((q.n / C::kQueue) & 1u) ^ 1u, s.wd, ROLE_LOAD, SITE_ITEM);
+    if (ok && lane_id() == 0) {
+        *reinterpret_cast<volatile int*>(s.smem + C::kItemOffset + slot * 4) = id;
+        mbar_arrive(s.bars + (C::kItemFull + slot) * 8);
+    }
+    ++q.n;
+    return ok;
+}
+template <int D, bool MASK>
+__device__ __forceinline__ int take(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& q, uint32_t role) {
+    using C = Cfg<D, MASK>;
+    const uint32_t slot = q.n % C::kQueue;
+    const bool ok = wait_bounded_warp(s.bars + (C::kItemFull + slot) * 8, (q.n / C::kQueue) & 1u, s.wd, role, SITE_ITEM);
+    const int id = ok ? *reinterpret_cast<volatile int*>(s.smem + C::kItemOffset + slot * 4) : a.n_kv_items + a.n_q_items;
+    __syncwarp();
+    if (ok && lane_id() == 0) mbar_arrive(s.bars + (C::kItemEmpty + slot) * 8);
+    ++q.n;
+    return id;
+}
+// The producer's next item: the first is the CTA's own number.
+__device__ __forceinline__ int next_item(const AttnBwdArgs& a, int last) {
+    if (a.counter == nullptr) return min(last + static_cast<int>(gridDim.x), a.n_kv_items + a.n_q_items);
+    int id = 0;
+    if (lane_id() == 0) id = static_cast<int>(gridDim.x) + static_cast<int>(atomicAdd(a.counter, 1u));
+    return min(__shfl_sync(0xffffffffu, id, 0), a.n_kv_items + a.n_q_items);
+}
 // The parity of use n of a slot of r.
 __device__ __forceinline__ uint32_t turn(int n, int r) { return static_cast<uint32_t>(n / r) & 1u; }
 
 // ------------------------------------------------------------ TMA producer (a warp; lane 0 issues)
 template <int D, bool KEY, bool MASK>
 __device__ __forceinline__ void produce(const Cta<D, MASK>& s, const CUtensorMap& tm_f0, const CUtensorMap& tm_f1,
-                                        const CUtensorMap& tm_x0, const CUtensorMap& tm_x1, const AttnBwdArgs& a) {
+                                        const CUtensorMap& tm_x0, const CUtensorMap& tm_x1, const AttnBwdArgs& a,
+                                        Queue& queue, int& id) {
     using C = Cfg<D, MASK>;
     constexpr int R0 = C::kR0, R1 = C::kR1;
     const bool leader = lane_id() == 0;
@@ -318,19 +350,24 @@ __device__ __forceinline__ void produce(const Cta<D, MASK>& s, const CUtensorMap
     int done = 0;                       // tiles copied
     int half = -1;                      // a tile whose X0 alone was copied
     bool ok = true;
-    for (int slot = first_item<KEY>(a); ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
-        const Item<KEY> it = decode<KEY, MASK>(a, slot);
+    const int last = KEY ? a.n_kv_items : a.n_kv_items + a.n_q_items;
+    for (int next; ok && id < last; id = next) {
+        const Item<KEY> it = decode<KEY, MASK>(a, id);
         Stream<KEY, MASK> stream(a, it);
         const int n = stream.count();
-        if (n == 0) continue;
-        ok = wait(C::kFixEmpty, (I & 1) ^ 1u, SITE_FIX_EMPTY);
-        if (!ok) break;
-        if (leader) {
-            mbar_arrive_expect_tx(bar(C::kFixFull), 2 * C::kTile);
-            copy(&tm_f0, s.f0(), C::kFixFull, it.fixed * kT, it.h, it.b);
-            copy(&tm_f1, s.f1(), C::kFixFull, it.fixed * kT, it.h, it.b);
+        if (n > 0) {
+            ok = wait(C::kFixEmpty, (I & 1) ^ 1u, SITE_FIX_EMPTY);
+            if (!ok) break;
+            if (leader) {
+                mbar_arrive_expect_tx(bar(C::kFixFull), 2 * C::kTile);
+                copy(&tm_f0, s.f0(), C::kFixFull, it.fixed * kT, it.h, it.b);
+                copy(&tm_f1, s.f1(), C::kFixFull, it.fixed * kT, it.h, it.b);
+            }
+            ++I;
         }
-        ++I;
+        next = next_item(a, id);        // (its latency behind the copies)
+        ok = publish(s, queue, next);
+        if (!ok) break;
         const float* const stat = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
         for (int j = 0; j < n; ++j, ++J) {
             const int x_row = stream.next() * kT;
@@ -384,12 +421,13 @@ __device__ __forceinline__ void produce(const Cta<D, MASK>& s, const CUtensorMap
 // Stage j holds word w (keys 32w .. of the fixed tile) of row r at [w][r]; a
 // stage is free again when its X0 slot is (dK of that tile is done).
 template <int D, bool MASK>
-__device__ __forceinline__ void stage_mask(const Cta<D, MASK>& s, const AttnBwdArgs& a) {
+__device__ __forceinline__ void stage_mask(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& queue) {
     using C = Cfg<D, MASK>;
     const int lane = static_cast<int>(lane_id());
     int J = 0;
-    for (int slot = first_item<true>(a); slot < item_count<true>(a); slot += static_cast<int>(gridDim.x)) {
-        const Item<true> it = decode<true, MASK>(a, slot);
+    for (int id = take(s, a, queue, ROLE_MASK); id < a.n_kv_items + a.n_q_items; id = take(s, a, queue, ROLE_MASK)) {
+        if (id >= a.n_kv_items) continue;
+        const Item<true> it = decode<true, MASK>(a, id);
         Stream<true, MASK> stream(a, it);
         for (int tile = stream.next(); tile >= 0; tile = stream.next(), ++J) {
             const int st = J % C::kStats;
@@ -434,7 +472,7 @@ struct RingPos {
 // Returns the items worked on; `before`: the key items this CTA worked on, whose
 // accumulators must have been read before the query items' products overwrite them.
 template <int D, bool KEY, bool MASK>
-__device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs& a, int before) {
+__device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& queue, int& id, int before) {
     using C = Cfg<D, MASK>;
     constexpr uint32_t kIdescT = idesc_bf16_f32(kT, kT, false);
     constexpr uint32_t kIdescAcc = idesc_bf16_f32(kT, D, true);
@@ -500,8 +538,8 @@ __device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs
         ok = wait_bounded_warp(s.template bar<true>(C::kAccFree), (before - 1) & 1, s.wd, ROLE_MMA, SITE_ACC_FREE);
     uint32_t J = 0;
     int I = 0;
-    for (int slot = first_item<KEY>(a); ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
-        const int n = Stream<KEY, MASK>(a, decode<KEY, MASK>(a, slot)).count();
+    for (; ok && id < (KEY ? a.n_kv_items : a.n_kv_items + a.n_q_items); id = take(s, a, queue, ROLE_MMA)) {
+        const int n = Stream<KEY, MASK>(a, decode<KEY, MASK>(a, id)).count();
         if (n == 0) continue;
         // the item's first T0, T1 (the previous item's last products are done with
         // T0, and its dS(last) was written after dP(last) had been read: in order)
@@ -588,7 +626,7 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&v)[8], bool wid
 }
 
 template <int D, bool KEY, bool OUT_BF16, bool MASK>
-__device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs& a) {
+__device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& queue, int& id) {
     using C = Cfg<D, MASK>;
     constexpr int R0 = C::kR0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -618,9 +656,10 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
     };
     // A query item's row statistics, asked for one item ahead.
     float next_nlse = 0.f, next_ndelta = 0.f;
-    auto ask = [&](int slot) {
-        if (KEY || slot >= item_count<KEY>(a) || a.stat == nullptr) return;    // (without keys there are no statistics)
-        const Item<KEY> it = decode<KEY, MASK>(a, slot);
+    const int last = KEY ? a.n_kv_items : a.n_kv_items + a.n_q_items;
+    auto ask = [&](int which) {
+        if (KEY || which >= last || a.stat == nullptr) return;    // (without keys there are no statistics)
+        const Item<KEY> it = decode<KEY, MASK>(a, which);
         const float* p = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT) + it.fixed * kT + wq * 32 + lane;
         next_nlse = __ldg(p);
         next_ndelta = __ldg(p + static_cast<int64_t>(a.q_tiles) * kT);
@@ -628,16 +667,16 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
 
     int J = 0, I = 0;
     bool ok = true;
-    int slot = first_item<KEY>(a);
-    ask(slot);
-    for (; ok && slot < item_count<KEY>(a); slot += static_cast<int>(gridDim.x)) {
-        const Item<KEY> it = decode<KEY, MASK>(a, slot);
+    ask(id);
+    for (int next; ok && id < last; id = next) {
+        next = take(s, a, queue, ROLE_SOFTMAX);
+        const Item<KEY> it = decode<KEY, MASK>(a, id);
         const int row0 = it.fixed * kT;
         const int row = row0 + wq * 32 + lane;      // this thread's row of the fixed tile
         Stream<KEY, MASK> stream(a, it);
         const int n_tiles = stream.count();
         const float nlse = next_nlse, ndelta = next_ndelta;
-        ask(slot + static_cast<int>(gridDim.x));
+        ask(next);
         const bool row_masked = !KEY && MASK && row < a.mask_rows;
         const uint32_t* mrow = row_masked ? a.mask + it.b * a.mask_sb + row * a.mask_si : nullptr;
 
@@ -763,7 +802,7 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
         {
             tc_fence_after();
             // the item decoded anew: nothing of it is held across the tiles but its number
-            int again = slot;
+            int again = id;
             asm volatile("" : "+r"(again));
             const Item<KEY> it = decode<KEY, MASK>(a, again);
             const int row0 = it.fixed * kT;
@@ -834,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     s.bars = s.base + C::kBarOffset;
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s.smem + C::kBarOffset + 2 * C::kNumBars * 8);
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s.smem + C::kItemOffset + C::kQueue * 4);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* const never_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
     s.wd = Watchdog{a.status, a.timeout_ns, abort_flag};
@@ -847,6 +886,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool all = (k >= C::kP && k <= C::kDS) || k == C::kAccFree;
             const bool warp_wide = k >= C::kMaskFull && k < C::kMaskFull + C::kStats;
             mbar_init(s.bars + i * 8, all ? 256 : (warp_wide ? 32 : 1));
+        }
+        for (int i = 0; i < C::kQueue; ++i) {
+            mbar_init(s.bars + (C::kItemFull + i) * 8, 1);
+            mbar_init(s.bars + (C::kItemEmpty + i) * 8, MASK ? 10 : 9);    // the MMA, softmax and mask warps
         }
         *abort_flag = 0;
         *never_flag = 0;
@@ -863,12 +906,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Each role runs through the key items, then the query items.  Nothing but
     // its barriers holds one back; a role that gave up leaves the others to.
+    Queue queue;
     if (warp >= 8) {
         regs_decrease<kOtherRegs>();
         if (warp == 8) {
-            const int worked = multiply<D, true, MASK>(s, a, 0);
+            int id = take(s, a, queue, ROLE_MMA);
+            const int worked = multiply<D, true, MASK>(s, a, queue, id, 0);
             __syncwarp();
-            if (!__any_sync(0xffffffffu, *abort_flag)) multiply<D, false, MASK>(s, a, worked);
+            if (!__any_sync(0xffffffffu, *abort_flag)) multiply<D, false, MASK>(s, a, queue, id, worked);
         } else if (warp == 9) {
             if (lane_id() == 0) {
                 tma_prefetch_desc(&tm_q);
@@ -876,18 +921,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&tm_v);
                 tma_prefetch_desc(&tm_do);
             }
-            produce<D, true, MASK>(s, tm_k, tm_v, tm_q, tm_do, a);
+            int id = static_cast<int>(blockIdx.x);       // (the grid is no larger than the items)
+            publish(s, queue, id);
+            produce<D, true, MASK>(s, tm_k, tm_v, tm_q, tm_do, a, queue, id);
             __syncwarp();
-            if (!__any_sync(0xffffffffu, *abort_flag)) produce<D, false, MASK>(s, tm_q, tm_do, tm_k, tm_v, a);
+            if (!__any_sync(0xffffffffu, *abort_flag)) produce<D, false, MASK>(s, tm_q, tm_do, tm_k, tm_v, a, queue, id);
         } else if (MASK && warp == 10) {
-            stage_mask<D, MASK>(s, a);
+            stage_mask<D, MASK>(s, a, queue);
         }
         __syncwarp();
     } else {
         regs_increase<kSoftmaxRegs>();
-        soften<D, true, OUT_BF16, MASK>(s, a);
+        int id = take(s, a, queue, ROLE_SOFTMAX);
+        soften<D, true, OUT_BF16, MASK>(s, a, queue, id);
         __syncwarp();
-        if (!__any_sync(0xffffffffu, *abort_flag)) soften<D, false, OUT_BF16, MASK>(s, a);
+        if (!__any_sync(0xffffffffu, *abort_flag)) soften<D, false, OUT_BF16, MASK>(s, a, queue, id);
     }
 
     tc_fence_before();
@@ -905,6 +953,7 @@ template <int D, bool OUT_BF16>
 __global__ void __launch_bounds__(256) attn_bwd_stat_kernel(const AttnBwdStatArgs a) {
     constexpr int LPR = D / 8;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (g == 0) *a.counter = 0u;      // of the main kernel's items
     const int64_t unit = g / LPR;
     const int c = static_cast<int>(g % LPR);
     const int64_t bh = unit / a.rows_pad;

@@ -41,7 +41,7 @@ inline BwdPlan plan_attn_bwd(int B, int Nq, int Nkv, int H, int D, int key_valid
         p.f_q = pieces(3.0 * p.kv_tiles, p.kv_tiles);
     }
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
-    p.stat_bytes = up(bh * 2 * p.q_tiles * 128 * 4);
+    p.stat_bytes = up(bh * 2 * p.q_tiles * 128 * 4) + 256;     // and the item counter
     p.part_kv_bytes = p.f_kv > 1 ? up(p.key_items * p.f_kv * 2 * 128 * D * 4) : 0;
     p.part_q_bytes = p.f_q > 1 ? up(p.query_items * p.f_q * 128 * D * 4) : 0;
     return p;

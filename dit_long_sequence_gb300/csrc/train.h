@@ -115,6 +115,7 @@ struct AttnBwdArgs {
     int n_kv_items, n_q_items;  // pieces counted
     FastDiv div_f_kv, div_f_q, div_kv_tiles, div_q_tiles, div_bh, div_h;   // item -> piece, tile, head
     int grid;
+    unsigned int* counter;      // items handed out beyond the first `grid` (nullptr: every grid-th)
     bool wide;                  // gradients may be stored 32 bytes at a time
     float *part_kv, *part_q;
     unsigned int* status;
@@ -128,6 +129,7 @@ struct AttnBwdStatArgs {
     const float *lse, *dlse;
     int B, Nq, H, rows_pad;     // rows_pad = q_tiles * 128
     float* stat;
+    unsigned int* counter;      // set to zero for the main kernel
 };
 
 cudaError_t launch_attn_bwd_stat(const AttnBwdStatArgs& a, int D, bool out_bf16, cudaStream_t s);
