@@ -35,8 +35,8 @@
 //                   tile, one TMEM lane = one row per thread
 //   warp 8          tcgen05.mma issuer (warp-wide, one elected lane issues);
 //                   owns the TMEM allocation
-//   warp 9          TMA producer (one thread)
-//   warp 10         stages mask words (key items with a mask)
+//   warp 9          TMA producer (one lane issues)
+//   warps 10, 11    idle (they complete the third warpgroup)
 // Registers: 168 at launch; softmax 208, the rest 88 (as the forward kernel).
 // TMEM (512 columns): T0 [0,128) T1 [128,256) ACC0 [256,256+D)
 // ACC1 [256+D,256+2D) (key items), a second T0 [384,512) (query items; D = 64).
@@ -77,11 +77,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum BwdSite : uint32_t {
     SITE_FIX_FULL = 11, SITE_X_FULL = 12, SITE_X_EMPTY = 13, SITE_T0_FULL = 14, SITE_T1_FULL = 15, SITE_P_READY = 16,
-    SITE_DS_READY = 17, SITE_ACC_FINAL = 19, SITE_MASK_FULL = 20, SITE_BWD_DRAIN = 21,
+    SITE_DS_READY = 17, SITE_ACC_FINAL = 19, SITE_BWD_DRAIN = 21,
     SITE_NO_ROOM = 22, SITE_FIX_EMPTY = 23, SITE_ACC_FREE = 24,
     SITE_ITEM = 25
 };
-constexpr uint32_t ROLE_MASK = 4;
 
 // Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -141,20 +140,18 @@ __device__ __forceinline__ void fadd2_mul2(float& d0, float& d1, float a0, float
         : "f"(a0), "f"(a1), "f"(c0), "f"(c1), "f"(b0), "f"(b1));
 }
 
-// MASK: a key CTA also stages mask words, which leaves D = 128 one slot less.
-template <int D, bool MASK>
+template <int D>
 struct Cfg {
     static constexpr int kTile = kT * D * 2;
     // Ring slots of X0 and of X1.  X0(j) is held until the last product of tile j,
     // so three of it keep the next copy three products ahead of its use; with
     // two and two, both kinds of CTA ran at 1.6 us a tile pair whatever their
     // products, waiting for copies.
-    static constexpr int kR0 = D == 128 ? (MASK ? 2 : 3) : 4;
+    static constexpr int kR0 = D == 128 ? 3 : 4;
     static constexpr int kR1 = D == 128 ? 2 : 4;
-    static constexpr int kStats = kR1;                   // statistics (and mask words) of this many tiles
+    static constexpr int kStats = kR1;                   // statistics of this many tiles
     static constexpr int kBlock = kT * 128;              // 128 rows x 64 bf16 (one swizzle column)
     static constexpr int kStatBytes = 2 * kT * 4;        // -lse2[128], -delta[128]
-    static constexpr int kMaskBytes = MASK ? kT * 16 : 0;   // 4 words x 128 rows
     // barriers
     static constexpr int kFixFull = 0;
     static constexpr int kXFull = 1;                     // X0 and X1 of a tile (by X0's slot)
@@ -171,12 +168,10 @@ struct Cfg {
     static constexpr int kAccFinal = kDS + 1;
     static constexpr int kAccFree = kAccFinal + 1;       // the accumulators have been read
     static constexpr int kFixEmpty = kAccFree + 1;       // the last T0, T1 of an item are done
-    static constexpr int kMaskFull = kFixEmpty + 1;
-    static constexpr int kDrain = kMaskFull + kStats;
+    static constexpr int kDrain = kFixEmpty + 1;
     static constexpr int kNumBars = kDrain + 1;
     static constexpr int kStatOffset = (2 + kR0 + kR1) * kTile;
-    static constexpr int kMaskOffset = kStatOffset + kStats * kStatBytes;
-    static constexpr int kBarOffset = kMaskOffset + kStats * kMaskBytes;
+    static constexpr int kBarOffset = kStatOffset + kStats * kStatBytes;
     // two sets of barriers: key items', query items'; then the item queue's
     static constexpr int kQueue = 4;                     // items published ahead at most
     static constexpr int kItemFull = 2 * kNumBars, kItemEmpty = kItemFull + kQueue;
@@ -184,12 +179,12 @@ struct Cfg {
     static constexpr int kUsedBytes = kItemOffset + kQueue * 4 + 16;
     // with room to start on a 1,024-byte boundary where the buffer does not
     static constexpr int kSmemBytes = kUsedBytes + 1024 <= 232448 ? kUsedBytes + 1024 : 232448;
-    static_assert(kUsedBytes <= kSmemBytes && (!MASK || kStats == kR0), "shared memory");
+    static_assert(kUsedBytes <= kSmemBytes, "shared memory");
     // TMEM columns
     static constexpr int kColT0 = 0, kColT1 = 128, kColAcc0 = 256, kColAcc1 = 256 + D, kColT0b = 384;
     static constexpr bool kKeyDouble = kColAcc1 + D <= kColT0b;     // key items have a second T0
-    // Query items' S(j+2) is issued while X0(j) is still held: three slots.
-    static constexpr bool kAhead = kR0 >= 3;
+    // with two T0, S(j+2) is issued while X0(j) is still held: three slots
+    static_assert(kR0 >= 3, "ring");
 };
 
 // One item: its fixed tile, and the streamed tiles [begin, end) of its piece.
@@ -281,9 +276,9 @@ struct Stream {
 };
 
 // What the roles of a CTA share.
-template <int D, bool MASK>
+template <int D>
 struct Cta {
-    using C = Cfg<D, MASK>;
+    using C = Cfg<D>;
     uint8_t* smem;
     uint32_t base, bars, tmem;
     Watchdog wd, wd_drain;      // wd_drain ignores the abort flag: it waits for work already in flight
@@ -300,9 +295,9 @@ struct Cta {
 struct Queue {
     uint32_t n = 0;
 };
-template <int D, bool MASK>
-__device__ __forceinline__ bool publish(const Cta<D, MASK>& s, Queue& q, int id) {
-    using C = Cfg<D, MASK>;
+template <int D>
+__device__ __forceinline__ bool publish(const Cta<D>& s, Queue& q, int id) {
+    using C = Cfg<D>;
     const uint32_t slot = q.n % C::kQueue;
     const bool ok = wait_bounded_warp(s.bars + (C::kItemEmpty + slot) * 8, ((q.n / C::kQueue) & 1u) ^ 1u, s.wd, ROLE_LOAD, SITE_ITEM);
     if (ok && lane_id() == 0) {
@@ -312,9 +307,9 @@ __device__ __forceinline__ bool publish(const Cta<D, MASK>& s, Queue& q, int id)
     ++q.n;
     return ok;
 }
-template <int D, bool MASK>
-__device__ __forceinline__ int take(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& q, uint32_t role) {
-    using C = Cfg<D, MASK>;
+template <int D>
+__device__ __forceinline__ int take(const Cta<D>& s, const AttnBwdArgs& a, Queue& q, uint32_t role) {
+    using C = Cfg<D>;
     const uint32_t slot = q.n % C::kQueue;
     const bool ok = wait_bounded_warp(s.bars + (C::kItemFull + slot) * 8, (q.n / C::kQueue) & 1u, s.wd, role, SITE_ITEM);
     const int id = ok ? *reinterpret_cast<volatile int*>(s.smem + C::kItemOffset + slot * 4) : a.n_kv_items + a.n_q_items;
@@ -335,10 +330,10 @@ __device__ __forceinline__ uint32_t turn(int n, int r) { return static_cast<uint
 
 // ------------------------------------------------------------ TMA producer (a warp; lane 0 issues)
 template <int D, bool KEY, bool MASK>
-__device__ __forceinline__ void produce(const Cta<D, MASK>& s, const CUtensorMap& tm_f0, const CUtensorMap& tm_f1,
+__device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f0, const CUtensorMap& tm_f1,
                                         const CUtensorMap& tm_x0, const CUtensorMap& tm_x1, const AttnBwdArgs& a,
                                         Queue& queue, int& id) {
-    using C = Cfg<D, MASK>;
+    using C = Cfg<D>;
     constexpr int R0 = C::kR0, R1 = C::kR1;
     const bool leader = lane_id() == 0;
     auto bar = [&](int i) { return s.template bar<KEY>(i); };
@@ -417,38 +412,6 @@ __device__ __forceinline__ void produce(const Cta<D, MASK>& s, const CUtensorMap
     }
 }
 
-// ------------------------------------------- mask words of the streamed query rows (key items; a warp)
-// Stage j holds word w (keys 32w .. of the fixed tile) of row r at [w][r]; a
-// stage is free again when its X0 slot is (dK of that tile is done).
-template <int D, bool MASK>
-__device__ __forceinline__ void stage_mask(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& queue) {
-    using C = Cfg<D, MASK>;
-    const int lane = static_cast<int>(lane_id());
-    int J = 0;
-    for (int id = take(s, a, queue, ROLE_MASK); id < a.n_kv_items + a.n_q_items; id = take(s, a, queue, ROLE_MASK)) {
-        if (id >= a.n_kv_items) continue;
-        const Item<true> it = decode<true, MASK>(a, id);
-        Stream<true, MASK> stream(a, it);
-        for (int tile = stream.next(); tile >= 0; tile = stream.next(), ++J) {
-            const int st = J % C::kStats;
-            if (!wait_bounded_warp(s.template bar<true>(C::kX0Empty + st), turn(J, C::kStats) ^ 1u, s.wd, ROLE_MASK, SITE_X_EMPTY)) return;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(s.smem + C::kMaskOffset + st * C::kMaskBytes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i * 32 + lane, row = tile * kT + r;
-                uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
-                if (row < a.mask_rows)
-                    w = __ldg(reinterpret_cast<const uint4*>(a.mask + it.b * a.mask_sb + row * a.mask_si) + it.fixed);
-                dst[r] = w.x;
-                dst[kT + r] = w.y;
-                dst[2 * kT + r] = w.z;
-                dst[3 * kT + r] = w.w;
-            }
-            mbar_arrive(s.template bar<true>(C::kMaskFull + st));
-        }
-    }
-}
-
 // ------------------------------------------------------------ MMA issuer (a warp)
 // A position in a ring: slot, the parity of its use, and the low word of its
 // tile's matrix descriptor (the start address field).  Stepped, not computed from
@@ -472,12 +435,11 @@ struct RingPos {
 // Returns the items worked on; `before`: the key items this CTA worked on, whose
 // accumulators must have been read before the query items' products overwrite them.
 template <int D, bool KEY, bool MASK>
-__device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& queue, int& id, int before) {
-    using C = Cfg<D, MASK>;
+__device__ __forceinline__ int multiply(const Cta<D>& s, const AttnBwdArgs& a, Queue& queue, int& id, int before) {
+    using C = Cfg<D>;
     constexpr uint32_t kIdescT = idesc_bf16_f32(kT, kT, false);
     constexpr uint32_t kIdescAcc = idesc_bf16_f32(kT, D, true);
-    constexpr bool kDouble = !KEY || C::kKeyDouble;              // two T0
-    constexpr bool kTwoAhead = kDouble && C::kAhead;             // S(j+2) issued at tile j
+    constexpr bool kDouble = !KEY || C::kKeyDouble;              // two T0: S(j+2) issued at tile j
     const uint32_t tT0 = s.tmem + C::kColT0, tT1 = s.tmem + C::kColT1, tT0b = s.tmem + C::kColT0b;
     const uint32_t tA0 = s.tmem + C::kColAcc0, tA1 = s.tmem + C::kColAcc1;
     const uint32_t bars = s.template bar<KEY>(0);
@@ -547,25 +509,20 @@ __device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs
         if (!ok) break;
         next_t0();
         next_t1(n == 1);
-        if (kTwoAhead && n > 1) {
+        if (kDouble && n > 1) {
             ok = wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL);
             if (!ok) break;
             next_t0();
         }
         for (int j = 0; j < n; ++j, ++J) {
             const bool more = j + 1 < n;
-            const bool t0_due = j + (kTwoAhead ? 2 : 1) < n;     // T0 has a tile to issue at this one
+            const bool t0_due = j + (kDouble ? 2 : 1) < n;     // T0 has a tile to issue at this one
             const bool first = j == 0 && I > 0;                  // the accumulators must have been read
             // With four slots X(j+2) has long been on its way and is awaited together
             // with P or dS; with three it is needed two products later, and awaited
             // then (together: query items of D = 128 1.31 ms against 0.95).
-            constexpr bool kTogether = kTwoAhead && C::kR0 >= 4;
+            constexpr bool kTogether = kDouble && C::kR0 >= 4;
             auto x_due = [&]() { return wait(C::kXFull + n0.slot, n0.parity, SITE_X_FULL); };
-            if (kDouble && !kTwoAhead && t0_due) {
-                ok = x_due();
-                if (!ok) break;
-                next_t0();
-            }
             if constexpr (KEY) {
                 const uint32_t p = C::kP + (kDouble ? (J & 1) : 0), pp = kDouble ? (J >> 1) & 1 : J & 1;
                 ok = kTogether && t0_due ? wait2(p, pp, SITE_P_READY, C::kXFull + n0.slot, n0.parity, SITE_X_FULL)
@@ -593,7 +550,7 @@ __device__ __forceinline__ int multiply(const Cta<D, MASK>& s, const AttnBwdArgs
                 if (!ok) break;
                 issue_acc(tA0, (J & 1) ? tT0b : tT0, c0.addr, j > 0);
                 commit(C::kX0Empty + c0.slot);
-                if (kTwoAhead && t0_due) {
+                if (kDouble && t0_due) {
                     if (!kTogether) ok = x_due();
                     if (!ok) break;
                     next_t0();
@@ -626,8 +583,8 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&v)[8], bool wid
 }
 
 template <int D, bool KEY, bool OUT_BF16, bool MASK>
-__device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs& a, Queue& queue, int& id) {
-    using C = Cfg<D, MASK>;
+__device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Queue& queue, int& id) {
+    using C = Cfg<D>;
     constexpr int R0 = C::kR0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = warp >> 2;    // column half
@@ -677,18 +634,37 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
         const int n_tiles = stream.count();
         const float nlse = next_nlse, ndelta = next_ndelta;
         ask(next);
-        const bool row_masked = !KEY && MASK && row < a.mask_rows;
-        const uint32_t* mrow = row_masked ? a.mask + it.b * a.mask_sb + row * a.mask_si : nullptr;
+        // Mask words, asked for one tile ahead.  Query item: this row's two words of
+        // the tile's half.  Key item: the word of this warp's 32 keys in query rows
+        // `lane` and 32 + `lane` of the half; the others' come by shuffles.
+        const uint32_t* const words = MASK ? a.mask + it.b * a.mask_sb : nullptr;
+        auto word_of = [&](int tile) {
+            uint2 w = make_uint2(~0u, ~0u);
+            if constexpr (MASK) {
+                if (tile < 0) return w;
+                if constexpr (KEY) {
+                    const int i = tile * kT + 64 * g + lane;
+                    const uint32_t* p = words + i * a.mask_si + 4 * it.fixed + wq;
+                    if (i < a.mask_rows) w.x = __ldg(p);
+                    if (i + 32 < a.mask_rows) w.y = __ldg(p + 32 * a.mask_si);
+                } else {
+                    if (row < a.mask_rows) w = __ldg(reinterpret_cast<const uint2*>(words + row * a.mask_si + 4 * tile) + g);
+                }
+            }
+            return w;
+        };
+        int tile_next = stream.next();
+        uint2 mw_next = word_of(tile_next);
 
         for (int j = 0; j < n_tiles; ++j, ++J) {
-            const int tile = stream.next();
+            const int tile = tile_next;
             const int st = J % C::kStats;
-            uint2 mw = make_uint2(~0u, ~0u);
-            if (row_masked) mw = __ldg(reinterpret_cast<const uint2*>(mrow + 4 * tile) + g);
+            const uint2 mw = mw_next;
+            tile_next = stream.next();
+            mw_next = word_of(tile_next);
             ok = kDouble ? wait(C::kT0Full + (J & 1), turn(J, 2), SITE_T0_FULL) : wait(C::kT0Full, J & 1, SITE_T0_FULL);
-            // the statistics (and mask words) of this stage have landed
+            // the statistics of this stage have landed
             if (KEY) ok = ok && wait(C::kXFull + J % R0, turn(J, R0), SITE_X_FULL);
-            if (KEY && MASK) ok = ok && wait(C::kMaskFull + st, turn(J, C::kStats), SITE_MASK_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -717,16 +693,16 @@ __device__ __forceinline__ void soften(const Cta<D, MASK>& s, const AttnBwdArgs&
 #pragma unroll
                 for (int c = 0; c < 32; ++c) q[c] = ex2_approx(q[c]);
                 if constexpr (MASK && KEY) {
-                    const uint2* m = reinterpret_cast<const uint2*>(s.smem + C::kMaskOffset + st * C::kMaskBytes) + wq * (kT / 2) + 32 * g + 16 * hf + (lane & 3);
-                    const int row4 = lane >> 2;
+                    const uint32_t held = hf ? mw.y : mw.x;
+                    const int row4 = lane >> 2, col = 2 * (lane & 3);
 #pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        const uint2 w = m[c];
+                    for (int c = 0; c < 16; c += 4) {       // columns 2c + col, 2c + col + 1
+                        const uint32_t w0 = __shfl_sync(0xffffffffu, held, 2 * c + col), w1 = __shfl_sync(0xffffffffu, held, 2 * c + col + 1);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {       // rows lane / 4 + 8 i: values 16 (i / 2) + c + 2 (i mod 2)
                             const int at = 16 * (i >> 1) + c + 2 * (i & 1);
-                            if (!((w.x >> (row4 + 8 * i)) & 1u)) q[at] = 0.f;
-                            if (!((w.y >> (row4 + 8 * i)) & 1u)) q[at + 1] = 0.f;
+                            if (!((w0 >> (row4 + 8 * i)) & 1u)) q[at] = 0.f;
+                            if (!((w1 >> (row4 + 8 * i)) & 1u)) q[at + 1] = 0.f;
                         }
                     }
                 }
@@ -861,9 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ AttnBwdArgs a) {
-    using C = Cfg<D, MASK>;
+    using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
-    Cta<D, MASK> s;
+    Cta<D> s;
     s.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     s.base = smem_u32(s.smem);
     // Dynamic shared memory starts on a 1,024-byte boundary when a kernel has no
@@ -884,12 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2 * C::kNumBars; ++i) {
             const int k = i % C::kNumBars;
             const bool all = (k >= C::kP && k <= C::kDS) || k == C::kAccFree;
-            const bool warp_wide = k >= C::kMaskFull && k < C::kMaskFull + C::kStats;
-            mbar_init(s.bars + i * 8, all ? 256 : (warp_wide ? 32 : 1));
+            mbar_init(s.bars + i * 8, all ? 256 : 1);
         }
         for (int i = 0; i < C::kQueue; ++i) {
             mbar_init(s.bars + (C::kItemFull + i) * 8, 1);
-            mbar_init(s.bars + (C::kItemEmpty + i) * 8, MASK ? 10 : 9);    // the MMA, softmax and mask warps
+            mbar_init(s.bars + (C::kItemEmpty + i) * 8, 9);    // the MMA and softmax warps
         }
         *abort_flag = 0;
         *never_flag = 0;
@@ -926,8 +901,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             produce<D, true, MASK>(s, tm_k, tm_v, tm_q, tm_do, a, queue, id);
             __syncwarp();
             if (!__any_sync(0xffffffffu, *abort_flag)) produce<D, false, MASK>(s, tm_q, tm_do, tm_k, tm_v, a, queue, id);
-        } else if (MASK && warp == 10) {
-            stage_mask<D, MASK>(s, a, queue);
         }
         __syncwarp();
     } else {
@@ -1037,9 +1010,9 @@ template <int D, bool OUT_BF16, bool MASK>
 cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                         const AttnBwdArgs& a, cudaStream_t s) {
     auto kern = attn_bwd_kernel<D, OUT_BF16, MASK>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, MASK>::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.grid, kThreads, Cfg<D, MASK>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
+    kern<<<a.grid, kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
     return cudaGetLastError();
 }
 
