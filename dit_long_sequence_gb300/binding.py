@@ -1,6 +1,7 @@
 """ctypes binding of libditattn.so (include/dit_attn.h).
 
-Argument marshalling only: tensors are passed as device pointers with their
+Argument marshalling only (for the training operators, whose small calls would
+be mostly marshalling, in the CPython extension csrc/py_calls.cpp): tensors are passed as device pointers with their
 element strides and the current CUDA stream; every step of the computation
 runs in the library's kernels.  PyTorch supplies device memory and streams.
 There is no fallback: if the library is missing or a call fails, an exception
@@ -14,10 +15,13 @@ gives a handle to it beside the product library.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
+from .build import CALLS as _CALLS_PATH
 from .build import DEBUG_LIB as _DEBUG_LIB_PATH
 from .build import LIB as _PRODUCT_LIB_PATH
 
@@ -48,8 +52,8 @@ class AttnBwdStrides(ctypes.Structure):
     _fields_ = [(n, Strides4) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
 
 
-_BwdStrideWords = ctypes.c_int64 * (ctypes.sizeof(AttnBwdStrides) // 8)
 DIT_ROPE_INTERLEAVED, DIT_ROPE_HALF = 0, 1
+_ROPE_LAYOUTS = {"interleaved": DIT_ROPE_INTERLEAVED, "half": DIT_ROPE_HALF}
 _ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 _vp, _i, _i64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
@@ -130,6 +134,23 @@ def _declare(lib):
 _lib = _declare(ctypes.CDLL(_LIB_PATH))
 
 
+def _load_calls():
+    """The extension of csrc/py_calls.cpp, calling this library's functions."""
+    if not os.path.exists(_CALLS_PATH):
+        raise ImportError(f"dit_calls.so not found at {_CALLS_PATH}; build it first with "
+                          "`python -m dit_long_sequence_gb300.build` (or __graft_entry__.build())")
+    loader = importlib.machinery.ExtensionFileLoader("dit_calls", _CALLS_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dit_calls", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+        "dit_attn_bwd", "dit_attn_bwd_masked", "dit_attn_bwd_workspace_bytes", "dit_layer_norm_fwd",
+        "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope")))
+    return module
+
+
+_calls = _load_calls()
+
+
 def load_debug_library():
     """ctypes handle of libditattn_debug.so with the C ABI declared: every
     dit_attn.h entry point plus dit_debug_configure / dit_debug_build.  Its
@@ -170,9 +191,6 @@ def _stream_ptr(stream) -> int:
     if stream is None:   # the current device's current stream, without a Stream object
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
-
-
-_DTYPES = {torch.bfloat16: DIT_BF16, torch.float32: DIT_F32}
 
 
 def _strides4(t: torch.Tensor) -> Strides4:
@@ -550,49 +568,12 @@ def attn_bwd_workspace_bytes(B: int, Nq: int, Nkv: int, H: int, D: int, key_vali
                                                  1 if masked else 0))
 
 
-def _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, dv, grad_dtype, workspace, masked):
-    B, Nq, H, D = q.shape
-    Nkv = k.shape[1]
-    for name, t in (("q", q), ("k", k), ("v", v), ("dout", dout)):
-        if t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if k.shape != (B, Nkv, H, D) or v.shape != (B, Nkv, H, D) or dout.shape != q.shape:
-        raise ValueError("k and v must be [B, Nkv, H, D] matching q, dout [B, Nq, H, D]")
-    if out.dtype not in (torch.float32, torch.bfloat16) or out.shape != q.shape:
-        raise ValueError("out must be a [B, Nq, H, D] fp32 or bf16 tensor")
-    for name, t in (("lse", lse), ("dlse", dlse)):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, H, Nq) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous fp32 [B, H, Nq] tensor")
-    if grad_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("gradients are fp32 or bf16")
-    kvl = Nkv if key_valid_len is None else int(key_valid_len)
-    sc = float(D) ** -0.5 if scale is None else float(scale)
-    gt = next((g.dtype for g in (dq, dk, dv) if g is not None), grad_dtype)
-    device = q.device
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=gt, device=device)
-    elif dq.dtype != gt or gt not in _DTYPES or dq.shape != q.shape:
-        raise ValueError("dq must be a [B, Nq, H, D] tensor, dq, dk and dv of one type (fp32 or bf16)")
-    grads_kv = []
-    for name, t in (("dk", dk), ("dv", dv)):
-        if t is None:
-            t = torch.empty(k.shape, dtype=gt, device=device)
-        elif t.dtype != gt or gt not in _DTYPES or t.shape != k.shape:
-            raise ValueError(f"{name} must be a [B, Nkv, H, D] tensor, dq, dk and dv of one type (fp32 or bf16)")
-        grads_kv.append(t)
-    dk, dv = grads_kv
-    if workspace is None:
-        nbytes = attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, kvl, masked)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    st = _BwdStrideWords(*q.stride(), *k.stride(), *v.stride(), *out.stride(), *dout.stride(), *dq.stride(), *dk.stride(),
-                         *dv.stride())       # AttnBwdStrides, filled in one go
-    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), DIT_F32 if out.dtype == torch.float32 else DIT_BF16,
-            lse.data_ptr(), dout.data_ptr(), None if dlse is None else dlse.data_ptr(), ctypes.byref(st), B, Nq, Nkv, H, D,
-            kvl)
-    tail = (sc, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), DIT_F32 if gt == torch.float32 else DIT_BF16,
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
-    return head, tail, (dq, dk, dv), workspace
+def _is_fp32(dtype: torch.dtype) -> bool:
+    if dtype is torch.float32:
+        return True
+    if dtype is torch.bfloat16:
+        return False
+    raise ValueError("results are fp32 or bf16")
 
 
 def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
@@ -608,10 +589,11 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     that of lse.  dq [B, Nq, H, D], dk and dv [B, Nkv, H, D] may be given (e.g.
     views of one fused [B, N, 3, H, D] gradient) or are allocated in grad_dtype;
     keys past key_valid_len get zeros.  Returns (dq, dk, dv)."""
-    head, tail, grads, workspace = _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, dv,
-                                                  grad_dtype, workspace, False)
-    _check(_lib.dit_attn_bwd(*head, *tail, _stream_ptr(stream)), "dit_attn_bwd")
-    return grads
+    rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv,
+                                 _is_fp32(grad_dtype), workspace, _stream_ptr(stream))
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_attn_bwd")
+    return tuple(grads)
 
 
 def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
@@ -621,44 +603,13 @@ def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
                     grad_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None, stream=None):
     """Gradients of attn_fwd_masked through `dit_attn_bwd_masked`: attn_bwd with
     the forward call's mask_bits and mask_rows."""
-    if mask_bits.dtype != torch.int32 or mask_bits.dim() != 3 or mask_bits.stride(2) != 1 or not mask_bits.is_cuda:
-        raise ValueError("mask_bits must be an int32 CUDA tensor [B or 1, rows, words], words contiguous")
-    if mask_bits.shape[0] not in (1, q.shape[0]):
-        raise ValueError("mask_bits must have B or 1 batch entries")
-    rows = mask_bits.shape[1] if mask_rows is None else int(mask_rows)
-    if rows > mask_bits.shape[1]:
-        raise ValueError("mask_rows exceeds the mask's rows")
-    head, tail, grads, workspace = _attn_bwd_args(q, k, v, out, lse, dout, dlse, key_valid_len, scale, dq, dk, dv,
-                                                  grad_dtype, workspace, True)
-    if 4 * ((head[-1] + 127) // 128) > mask_bits.shape[2]:
-        raise ValueError("mask_bits must have 4 * ceil(key_valid_len / 128) words a row")
-    sb = 0 if mask_bits.shape[0] == 1 else mask_bits.stride(0)
-    _check(_lib.dit_attn_bwd_masked(*head, mask_bits.data_ptr(), sb, mask_bits.stride(1), rows, *tail,
-                                    _stream_ptr(stream)), "dit_attn_bwd_masked")
-    return grads
-
-
-def _rows4(t: torch.Tensor) -> torch.Tensor:
-    """[B, N, C] seen as [B, N, 1, C]; [B, N, H, C] as it is."""
-    if t.dim() == 3:
-        return t.unsqueeze(2)
-    if t.dim() != 4:
-        raise ValueError("expected a [B, N, C] or [B, N, H, C] tensor")
-    return t
-
-
-def _norm_params(B, C, params):
-    """param_batches of weight / bias tensors ([C] or [B, C]), all of one shape."""
-    shape = None
-    for name, p in params:
-        if p is None:
-            continue
-        if p.dtype != torch.float32 or not p.is_contiguous() or tuple(p.shape) not in ((C,), (B, C)):
-            raise ValueError(f"{name} must be a contiguous fp32 [C] or [B, C] tensor")
-        if shape is not None and tuple(p.shape) != shape:
-            raise ValueError("weight and bias must have one shape")
-        shape = tuple(p.shape)
-    return B if shape is not None and len(shape) == 2 else 1
+    if mask_bits is None:
+        raise ValueError("mask_bits is missing")
+    rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
+                                 _is_fp32(grad_dtype), workspace, _stream_ptr(stream))
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_attn_bwd_masked")
+    return tuple(grads)
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
@@ -672,27 +623,11 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     (modulation).  Returns (y, mean, rstd): y in out_dtype (default x's; fp32 x
     may give bf16 y), mean (None without center) and rstd fp32 without the
     channel dimension."""
-    x4 = _rows4(x)
-    B, N, H, C = x4.shape
-    if x.dtype not in _DTYPES or not x.is_cuda:
-        raise TypeError("x must be a bf16 or fp32 CUDA tensor")
-    groups = _norm_params(B, C, (("weight", weight), ("bias", bias)))
-    device = x.device
-    if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=device)
-    if out.dtype not in _DTYPES or out.shape != x.shape:
-        raise ValueError("out must have x's shape, bf16 or fp32")
-    o4 = _rows4(out)
-    rows = x.shape[:-1]
-    rstd = torch.empty(rows, dtype=torch.float32, device=device)
-    mean = torch.empty(rows, dtype=torch.float32, device=device) if center else None
-    rc = _lib.dit_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x4)), B, N, H, C,
-                                 None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
-                                 groups, float(eps), 1 if center else 0, out.data_ptr(), _DTYPES[out.dtype],
-                                 ctypes.byref(_strides4(o4)), None if mean is None else mean.data_ptr(), rstd.data_ptr(),
-                                 _stream_ptr(stream))
-    _check(rc, "dit_layer_norm_fwd")
-    return out, mean, rstd
+    rc, y, mean, rstd = _calls.norm_fwd(x, weight, bias, eps, center, out,
+                                        None if out_dtype is None else _is_fp32(out_dtype), _stream_ptr(stream))
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_layer_norm_fwd")
+    return y, mean, rstd
 
 
 def layer_norm_bwd_workspace_bytes(B: int, N: int, H: int, C: int, param_batches: int = 1) -> int:
@@ -710,38 +645,11 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor | None,
     in the forward call.  Returns (dx, dweight, dbias): dx in x's type; dweight
     and dbias fp32 in weight's shape, None without a weight (dbias also without
     has_bias) unless a tensor to fill is given."""
-    x4, d4 = _rows4(x), _rows4(dy)
-    B, N, H, C = x4.shape
-    if x.dtype not in _DTYPES or dy.dtype not in _DTYPES or not x.is_cuda or not dy.is_cuda:
-        raise TypeError("x and dy must be bf16 or fp32 CUDA tensors")
-    if dy.shape != x.shape:
-        raise ValueError("dy must have x's shape")
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None and (t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous fp32 tensor of x's shape without the channels")
-    if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if dx.shape != x.shape or dx.dtype != x.dtype:
-        raise ValueError("dx must have x's shape and type")
-    if weight is not None and dweight is None:
-        dweight = torch.empty_like(weight)
-    if weight is not None and has_bias and dbias is None:
-        dbias = torch.empty_like(weight)
-    groups = _norm_params(B, C, (("weight", weight), ("dweight", dweight), ("dbias", dbias)))
-    if workspace is None and (dweight is not None or dbias is not None):
-        nbytes = layer_norm_bwd_workspace_bytes(B, N, H, C, groups)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-    rc = _lib.dit_layer_norm_bwd(dy.data_ptr(), _DTYPES[dy.dtype], ctypes.byref(_strides4(d4)), x.data_ptr(),
-                                 _DTYPES[x.dtype], ctypes.byref(_strides4(x4)), ptr(mean), rstd.data_ptr(), ptr(weight),
-                                 B, N, H, C, groups, 0 if mean is None else 1, dx.data_ptr(),
-                                 ctypes.byref(_strides4(_rows4(dx))), ptr(dweight), ptr(dbias), ptr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                 _stream_ptr(stream))
-    _check(rc, "dit_layer_norm_bwd")
-    return dx, dweight, dbias
+    rc, dx, dw, db = _calls.norm_bwd(dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace,
+                                     _stream_ptr(stream))
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_layer_norm_bwd")
+    return dx, dw, db
 
 
 def rope_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -775,41 +683,13 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions: torch.Tensor | None
     (i, i + rotary_dim / 2).  positions: int32 CUDA tensor [N] or [B or 1, N, axes]
     (None: 0, 1, ...), offset added; axis_pairs: how many pairs turn with each
     axis.  inverse turns back (the gradient).  out may be x."""
-    B, N, H, D = x.shape
-    if x.dtype not in _DTYPES or not x.is_cuda:
-        raise TypeError("x must be a bf16 or fp32 CUDA tensor")
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous one-dimensional fp64 CPU tensor")
-    if layout not in ("interleaved", "half"):
+    if layout not in _ROPE_LAYOUTS:
         raise ValueError('layout must be "interleaved" or "half"')
-    n_pairs = inv_freq.numel()
-    pairs = (n_pairs,) if axis_pairs is None else tuple(axis_pairs)
-    axes = len(pairs)
-    if sum(pairs) != n_pairs:
-        raise ValueError("axis_pairs must sum to the number of pairs")
-    pos_sb = 0
-    if positions is not None:
-        if positions.dtype != torch.int32 or not positions.is_cuda:
-            raise TypeError("positions must be an int32 CUDA tensor")
-        shape, step = positions.shape, positions.stride()
-        if len(shape) == 1 and axes == 1:
-            shape, step = (1, shape[0], 1), (0, step[0], 1)
-        if len(shape) != 3 or shape[0] not in (1, B) or shape[1] != N or shape[2] != axes:
-            raise ValueError("positions must be [N] (one axis) or [B or 1, N, axes]")
-        if (N > 1 and step[1] != axes) or (axes > 1 and step[2] != 1):
-            raise ValueError("each batch entry's positions must be contiguous")
-        pos_sb = 0 if shape[0] == 1 else step[0]
-    if out is None:
-        out = torch.empty((B, N, H, D), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and type")
-    rc = _lib.dit_rope(x.data_ptr(), _DTYPES[x.dtype], ctypes.byref(_strides4(x)), B, N, H, D, 2 * n_pairs,
-                       DIT_ROPE_HALF if layout == "half" else DIT_ROPE_INTERLEAVED, inv_freq.data_ptr(),
-                       (ctypes.c_int * axes)(*pairs), axes, None if positions is None else positions.data_ptr(), pos_sb,
-                       int(offset), float(mscale), 1 if inverse else 0, out.data_ptr(), ctypes.byref(_strides4(out)),
-                       _stream_ptr(stream))
-    _check(rc, "dit_rope")
-    return out
+    rc, y = _calls.rope(x, inv_freq, positions, _ROPE_LAYOUTS[layout], axis_pairs, offset, mscale, inverse, out,
+                        _stream_ptr(stream))
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_rope")
+    return y
 
 
 def watchdog_selftest(limit_us: int = 100_000, stream=None):

@@ -1,4 +1,5 @@
-"""Builds libditattn.so in-tree with nvcc for sm_103a (no cmake, no torch).
+"""Builds libditattn.so in-tree with nvcc for sm_103a (no cmake; the library
+itself without torch).
 
     python -m dit_long_sequence_gb300.build [--force] [--verbose]
 
@@ -6,7 +7,9 @@ Each .cu under csrc/ compiles to an object in parallel, then one shared-library
 link: dit_long_sequence_gb300/_build/libditattn.so.  The same sources compiled
 with -DDIT_DEBUG (in-kernel bounds checks and fault injection,
 include/dit_attn_debug.h) give _build/debug/libditattn_debug.so, built in the
-same parallel pass.
+same parallel pass, and so does _build/dit_calls.so, the CPython extension that
+marshals the training operators' calls (csrc/py_calls.cpp, g++ against
+PyTorch's headers).
 """
 from __future__ import annotations
 
@@ -15,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +29,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libditattn.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libditattn_debug.so")
+CALLS = os.path.join(BUILD, "dit_calls.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_fwd_fp8.cu", "qkv_cast_fp8.cu", "lse_merge.cu", "qkv_layout.cu",
            "qkv_norm_rope.cu", "mask_occupancy.cu", "selftest.cu", "api_train.cu", "attn_bwd.cu", "layer_norm.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,15 +56,36 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def build_calls() -> str:
+    """Compiles the call layer against the installed PyTorch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"]]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE]
+    for d in dirs:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "py_calls.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for py_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
-    """Builds libditattn.so (and, with debug=True, libditattn_debug.so) if
-    a source is newer; returns the product library's path."""
+    """Builds libditattn.so and the call layer (and, with debug=True,
+    libditattn_debug.so) if a source is newer; returns the product library's path."""
     targets = [(LIB, BUILD, [])]
     if debug:
         targets.append((DEBUG_LIB, DEBUG_BUILD, ["-DDIT_DEBUG"]))
     targets = [t for t in targets if force or not up_to_date(t[0])]
-    if not targets:
+    calls = force or not up_to_date(CALLS)
+    if not targets and not calls:
         return LIB
+    os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
     if verbose:
@@ -80,8 +106,11 @@ def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str
     for lib, out_dir, defs in targets:
         os.makedirs(out_dir, exist_ok=True)
         jobs += [(src, out_dir, defs) for src in SOURCES]
-    with ThreadPoolExecutor(max_workers=min(len(jobs), max(4, os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, max(4, os.cpu_count() or 4))) as ex:
+        layer = ex.submit(build_calls) if calls else None
         objs = list(ex.map(compile_one, jobs))
+        if layer is not None:
+            layer.result()
     for lib, out_dir, _ in targets:
         mine = [o for o in objs if os.path.dirname(o) == out_dir]
         tmp = lib + f".tmp{os.getpid()}"
