@@ -12,7 +12,9 @@
 // 2^64 -- the wrap-around is the range reduction, exact at any 32-bit
 // position (the fraction's rounding moves an angle by at most 2 pi * 2^-65
 // per step, and the caller's fp64 frequency by 2^-53 of itself).  The upper
-// 32 bits, rounded, go to sincospif as half turns in [-1, 1).
+// 32 bits, rounded, split into a quarter turn and a signed rest of at most an
+// eighth, whose sine and cosine are their Taylor polynomials of degree 9 and 10
+// (the first terms left out are below 2^-28 of an eighth turn's values).
 //
 // HBM-bound: every element is read once and written once; positions are 4
 // bytes a token.  A block takes `tokens` tokens: the cos/sin of their pairs
@@ -48,6 +50,25 @@ __host__ __device__ constexpr int unroll(bool half) { return half ? 2 : 4; }
 
 template <typename T> struct IsF32 { static constexpr bool value = false; };
 template <> struct IsF32<float> { static constexpr bool value = true; };
+
+// sin and cos of t / 2^32 turns.
+__device__ __forceinline__ void sincos_turns(uint32_t t, float& sn, float& cs) {
+    const uint32_t q = (t + 0x20000000u) >> 30;                        // nearest quarter turn
+    const float x = static_cast<float>(static_cast<int32_t>(t - (q << 30))) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    const float z = x * x;
+    float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(z, s, 1.f / 120.f);
+    s = fmaf(z, s, -1.f / 6.f);
+    s = fmaf(z * x, s, x);
+    float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+    c = fmaf(z, c, -1.f / 720.f);
+    c = fmaf(z, c, 1.f / 24.f);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.f);
+    const float a = (q & 1u) ? c : s, b = (q & 1u) ? s : c;
+    sn = __uint_as_float(__float_as_uint(a) ^ ((q & 2u) << 30));
+    cs = __uint_as_float(__float_as_uint(b) ^ (((q + 1u) & 2u) << 30));
+}
 
 // `VEC` elements as raw 32-bit words (or one 16-bit element).
 template <typename T, int VEC>
@@ -100,7 +121,7 @@ struct Pack {
 // units are kThreads apart in (token, head, unit) order, so it steps from one to
 // the next with additions (`step`) instead of dividing.
 template <typename T, bool HALF, int VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, const RopeGrid gr) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, const RopeGrid gr) {
     // units in flight per thread: a half-layout unit is two loads
     constexpr int kUnroll = unroll(HALF);
     extern __shared__ __align__(16) float angles[];     // cos [tokens][stride], then sin
@@ -146,7 +167,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, const 
     };
     load();
 
-    // cos/sin of every (token, pair) of this block
+    // cos/sin of every (token, pair) of this block.  The table of turns is read
+    // through a plain address: indexed as a parameter its 32 lanes' different
+    // elements would be fetched one after another.
+    const uint64_t* turns = a.turns;
+    asm volatile("" : "+l"(turns));
     for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(nt * a.pairs); i += kThreads) {
         uint32_t pr;
         const uint32_t n = gr.div_pairs.divmod(i, pr);
@@ -155,9 +180,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, const 
         for (int k = 0; k + 1 < kRopeMaxAxes; ++k) axis += (k + 1 < a.axes && pr >= a.axis_end[k]) ? 1 : 0;
         const int64_t pos = a.offset + (a.pos != nullptr ? static_cast<int64_t>(__ldg(a.pos + b * a.pos_sb + static_cast<int64_t>(n0 + n) * a.axes + axis))
                                                         : static_cast<int64_t>(n0 + n));
-        const uint64_t t = static_cast<uint64_t>(pos) * a.turns[pr] + 0x80000000ull;
+        const uint64_t t = static_cast<uint64_t>(pos) * turns[pr] + 0x80000000ull;
         float s, c;
-        sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &s, &c);
+        sincos_turns(static_cast<uint32_t>(t >> 32), s, c);
         cosv[n * gr.stride + pr] = c * a.mscale;
         sinv[n * gr.stride + pr] = (a.inverse ? -s : s) * a.mscale;
     }

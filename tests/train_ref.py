@@ -116,9 +116,9 @@ def layer_norm_bwd(dy, x, mean, rstd, weight, chain):
 
 def rope(x, inv_freq, pos, pairs, half, mscale, inverse):
     """fp64 rotation of [B, N, H, D] and its bound without y's rounding: the
-    angle reaches sincospif as a half turn rounded to fp32 (2^-25 of a half turn,
-    pi 2^-25 rad) and its results are good to 2 steps, then four operations:
-    2^-20 (|a| + |b|) mscale."""
+    angle, an integer of 2^-32 turns, becomes an fp32 number of at most an eighth
+    turn (2^-25 of it) times 2 pi (another), and the polynomials' results are good
+    to a few steps, then four operations: 2^-20 (|a| + |b|) mscale."""
     R = 2 * inv_freq.numel()
     axis = torch.cat([torch.full((n,), i, dtype=torch.long) for i, n in enumerate(pairs)]).to(x.device)
     # the angle modulo a turn in exact integer arithmetic over Python ints would be slow; fp64 is exact to
