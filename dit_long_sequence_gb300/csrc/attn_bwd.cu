@@ -878,6 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     s.tmem = *tmem_slot;
+    if (threadIdx.x == 0) let_next();
+    after_previous();      // the statistics, and the counter's zero
 
     // Each role runs through the key items, then the query items.  Nothing but
     // its barriers holds one back; a role that gave up leaves the others to.
@@ -926,6 +928,7 @@ template <int D, bool OUT_BF16>
 __global__ void __launch_bounds__(256) attn_bwd_stat_kernel(const AttnBwdStatArgs a) {
     constexpr int LPR = D / 8;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (threadIdx.x == 0) let_next();
     if (g == 0) *a.counter = 0u;      // of the main kernel's items
     const int64_t unit = g / LPR;
     const int c = static_cast<int>(g % LPR);
@@ -976,6 +979,7 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_kernel(const AttnBwdStatArg
 // blockIdx.y: 0 dv, 1 dk, 2 dq (those that were split).
 template <int D, bool OUT_BF16>
 __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const AttnBwdArgs a, int first) {
+    after_previous();
     const int which = static_cast<int>(blockIdx.y) + first;
     const bool key = which < 2;
     const int f = key ? a.f_kv : a.f_q;
@@ -1012,8 +1016,7 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     auto kern = attn_bwd_kernel<D, OUT_BF16, MASK>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.grid, kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
-    return cudaGetLastError();
+    return launch_behind(kern, a.grid, kThreads, Cfg<D>::kSmemBytes, s, tq, tk, tv, tdo, a);
 }
 
 }  // namespace
@@ -1053,13 +1056,12 @@ cudaError_t launch_attn_bwd_sum(const AttnBwdArgs& a, int D, bool grad_bf16, cud
     const dim3 grid(static_cast<unsigned>((threads + 255) / 256), (kv ? 2 : 0) + (q ? 1 : 0));
     const int first = kv ? 0 : 2;
     if (D == 128) {
-        if (grad_bf16) attn_bwd_sum_kernel<128, true><<<grid, 256, 0, s>>>(a, first);
-        else attn_bwd_sum_kernel<128, false><<<grid, 256, 0, s>>>(a, first);
+        if (grad_bf16) return launch_behind(attn_bwd_sum_kernel<128, true>, grid, 256, 0, s, a, first);
+        else return launch_behind(attn_bwd_sum_kernel<128, false>, grid, 256, 0, s, a, first);
     } else {
-        if (grad_bf16) attn_bwd_sum_kernel<64, true><<<grid, 256, 0, s>>>(a, first);
-        else attn_bwd_sum_kernel<64, false><<<grid, 256, 0, s>>>(a, first);
+        if (grad_bf16) return launch_behind(attn_bwd_sum_kernel<64, true>, grid, 256, 0, s, a, first);
+        else return launch_behind(attn_bwd_sum_kernel<64, false>, grid, 256, 0, s, a, first);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace dit

@@ -30,6 +30,39 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 
+// Two fp32 numbers in a register pair: the kernels are bound by instructions as
+// much as by memory, and packed operations halve the arithmetic.  Pairs are kept
+// as 64-bit values throughout, so that none is packed twice.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpk(f2 p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 p) {
+    float lo, hi;
+    unpk(p, lo, hi);
+    return lo + hi;
+}
+// Pairs of VEC channels; a single channel is a pair whose second number is 0.
+__host__ __device__ constexpr int pairs_of(int vec) { return vec == 1 ? 1 : vec / 2; }
+
 template <typename T, int VEC>
 struct Row {   // VEC elements as loaded
     static constexpr int kBytes = static_cast<int>(sizeof(T)) * VEC;
@@ -55,19 +88,24 @@ struct Row {   // VEC elements as loaded
             w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
         }
     }
-    __device__ __forceinline__ float get(int i) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+    static constexpr int kPairs = pairs_of(VEC);
+    // channels 2i and 2i + 1
+    __device__ __forceinline__ f2 pair(int i) const {
+        if constexpr (VEC == 1) return pk(__uint_as_float(sizeof(T) == 4 ? w[0] : w[0] << 16), 0.f);
+        else if constexpr (sizeof(T) == 4) return pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[VEC]) {
+    // rounded to T once
+    static __device__ __forceinline__ void store(T* p, const f2 (&v)[kPairs]) {
         Row r;
-        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) r.w[i] = __float_as_uint(v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                const float lo = v[VEC > 1 ? 2 * i : 0], hi = VEC > 1 ? v[VEC > 1 ? 2 * i + 1 : 0] : 0.f;
+        for (int i = 0; i < kPairs; ++i) {
+            float lo, hi;
+            unpk(v[i], lo, hi);
+            if constexpr (sizeof(T) == 4) {
+                r.w[VEC == 1 ? 0 : 2 * i] = __float_as_uint(lo);
+                if constexpr (VEC > 1) r.w[2 * i + 1] = __float_as_uint(hi);
+            } else {
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(hi), "f"(lo));
             }
         }
@@ -95,7 +133,7 @@ struct Ring {
     using R = Row<T, VEC>;
     static constexpr bool kAsync = R::kBytes >= 4;
     static constexpr int kChunk = R::kBytes < 16 ? R::kBytes : 16;    // bytes of one copy
-    static constexpr int kChunks = kAsync ? R::kBytes / kChunk : 1;
+    static constexpr int kChunks = R::kBytes < 16 ? 1 : R::kBytes / 16;
     static constexpr int kStageBytes = NV * R::kBytes;                // per thread
     uint32_t base;              // this thread's first chunk; chunks lie blockDim.x apart
     R reg[kAsync ? 1 : NV];
@@ -154,21 +192,6 @@ __host__ __device__ constexpr int ring_depth(int stage_bytes, bool async) {
     return p < 2 ? 2 : (p > 6 ? 6 : p);
 }
 
-// Packed pairs of fp32 operations: the kernels are bound by instructions as
-// much as by memory, and these halve the arithmetic.
-__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-
 // The threads of one row: `tpr` of them (a power of two), whole warps when
 // tpr > 32.  Sums over the row reach every thread in the same order.
 struct RowGroup {
@@ -188,6 +211,30 @@ struct RowGroup {
             for (int o = tpr >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         }
         return v;
+    }
+    // Two sums at once: lanes of the lower half end with the first, of the upper
+    // half with the second (5 shuffles for both; whole warps only).
+    __device__ __forceinline__ float lanes_two(float a, float b) const {
+        const bool upper = (threadIdx.x & 16) != 0;
+        float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    // The sums of lanes_two over the row's warps, to every thread.
+    __device__ __forceinline__ f2 across_two(float v) {
+        float* const b = reinterpret_cast<float*>(buf + flip * (kMaxThreads / 32));
+        flip ^= 1;
+        if ((threadIdx.x & 15) == 0) b[threadIdx.x >> 4] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(tpr) : "memory");
+        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(b + 2 * id * warps);    // (two warps or more)
+        ulonglong2 q = p[0];
+        f2 t = add2(q.x, q.y);
+        for (int w = 1; w < (warps >> 1); ++w) {
+            q = p[w];
+            t = add2(t, add2(q.x, q.y));
+        }
+        return t;
     }
     // Each warp's pair to the row's other warps: lane l gets that of warp
     // l mod warps.  One barrier among the row's threads; the other buffer is
@@ -224,15 +271,18 @@ struct RowAt {
 };
 
 template <int VEC>
-__device__ __forceinline__ void load_params(const float* p, float (&v)[VEC]) {
+__device__ __forceinline__ void load_params(const float* p, f2 (&v)[pairs_of(VEC)]) {
     if constexpr (VEC == 8) {
         const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w; v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        v[0] = pk(lo.x, lo.y);
+        v[1] = pk(lo.z, lo.w);
+        v[2] = pk(hi.x, hi.y);
+        v[3] = pk(hi.z, hi.w);
     } else if constexpr (VEC == 2) {
         const float2 x = __ldg(reinterpret_cast<const float2*>(p));
-        v[0] = x.x; v[1] = x.y;
+        v[0] = pk(x.x, x.y);
     } else {
-        v[0] = __ldg(p);
+        v[0] = pk(__ldg(p), 0.f);
     }
 }
 
@@ -271,11 +321,12 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
         ring_commit();
     };
     for (int k = 0; k < P - 1; ++k) fetch(k);
-    float w[NV][VEC], bi[NV][VEC];
+    constexpr int NP = pairs_of(VEC);
+    f2 w[NV][NP], bi[NV][NP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) { w[i][e] = 1.f; bi[i][e] = 0.f; }
+        for (int e = 0; e < NP; ++e) { w[i][e] = pk(1.f, 1.f); bi[i][e] = 0ull; }
         if (live[i] && a.weight) load_params<VEC>(a.weight + static_cast<int64_t>(blockIdx.y) * a.C + col[i], w[i]);
         if (live[i] && a.bias) load_params<VEC>(a.bias + static_cast<int64_t>(blockIdx.y) * a.C + col[i], bi[i]);
     }
@@ -297,48 +348,38 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
         fetch(k + P - 1);
         ring_wait<P - 1>();
         const bool ok = r < a.rows_per_group;
-        float x[NV][VEC];
+        f2 x[NV][NP];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (ok && live[i]) {
-                const Row<TX, VEC> v = ring.take(k % P, i);
+            Row<TX, VEC> v;
+            v.zero();
+            if (ok && live[i]) v = ring.take(k % P, i);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) x[i][e] = v.get(e);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
-            }
+            for (int e = 0; e < NP; ++e) x[i][e] = v.pair(e);
         }
         // This warp's mean and sum of squared deviations from it, then the row's
         // from all its warps': sum of (their deviations + n (their mean - mean)^2).
         float mean = 0.f, s = 0.f;
         if (a.center) {
-            float s0 = 0.f, s1 = 0.f;
+            f2 t = 0ull;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if constexpr (VEC == 1) s0 += x[i][0];
-                else
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int e = 0; e < VEC; e += 2) add2(s0, s1, s0, s1, x[i][e], x[i][e + 1]);
-            }
-            s = g.lanes(s0 + s1);
+                for (int e = 0; e < NP; ++e) t = add2(t, x[i][e]);
+            s = g.lanes(sum2(t));
             mean = s * own_inv;
         }
-        float q0 = 0.f, q1 = 0.f;
+        f2 u = 0ull;
+        const f2 minus = pk(-mean, VEC == 1 ? 0.f : -mean);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if constexpr (VEC == 1) {
-                x[i][0] = live[i] ? x[i][0] - mean : 0.f;
-                q0 = fmaf(x[i][0], x[i][0], q0);
-            } else if (live[i]) {
+        for (int i = 0; i < NV; ++i)
+            if (live[i])
 #pragma unroll
-                for (int e = 0; e < VEC; e += 2) {
-                    add2(x[i][e], x[i][e + 1], x[i][e], x[i][e + 1], -mean, -mean);
-                    fma2(q0, q1, x[i][e], x[i][e + 1], x[i][e], x[i][e + 1], q0, q1);
+                for (int e = 0; e < NP; ++e) {
+                    x[i][e] = add2(x[i][e], minus);
+                    u = fma2(x[i][e], x[i][e], u);
                 }
-            }
-        }
-        float q = g.lanes(q0 + q1);
+        float q = g.lanes(sum2(u));
         float shift = 0.f;          // this warp's mean - the row's, still in x
         if (tpr > 32) {
             const float2 p = g.exchange(make_float2(s, q));
@@ -355,20 +396,13 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
         const float rstd = 1.f / sqrtf(q * a.inv_c + a.eps);
         if (ok) {
             TY* const p = static_cast<TY*>(a.y) + y_at(a, row0 + r);
-            const float sr = shift * rstd;
+            const f2 r2 = pk(rstd, rstd), sr = pk(shift * rstd, shift * rstd);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live[i]) {
-                    float v[VEC];
-                    if constexpr (VEC == 1) {
-                        v[0] = fmaf(fmaf(x[i][0], rstd, sr), w[i][0], bi[i][0]);
-                    } else {
+                    f2 v[NP];
 #pragma unroll
-                        for (int e = 0; e < VEC; e += 2) {
-                            fma2(v[e], v[e + 1], x[i][e], x[i][e + 1], rstd, rstd, sr, sr);
-                            fma2(v[e], v[e + 1], v[e], v[e + 1], w[i][e], w[i][e + 1], bi[i][e], bi[i][e + 1]);
-                        }
-                    }
+                    for (int e = 0; e < NP; ++e) v[e] = fma2(fma2(x[i][e], r2, sr), w[i][e], bi[i][e]);
                     Row<TY, VEC>::store(p + col[i], v);
                 }
             if (g.t == 0) {
@@ -384,9 +418,10 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
     using RX = Ring<TX, VEC, NV>;
     using RD = Ring<TY, VEC, NV>;
     constexpr int P = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
-    __shared__ float2 buf[2 * kMaxThreads / 32];
+    __shared__ __align__(16) float2 buf[2 * kMaxThreads / 32];
     extern __shared__ __align__(16) uint8_t ring_mem[];   // the rings; after the rows, [slots][tpr * NV * VEC] sums
     float* const acc = reinterpret_cast<float*>(ring_mem);
+    if (threadIdx.x == 0) let_next();
     RowGroup g(tpr, buf);
     RX rx;
     RD rd;
@@ -428,11 +463,12 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
     };
     for (int k = 0; k < P - 1; ++k) fetch(k);
     stats(0);
-    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    constexpr int NP = pairs_of(VEC);
+    f2 w[NV][NP], dw[NV][NP], db[NV][NP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) { w[i][e] = 1.f; dw[i][e] = 0.f; db[i][e] = 0.f; }
+        for (int e = 0; e < NP; ++e) { w[i][e] = pk(1.f, 1.f); dw[i][e] = 0ull; db[i][e] = 0ull; }
         if (live[i] && a.weight) load_params<VEC>(a.weight + static_cast<int64_t>(blockIdx.y) * a.C + col[i], w[i]);
     }
     uint32_t r = first;
@@ -442,8 +478,9 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
         const bool ok = r < a.rows_per_group;
         const float rstd = nrstd, mr = -nmean * nrstd;
         stats(k + 1);
-        float xh[NV][VEC], gr[NV][VEC];      // xh and g, kept for dx
-        float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+        f2 xh[NV][NP], gr[NV][NP];      // xh and g, kept for dx
+        f2 s2 = 0ull, t2 = 0ull;
+        const f2 r2 = pk(rstd, rstd), m2 = pk(mr, mr);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             Row<TX, VEC> x;
@@ -451,51 +488,36 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
             x.zero();
             d.zero();
             if (ok && live[i]) { x = rx.take(k % P, i); d = rd.take(k % P, i); }
-            if constexpr (VEC == 1) {
-                const float dy = d.get(0);
-                xh[i][0] = fmaf(x.get(0), rstd, mr);
-                gr[i][0] = dy * w[i][0];
-                s0 += gr[i][0];
-                t0 = fmaf(gr[i][0], xh[i][0], t0);
-                dw[i][0] = fmaf(dy, xh[i][0], dw[i][0]);
-                db[i][0] += dy;
-            } else {
 #pragma unroll
-                for (int e = 0; e < VEC; e += 2) {
-                    const float d0 = d.get(e), d1 = d.get(e + 1);
-                    fma2(xh[i][e], xh[i][e + 1], x.get(e), x.get(e + 1), rstd, rstd, mr, mr);
-                    mul2(gr[i][e], gr[i][e + 1], d0, d1, w[i][e], w[i][e + 1]);
-                    add2(s0, s1, s0, s1, gr[i][e], gr[i][e + 1]);
-                    fma2(t0, t1, gr[i][e], gr[i][e + 1], xh[i][e], xh[i][e + 1], t0, t1);
-                    fma2(dw[i][e], dw[i][e + 1], d0, d1, xh[i][e], xh[i][e + 1], dw[i][e], dw[i][e + 1]);
-                    add2(db[i][e], db[i][e + 1], db[i][e], db[i][e + 1], d0, d1);
-                }
+            for (int e = 0; e < NP; ++e) {
+                const f2 dy = d.pair(e);
+                xh[i][e] = fma2(x.pair(e), r2, m2);
+                gr[i][e] = mul2(dy, w[i][e]);
+                s2 = add2(s2, gr[i][e]);
+                t2 = fma2(gr[i][e], xh[i][e], t2);
+                dw[i][e] = fma2(dy, xh[i][e], dw[i][e]);
+                db[i][e] = add2(db[i][e], dy);
             }
         }
-        float sg = a.center ? g.lanes(s0 + s1) : 0.f;
-        float st = g.lanes(t0 + t1);
+        float sg, st;
         if (tpr > 32) {
-            const float2 p = g.exchange(make_float2(sg, st));
-            if (a.center) sg = g.across(p.x);
-            st = g.across(p.y);
+            unpk(g.across_two(g.lanes_two(sum2(s2), sum2(t2))), sg, st);
+        } else {
+            sg = g.lanes(sum2(s2));
+            st = g.lanes(sum2(t2));
         }
+        if (!a.center) sg = 0.f;
         // dx = rstd g - rstd c1 - xh (rstd c2)
         const float n1 = -sg * a.inv_c * rstd, n2 = -st * a.inv_c * rstd;
         if (ok) {
             TX* const p = static_cast<TX*>(a.y) + y_at(a, row0 + r);
+            const f2 c1 = pk(n1, n1), c2 = pk(n2, n2);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live[i]) {
-                    float v[VEC];
-                    if constexpr (VEC == 1) {
-                        v[0] = fmaf(gr[i][0], rstd, fmaf(xh[i][0], n2, n1));
-                    } else {
+                    f2 v[NP];
 #pragma unroll
-                        for (int e = 0; e < VEC; e += 2) {
-                            fma2(v[e], v[e + 1], xh[i][e], xh[i][e + 1], n2, n2, n1, n1);
-                            fma2(v[e], v[e + 1], gr[i][e], gr[i][e + 1], rstd, rstd, v[e], v[e + 1]);
-                        }
-                    }
+                    for (int e = 0; e < NP; ++e) v[e] = fma2(gr[i][e], r2, fma2(xh[i][e], c2, c1));
                     Row<TX, VEC>::store(p + col[i], v);
                 }
         }
@@ -504,7 +526,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
     // The block's sums: row slots added in order, then one partial per block
     // (the gradient itself when the group has one block).
     const int width = tpr * NV * VEC;
-    auto leave = [&](float (&v)[NV][VEC], float* part, float* grad) {
+    auto leave = [&](f2 (&v)[NV][NP], float* part, float* grad) {
         float* const out = gridDim.x == 1 ? grad + static_cast<int64_t>(blockIdx.y) * a.C
                                           : part + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * a.C;
         if (slots == 1) {
@@ -512,14 +534,24 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
             for (int i = 0; i < NV; ++i)
                 if (live[i])
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) out[col[i] + e] = v[i][e];
+                    for (int e = 0; e < NP; ++e) {
+                        float lo, hi;
+                        unpk(v[i][e], lo, hi);
+                        out[col[i] + 2 * e] = lo;
+                        if (VEC > 1) out[col[i] + 2 * e + 1] = hi;
+                    }
             return;
         }
         __syncthreads();     // the rings (or the last sums) have been read
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[g.id * width + col[i] + e] = v[i][e];
+            for (int e = 0; e < NP; ++e) {
+                float lo, hi;
+                unpk(v[i][e], lo, hi);
+                acc[g.id * width + col[i] + 2 * e] = lo;
+                if (VEC > 1) acc[g.id * width + col[i] + 2 * e + 1] = hi;
+            }
         __syncthreads();
         for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
             float t = 0.f;
@@ -532,22 +564,25 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
 }
 
 // dweight / dbias [groups][C] = the sum over a group's `parts` partials, each
-// column's in a fixed order: 8 interleaved sums, then those in order.
-__global__ void __launch_bounds__(256) layer_norm_param_sum_kernel(const NormArgs a, int parts) {
-    __shared__ float s[8][33];
+// column's in a fixed order: 32 interleaved sums, then those in order.
+__global__ void __launch_bounds__(1024) layer_norm_param_sum_kernel(const NormArgs a, int parts) {
+    __shared__ float s[32][33];
+    after_previous();
     const int cx = threadIdx.x & 31, py = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + cx;
     const bool second = blockIdx.z != 0 || !a.want_w;
     float* const out = second ? a.dbias : a.dweight;
     const float* const p = a.part + (static_cast<int64_t>(second ? a.groups : 0) + blockIdx.y) * parts * a.C;
     float t = 0.f;
-    if (c < a.C)
-        for (int k = py; k < parts; k += 8) t += __ldcs(p + static_cast<int64_t>(k) * a.C + c);
+    if (c < a.C) {
+#pragma unroll 4
+        for (int k = py; k < parts; k += 32) t += __ldcs(p + static_cast<int64_t>(k) * a.C + c);
+    }
     s[py][cx] = t;
     __syncthreads();
     if (py == 0 && c < a.C) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) t += s[k][cx];
+        for (int k = 1; k < 32; ++k) t += s[k][cx];
         out[static_cast<int64_t>(blockIdx.y) * a.C + c] = t;
     }
 }
@@ -582,8 +617,7 @@ cudaError_t bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     const int wants = (a.want_w ? 1 : 0) + (a.want_b ? 1 : 0);
     if (e != cudaSuccess || p.blocks == 1 || wants == 0) return e;
-    layer_norm_param_sum_kernel<<<dim3((a.C + 31) / 32, a.groups, wants), 256, 0, s>>>(a, p.blocks);
-    return cudaGetLastError();
+    return launch_behind(layer_norm_param_sum_kernel, dim3((a.C + 31) / 32, a.groups, wants), 1024, 0, s, a, p.blocks);
 }
 
 template <typename TX, typename TY, bool BWD>
@@ -592,7 +626,9 @@ cudaError_t pick(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
     if (p.vec == V && p.nv == N) return BWD ? bwd<TX, TY, V, N>(a, p, s) : fwd<TX, TY, V, N>(a, p, s);
     DIT_NORM_CASE(8, 1)
     DIT_NORM_CASE(8, 2)
-    DIT_NORM_CASE(8, 4)
+    if constexpr (!BWD) {
+        DIT_NORM_CASE(8, 4)
+    }
     DIT_NORM_CASE(2, 4)
     DIT_NORM_CASE(2, 8)
     DIT_NORM_CASE(1, 8)

@@ -34,6 +34,29 @@ struct FastDiv {
 #endif
 };
 
+#ifdef __CUDACC__
+// Launches a kernel that may be set up while the one before it on the stream
+// ends (a programmatic dependent launch); it calls after_previous() before it
+// touches anything the other wrote.  The other calls let_next() at its start:
+// the next kernel's blocks then take what room is left, and the rest later.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // ------------------------------------------------------------ layer norm
 
 struct NormArgs {
