@@ -29,6 +29,9 @@ namespace dit {
 namespace {
 
 constexpr int kMaxThreads = 512;
+// Cross-warp sums of a block, in 8 bytes a warp; a row's warps are padded to an
+// even number (5 rows of 3 warps take 20).
+constexpr int kSums = 24;
 
 // Two fp32 numbers in a register pair: the kernels are bound by instructions as
 // much as by memory, and packed operations halve the arithmetic.  Pairs are kept
@@ -60,8 +63,8 @@ __device__ __forceinline__ float sum2(f2 p) {
     unpk(p, lo, hi);
     return lo + hi;
 }
-// Pairs of VEC channels; a single channel is a pair whose second number is 0.
-__host__ __device__ constexpr int pairs_of(int vec) { return vec == 1 ? 1 : vec / 2; }
+// A thread's channels of a row, NV loads of VEC, are NV * VEC / 2 pairs: two
+// neighbours of one load, or with VEC = 1 the channels of two loads.
 
 template <typename T, int VEC>
 struct Row {   // VEC elements as loaded
@@ -88,53 +91,67 @@ struct Row {   // VEC elements as loaded
             w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
         }
     }
-    static constexpr int kPairs = pairs_of(VEC);
+    __device__ __forceinline__ float one() const { return __uint_as_float(sizeof(T) == 4 ? w[0] : w[0] << 16); }
     // channels 2i and 2i + 1
     __device__ __forceinline__ f2 pair(int i) const {
-        if constexpr (VEC == 1) return pk(__uint_as_float(sizeof(T) == 4 ? w[0] : w[0] << 16), 0.f);
-        else if constexpr (sizeof(T) == 4) return pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        if constexpr (sizeof(T) == 4) return pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
         else return pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    // rounded to T once
-    static __device__ __forceinline__ void store(T* p, const f2 (&v)[kPairs]) {
-        Row r;
+};
+// Pair k of a thread's NV loads.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ f2 pair_of(const Row<T, VEC> (&r)[NV], int k) {
+    if constexpr (VEC == 1) return pk(r[2 * k].one(), r[2 * k + 1].one());
+    else return r[k / (VEC / 2)].pair(k % (VEC / 2));
+}
+// Load i's channels from its pairs, rounded to T once.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row(T* p, int i, const f2 (&v)[NV * VEC / 2]) {
+    using R = Row<T, VEC>;
+    uint32_t w[R::kWords];
+    if constexpr (VEC == 1) {
+        float lo, hi;
+        unpk(v[i / 2], lo, hi);
+        const float x = (i & 1) ? hi : lo;
+        if constexpr (sizeof(T) == 4) w[0] = __float_as_uint(x);
+        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(0.f), "f"(x));
+    } else {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
+        for (int e = 0; e < VEC / 2; ++e) {
             float lo, hi;
-            unpk(v[i], lo, hi);
+            unpk(v[i * (VEC / 2) + e], lo, hi);
             if constexpr (sizeof(T) == 4) {
-                r.w[VEC == 1 ? 0 : 2 * i] = __float_as_uint(lo);
-                if constexpr (VEC > 1) r.w[2 * i + 1] = __float_as_uint(hi);
+                w[2 * e] = __float_as_uint(lo);
+                w[2 * e + 1] = __float_as_uint(hi);
             } else {
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(hi), "f"(lo));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(hi), "f"(lo));
             }
         }
-        if constexpr (kBytes >= 16) {
-#pragma unroll
-            for (int i = 0; i < kWords / 4; ++i)
-                __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]));
-        } else if constexpr (kBytes == 8) {
-            __stcs(reinterpret_cast<uint2*>(p), make_uint2(r.w[0], r.w[1]));
-        } else if constexpr (kBytes == 4) {
-            __stcs(reinterpret_cast<uint32_t*>(p), r.w[0]);
-        } else {
-            __stcs(reinterpret_cast<unsigned short*>(p), static_cast<unsigned short>(r.w[0]));
-        }
     }
-};
+    if constexpr (R::kBytes >= 16) {
+#pragma unroll
+        for (int e = 0; e < R::kWords / 4; ++e)
+            __stcs(reinterpret_cast<uint4*>(p) + e, make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+    } else if constexpr (R::kBytes == 8) {
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+    } else if constexpr (R::kBytes == 4) {
+        __stcs(reinterpret_cast<uint32_t*>(p), w[0]);
+    } else {
+        __stcs(reinterpret_cast<unsigned short*>(p), static_cast<unsigned short>(w[0]));
+    }
+}
 
 // A thread's own ring of P staged rows in shared memory, filled by asynchronous
 // copies of its channels (no other thread reads them, so waiting for its own
 // copies is all the synchronisation there is).  Loads of single bf16 channels
-// are below the smallest asynchronous copy: those are loaded when their row is
-// due (a depth of one).
+// are below the smallest asynchronous copy: those wait in registers, a row ahead.
 template <typename T, int VEC, int NV>
 struct Ring {
     using R = Row<T, VEC>;
     static constexpr bool kAsync = R::kBytes >= 4;
     static constexpr int kChunk = R::kBytes < 16 ? R::kBytes : 16;    // bytes of one copy
     static constexpr int kChunks = R::kBytes < 16 ? 1 : R::kBytes / 16;
-    static constexpr int kStageBytes = NV * R::kBytes;                // per thread
+    static constexpr int kStageBytes = kAsync ? NV * kChunk * kChunks : 0;    // per thread
     uint32_t base;              // this thread's first chunk; chunks lie blockDim.x apart
     R reg[kAsync ? 1 : NV];
     __device__ __forceinline__ uint32_t slot(int stage, int i, int c) const {
@@ -181,26 +198,38 @@ __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows staged ahead: as many as keep some 64 bytes a thread and direction in
-// flight without holding more than half an SM's shared memory per 512 threads.
-#ifndef DIT_NORM_STAGE_BYTES
-#define DIT_NORM_STAGE_BYTES 128
-#endif
+// Rows staged ahead: as many as fill some 128 bytes of shared memory a thread
+// (64 KB for an SM's 512 threads), between 2 and 6.
+constexpr int kStagedBytes = 128;
 __host__ __device__ constexpr int ring_depth(int stage_bytes, bool async) {
     if (!async) return 1;
-    const int p = DIT_NORM_STAGE_BYTES / stage_bytes;
+    const int p = kStagedBytes / stage_bytes;
     return p < 2 ? 2 : (p > 6 ? 6 : p);
 }
 
-// The threads of one row: `tpr` of them (a power of two), whole warps when
-// tpr > 32.  Sums over the row reach every thread in the same order.
+// The threads of one row: `tpr` of them, a power of two up to 32 or else whole
+// warps.  Sums over the row reach every thread in the same order.
+// A forward block holds two rows of more than a warp at most, and names its
+// barriers: a barrier named at run time takes all 16 of a block, and an SM has
+// room for four such blocks.
+template <bool FWD>
 struct RowGroup {
     int tpr, t, id;             // threads per row, index in the row, row slot of the block
-    int warps;                  // warps of a row (1 when tpr <= 32)
-    float2* buf;                // [2][kMaxThreads / 32] cross-warp partials
+    int warps;                  // warps of a row (1 when tpr <= 32), at most 16
+    int span;                   // the next power of two: across() adds over that many lanes
+    float2* buf;                // [2][kSums], zeroed
+    int pitch;                  // a row's place in it: its warps, rounded up to even
     int flip;
     __device__ RowGroup(int tpr_, float2* b)
-        : tpr(tpr_), t(threadIdx.x & (tpr_ - 1)), id(threadIdx.x / tpr_), warps(tpr_ > 32 ? tpr_ >> 5 : 1), buf(b), flip(0) {}
+        : tpr(tpr_), t(threadIdx.x % tpr_), id(threadIdx.x / tpr_), warps(tpr_ > 32 ? tpr_ >> 5 : 1),
+          span(1), buf(b), pitch((warps + 1) & ~1), flip(0) {
+        while (span < warps) span *= 2;
+    }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (!FWD) asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(tpr) : "memory");
+        else if (id == 0) asm volatile("bar.sync 1, %0;" ::"r"(tpr) : "memory");
+        else asm volatile("bar.sync 2, %0;" ::"r"(tpr) : "memory");
+    }
     // Sum over the row's lanes of this warp.  Lanes of one warp may belong to
     // row slots that have run out of rows: every lane takes part in every sum.
     __device__ __forceinline__ float lanes(float v) const {
@@ -223,32 +252,33 @@ struct RowGroup {
     }
     // The sums of lanes_two over the row's warps, to every thread.
     __device__ __forceinline__ f2 across_two(float v) {
-        float* const b = reinterpret_cast<float*>(buf + flip * (kMaxThreads / 32));
+        float* const b = reinterpret_cast<float*>(buf + flip * kSums + id * pitch);
         flip ^= 1;
-        if ((threadIdx.x & 15) == 0) b[threadIdx.x >> 4] = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(tpr) : "memory");
-        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(b + 2 * id * warps);    // (two warps or more)
+        if ((threadIdx.x & 15) == 0) b[t >> 4] = v;
+        sync();
+        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(b);
         ulonglong2 q = p[0];
-        f2 t = add2(q.x, q.y);
-        for (int w = 1; w < (warps >> 1); ++w) {
+        f2 s = add2(q.x, q.y);
+        for (int w = 1; w < (pitch >> 1); ++w) {
             q = p[w];
-            t = add2(t, add2(q.x, q.y));
+            s = add2(s, add2(q.x, q.y));
         }
-        return t;
+        return s;
     }
     // Each warp's pair to the row's other warps: lane l gets that of warp
-    // l mod warps.  One barrier among the row's threads; the other buffer is
+    // l mod span (0 past the last).  One barrier among the row's threads; the other buffer is
     // written next, so a second is not needed.
     __device__ __forceinline__ float2 exchange(float2 v) {
-        float2* const b = buf + flip * (kMaxThreads / 32);
+        float2* const b = buf + flip * kSums + id * pitch;
         flip ^= 1;
-        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(tpr) : "memory");
-        return b[id * warps + (threadIdx.x & (warps - 1))];
+        if ((threadIdx.x & 31) == 0) b[t >> 5] = v;
+        sync();
+        const int w = threadIdx.x & (span - 1);
+        return w < warps ? b[w] : make_float2(0.f, 0.f);
     }
     // Sum of what exchange() handed out, over the row's warps.
     __device__ __forceinline__ float across(float v) const {
-        for (int o = warps >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int o = span >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
 };
@@ -270,20 +300,30 @@ struct RowAt {
     }
 };
 
-template <int VEC>
-__device__ __forceinline__ void load_params(const float* p, f2 (&v)[pairs_of(VEC)]) {
-    if constexpr (VEC == 8) {
-        const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        v[0] = pk(lo.x, lo.y);
-        v[1] = pk(lo.z, lo.w);
-        v[2] = pk(hi.x, hi.y);
-        v[3] = pk(hi.z, hi.w);
-    } else if constexpr (VEC == 2) {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(p));
-        v[0] = pk(x.x, x.y);
-    } else {
-        v[0] = pk(__ldg(p), 0.f);
+// A thread's weights (or biases), `other` where it has no channel or there are none.
+template <int VEC, int NV>
+__device__ __forceinline__ void load_params(const float* p, const bool (&live)[NV], const int (&col)[NV], float other,
+                                            f2 (&v)[NV * VEC / 2]) {
+    float f[NV * VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[i * VEC + e] = other;
+        if (p == nullptr || !live[i]) continue;
+        if constexpr (VEC == 8) {
+            const float4 lo = __ldg(reinterpret_cast<const float4*>(p + col[i])), hi = __ldg(reinterpret_cast<const float4*>(p + col[i]) + 1);
+            f[8 * i] = lo.x; f[8 * i + 1] = lo.y; f[8 * i + 2] = lo.z; f[8 * i + 3] = lo.w;
+            f[8 * i + 4] = hi.x; f[8 * i + 5] = hi.y; f[8 * i + 6] = hi.z; f[8 * i + 7] = hi.w;
+        } else if constexpr (VEC == 2) {
+            const float2 x = __ldg(reinterpret_cast<const float2*>(p + col[i]));
+            f[2 * i] = x.x;
+            f[2 * i + 1] = x.y;
+        } else {
+            f[i] = __ldg(p + col[i]);
+        }
     }
+#pragma unroll
+    for (int k = 0; k < NV * VEC / 2; ++k) v[k] = pk(f[2 * k], f[2 * k + 1]);
 }
 
 // grid (blocks, groups).  Every thread of a block makes the same number of
@@ -292,9 +332,9 @@ template <typename TX, typename TY, int VEC, int NV>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormArgs a, int tpr) {
     using RX = Ring<TX, VEC, NV>;
     constexpr int P = ring_depth(RX::kStageBytes, RX::kAsync);
-    __shared__ float2 buf[2 * kMaxThreads / 32];
+    __shared__ __align__(16) float2 buf[2 * kSums];
     extern __shared__ __align__(16) uint8_t ring_mem[];
-    RowGroup g(tpr, buf);
+    RowGroup<true> g(tpr, buf);
     RX ring;
     ring.init(ring_mem);
     const RowAt x_at(a, a.sx), y_at(a, a.sy);
@@ -320,65 +360,60 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
         }
         ring_commit();
     };
-    for (int k = 0; k < P - 1; ++k) fetch(k);
-    constexpr int NP = pairs_of(VEC);
-    f2 w[NV][NP], bi[NV][NP];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int e = 0; e < NP; ++e) { w[i][e] = pk(1.f, 1.f); bi[i][e] = 0ull; }
-        if (live[i] && a.weight) load_params<VEC>(a.weight + static_cast<int64_t>(blockIdx.y) * a.C + col[i], w[i]);
-        if (live[i] && a.bias) load_params<VEC>(a.bias + static_cast<int64_t>(blockIdx.y) * a.C + col[i], bi[i]);
-    }
+    for (int k = 0; k < (RX::kAsync ? P - 1 : 1); ++k) fetch(k);
+    constexpr int NP = NV * VEC / 2;
+    f2 w[NP], bi[NP];
+    load_params<VEC, NV>(a.weight ? a.weight + static_cast<int64_t>(blockIdx.y) * a.C : nullptr, live, col, 1.f, w);
+    load_params<VEC, NV>(a.bias ? a.bias + static_cast<int64_t>(blockIdx.y) * a.C : nullptr, live, col, 0.f, bi);
     // Channels held by warp v of a row, 1 / that (0 for none): by this thread's
     // own warp, and by the warp whose pair exchange() hands this lane.
     auto held = [&](int v) {
         int n = 0;
+        if (v >= g.warps) return 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) n += min(max(a.C - (i * tpr + 32 * v) * VEC, 0), 32 * VEC);
         return static_cast<float>(n);
     };
     const float own_n = tpr > 32 ? held(g.t >> 5) : static_cast<float>(a.C);
     const float own_inv = own_n > 0.f ? 1.f / own_n : 0.f;
-    const float got_n = tpr > 32 ? held(threadIdx.x & (g.warps - 1)) : 0.f;
+    const float got_n = tpr > 32 ? held(threadIdx.x & (g.span - 1)) : 0.f;
     const float got_inv = got_n > 0.f ? 1.f / got_n : 0.f;
 
     uint32_t r = first;
     for (uint32_t k = 0; k < rounds; ++k, r += step) {
-        fetch(k + P - 1);
-        ring_wait<P - 1>();
+        if constexpr (RX::kAsync) {
+            fetch(k + P - 1);
+            ring_wait<P - 1>();
+        }
         const bool ok = r < a.rows_per_group;
-        f2 x[NV][NP];
+        Row<TX, VEC> raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            Row<TX, VEC> v;
-            v.zero();
-            if (ok && live[i]) v = ring.take(k % P, i);
-#pragma unroll
-            for (int e = 0; e < NP; ++e) x[i][e] = v.pair(e);
+            raw[i].zero();
+            if (ok && live[i]) raw[i] = ring.take(k % P, i);
         }
+        if constexpr (!RX::kAsync) fetch(k + 1);
+        f2 x[NP];
+#pragma unroll
+        for (int e = 0; e < NP; ++e) x[e] = pair_of(raw, e);
         // This warp's mean and sum of squared deviations from it, then the row's
         // from all its warps': sum of (their deviations + n (their mean - mean)^2).
         float mean = 0.f, s = 0.f;
         if (a.center) {
             f2 t = 0ull;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < NP; ++e) t = add2(t, x[i][e]);
+            for (int e = 0; e < NP; ++e) t = add2(t, x[e]);
             s = g.lanes(sum2(t));
             mean = s * own_inv;
         }
         f2 u = 0ull;
-        const f2 minus = pk(-mean, VEC == 1 ? 0.f : -mean);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (live[i])
-#pragma unroll
-                for (int e = 0; e < NP; ++e) {
-                    x[i][e] = add2(x[i][e], minus);
-                    u = fma2(x[i][e], x[i][e], u);
-                }
+        for (int e = 0; e < NP; ++e) {       // (channels a thread does not have stay 0)
+            constexpr int kPer = VEC == 1 ? 1 : VEC / 2;     // pairs of a load
+            const bool l0 = live[VEC == 1 ? 2 * e : e / kPer], l1 = live[VEC == 1 ? 2 * e + 1 : e / kPer];
+            x[e] = add2(x[e], pk(l0 ? -mean : 0.f, l1 ? -mean : 0.f));
+            u = fma2(x[e], x[e], u);
+        }
         float q = g.lanes(sum2(u));
         float shift = 0.f;          // this warp's mean - the row's, still in x
         if (tpr > 32) {
@@ -397,14 +432,12 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
         if (ok) {
             TY* const p = static_cast<TY*>(a.y) + y_at(a, row0 + r);
             const f2 r2 = pk(rstd, rstd), sr = pk(shift * rstd, shift * rstd);
+            f2 v[NP];
+#pragma unroll
+            for (int e = 0; e < NP; ++e) v[e] = fma2(fma2(x[e], r2, sr), w[e], bi[e]);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (live[i]) {
-                    f2 v[NP];
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) v[e] = fma2(fma2(x[i][e], r2, sr), w[i][e], bi[i][e]);
-                    Row<TY, VEC>::store(p + col[i], v);
-                }
+                if (live[i]) store_row<TY, VEC, NV>(p + col[i], i, v);
             if (g.t == 0) {
                 if (a.center) a.mean[row0 + r] = mean;
                 a.rstd[row0 + r] = rstd;
@@ -418,15 +451,17 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
     using RX = Ring<TX, VEC, NV>;
     using RD = Ring<TY, VEC, NV>;
     constexpr int P = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
-    __shared__ __align__(16) float2 buf[2 * kMaxThreads / 32];
+    __shared__ __align__(16) float2 buf[2 * kSums];
+    for (int i = threadIdx.x; i < 2 * kSums; i += blockDim.x) buf[i] = make_float2(0.f, 0.f);
+    __syncthreads();
     extern __shared__ __align__(16) uint8_t ring_mem[];   // the rings; after the rows, [slots][tpr * NV * VEC] sums
     float* const acc = reinterpret_cast<float*>(ring_mem);
     if (threadIdx.x == 0) let_next();
-    RowGroup g(tpr, buf);
+    RowGroup<false> g(tpr, buf);
     RX rx;
     RD rd;
     rx.init(ring_mem);
-    rd.init(ring_mem + (RX::kAsync ? P * RX::kStageBytes * blockDim.x : 0));
+    rd.init(ring_mem + P * RX::kStageBytes * blockDim.x);
     const RowAt x_at(a, a.sx), d_at(a, a.sdy), y_at(a, a.sy);
     const uint32_t slots = blockDim.x / tpr;
     const uint32_t step = gridDim.x * slots;
@@ -461,43 +496,46 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
         }
         ring_commit();
     };
-    for (int k = 0; k < P - 1; ++k) fetch(k);
+    constexpr bool kAsync = RX::kAsync && RD::kAsync;
+    for (int k = 0; k < (kAsync ? P - 1 : 1); ++k) fetch(k);
     stats(0);
-    constexpr int NP = pairs_of(VEC);
-    f2 w[NV][NP], dw[NV][NP], db[NV][NP];
+    constexpr int NP = NV * VEC / 2;
+    f2 w[NP], dw[NP], db[NP];
+    load_params<VEC, NV>(a.weight ? a.weight + static_cast<int64_t>(blockIdx.y) * a.C : nullptr, live, col, 1.f, w);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int e = 0; e < NP; ++e) { w[i][e] = pk(1.f, 1.f); dw[i][e] = 0ull; db[i][e] = 0ull; }
-        if (live[i] && a.weight) load_params<VEC>(a.weight + static_cast<int64_t>(blockIdx.y) * a.C + col[i], w[i]);
-    }
+    for (int e = 0; e < NP; ++e) dw[e] = db[e] = 0ull;
     uint32_t r = first;
     for (uint32_t k = 0; k < rounds; ++k, r += step) {
-        fetch(k + P - 1);
-        ring_wait<P - 1>();
+        if constexpr (kAsync) {
+            fetch(k + P - 1);
+            ring_wait<P - 1>();
+        } else {
+            ring_wait<0>();
+        }
         const bool ok = r < a.rows_per_group;
         const float rstd = nrstd, mr = -nmean * nrstd;
+        Row<TX, VEC> x[NV];
+        Row<TY, VEC> d[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i].zero();
+            d[i].zero();
+            if (ok && live[i]) { x[i] = rx.take(k % P, i); d[i] = rd.take(k % P, i); }
+        }
+        if constexpr (!kAsync) fetch(k + 1);
         stats(k + 1);
-        f2 xh[NV][NP], gr[NV][NP];      // xh and g, kept for dx
+        f2 xh[NP], gr[NP];      // xh and g, kept for dx
         f2 s2 = 0ull, t2 = 0ull;
         const f2 r2 = pk(rstd, rstd), m2 = pk(mr, mr);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            Row<TX, VEC> x;
-            Row<TY, VEC> d;
-            x.zero();
-            d.zero();
-            if (ok && live[i]) { x = rx.take(k % P, i); d = rd.take(k % P, i); }
-#pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                const f2 dy = d.pair(e);
-                xh[i][e] = fma2(x.pair(e), r2, m2);
-                gr[i][e] = mul2(dy, w[i][e]);
-                s2 = add2(s2, gr[i][e]);
-                t2 = fma2(gr[i][e], xh[i][e], t2);
-                dw[i][e] = fma2(dy, xh[i][e], dw[i][e]);
-                db[i][e] = add2(db[i][e], dy);
-            }
+        for (int e = 0; e < NP; ++e) {
+            const f2 dy = pair_of(d, e);
+            xh[e] = fma2(pair_of(x, e), r2, m2);
+            gr[e] = mul2(dy, w[e]);
+            s2 = add2(s2, gr[e]);
+            t2 = fma2(gr[e], xh[e], t2);
+            dw[e] = fma2(dy, xh[e], dw[e]);
+            db[e] = add2(db[e], dy);
         }
         float sg, st;
         if (tpr > 32) {
@@ -512,46 +550,37 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
         if (ok) {
             TX* const p = static_cast<TX*>(a.y) + y_at(a, row0 + r);
             const f2 c1 = pk(n1, n1), c2 = pk(n2, n2);
+            f2 v[NP];
+#pragma unroll
+            for (int e = 0; e < NP; ++e) v[e] = fma2(gr[e], r2, fma2(xh[e], c2, c1));
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (live[i]) {
-                    f2 v[NP];
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) v[e] = fma2(gr[i][e], r2, fma2(xh[i][e], c2, c1));
-                    Row<TX, VEC>::store(p + col[i], v);
-                }
+                if (live[i]) store_row<TX, VEC, NV>(p + col[i], i, v);
         }
     }
     ring_wait<0>();
     // The block's sums: row slots added in order, then one partial per block
     // (the gradient itself when the group has one block).
     const int width = tpr * NV * VEC;
-    auto leave = [&](f2 (&v)[NV][NP], float* part, float* grad) {
+    auto leave = [&](f2 (&v)[NP], float* part, float* grad) {
         float* const out = gridDim.x == 1 ? grad + static_cast<int64_t>(blockIdx.y) * a.C
                                           : part + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * a.C;
+        float f[2 * NP];
+#pragma unroll
+        for (int e = 0; e < NP; ++e) unpk(v[e], f[2 * e], f[2 * e + 1]);
         if (slots == 1) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live[i])
 #pragma unroll
-                    for (int e = 0; e < NP; ++e) {
-                        float lo, hi;
-                        unpk(v[i][e], lo, hi);
-                        out[col[i] + 2 * e] = lo;
-                        if (VEC > 1) out[col[i] + 2 * e + 1] = hi;
-                    }
+                    for (int e = 0; e < VEC; ++e) out[col[i] + e] = f[i * VEC + e];
             return;
         }
         __syncthreads();     // the rings (or the last sums) have been read
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                float lo, hi;
-                unpk(v[i][e], lo, hi);
-                acc[g.id * width + col[i] + 2 * e] = lo;
-                if (VEC > 1) acc[g.id * width + col[i] + 2 * e + 1] = hi;
-            }
+            for (int e = 0; e < VEC; ++e) acc[g.id * width + col[i] + e] = f[i * VEC + e];
         __syncthreads();
         for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
             float t = 0.f;
@@ -590,7 +619,7 @@ __global__ void __launch_bounds__(1024) layer_norm_param_sum_kernel(const NormAr
 template <typename TX, typename TY, int VEC, int NV>
 cudaError_t fwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
     using RX = Ring<TX, VEC, NV>;
-    const int smem = RX::kAsync ? ring_depth(RX::kStageBytes, true) * RX::kStageBytes * p.threads : 0;
+    const int smem = ring_depth(RX::kStageBytes, RX::kAsync) * RX::kStageBytes * p.threads;
     auto kern = layer_norm_fwd_kernel<TX, TY, VEC, NV>;
     if (smem > 47 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -605,7 +634,7 @@ cudaError_t bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
     using RX = Ring<TX, VEC, NV>;
     using RD = Ring<TY, VEC, NV>;
     const int depth = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
-    const int rings = ((RX::kAsync ? RX::kStageBytes : 0) + (RD::kAsync ? RD::kStageBytes : 0)) * depth * p.threads;
+    const int rings = (RX::kStageBytes + RD::kStageBytes) * depth * p.threads;
     const int sums = p.threads > p.tpr ? p.threads * NV * VEC * static_cast<int>(sizeof(float)) : 0;
     const int smem = rings > sums ? rings : sums;
     auto kern = layer_norm_bwd_kernel<TX, TY, VEC, NV>;
@@ -623,12 +652,13 @@ cudaError_t bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
 template <typename TX, typename TY, bool BWD>
 cudaError_t pick(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
 #define DIT_NORM_CASE(V, N) \
-    if (p.vec == V && p.nv == N) return BWD ? bwd<TX, TY, V, N>(a, p, s) : fwd<TX, TY, V, N>(a, p, s);
+    if (p.vec == V && p.nv == N) {                                                                 \
+        if constexpr (BWD) return bwd<TX, TY, V, N>(a, p, s);                                      \
+        else return fwd<TX, TY, V, N>(a, p, s);                                                    \
+    }
     DIT_NORM_CASE(8, 1)
     DIT_NORM_CASE(8, 2)
-    if constexpr (!BWD) {
-        DIT_NORM_CASE(8, 4)
-    }
+    if constexpr (!BWD) DIT_NORM_CASE(8, 4)
     DIT_NORM_CASE(2, 4)
     DIT_NORM_CASE(2, 8)
     DIT_NORM_CASE(1, 8)
@@ -647,28 +677,38 @@ cudaError_t pick_types(const NormArgs& a, const NormPlan& p, bool x_f32, bool y_
 
 // Channels a thread: forward 32 (16 without 16-byte loads), so that a row of
 // 4,096 is four warps' and one of 1,024 a single warp's, without a barrier:
-// 70 us for 24,576 x 4,096 bf16 against 101 with 16 a thread and 167 with 8; halved
-// while rows are so few that the SMs would not get 512 threads each.  Backward
-// 16: its sums over rows hold two registers a channel (120 us there; 32 spill).
-// 512 threads an SM either way: forward in blocks of 128 (a row's threads when
-// those are more), backward in one block, which leaves one partial (1,024 threads
-// an SM measured 127 us, for its partials).
+// 69 us for 24,576 x 4,096 bf16 against 101 with 16 a thread and 167 with 8;
+// halved while rows are so few that the SMs would not get 512 threads each.
+// Backward 16: its sums over rows hold two registers a channel (113 us there; 32
+// spill), and 8 where rows are read channel by channel (24,576 x 4,095: 240 us
+// against 550, whose prefetched row spills).
+// A row's threads are whole warps and not a power of two: 24,576 x 2,560 takes
+// 56 and 76 us (floor 37 and 56) against 61 and 101 with 128 and 256 threads.
+// 512 threads an SM either way: forward in blocks of up to 128 (a row's threads
+// when those are more), backward in one block, which leaves one partial (1,024
+// threads an SM measured 127 us, for its partials).  Above 4,096 channels the
+// backward pass has one row at a time on an SM and is bound by its chain of sums:
+// 195 us for 24,576 x 5,120 (floor 111); 640 threads of 8 channels took 205.
 NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max, int sms, bool backward) {
     NormPlan p;
     p.vec = vec_max;
     int per = backward || vec_max < 8 ? 16 : 32;
+    if (backward && vec_max == 1 && C <= 8 * kMaxThreads) per = 8;
     const uint64_t rows = static_cast<uint64_t>(groups) * rows_per_group;
     while (per > 8 && rows * ((C + per - 1) / per) < static_cast<uint64_t>(sms) * 512 && C <= per / 2 * kMaxThreads) per /= 2;
     p.nv = per / p.vec;
-    p.tpr = 1;
-    while (p.tpr * per < C) p.tpr *= 2;
-    p.threads = backward ? kMaxThreads : 128;
-    if (p.threads < p.tpr) p.threads = p.tpr;
-    // never more row slots than rows
-    while (p.threads > 32 && p.threads > p.tpr && static_cast<uint32_t>(p.threads / p.tpr) > rows_per_group) p.threads /= 2;
-    const uint32_t slots = static_cast<uint32_t>(p.threads / p.tpr);
+    const int need_threads = (C + per - 1) / per;
+    p.tpr = (need_threads + 31) / 32 * 32;
+    if (need_threads <= 32)
+        for (p.tpr = 1; p.tpr < need_threads;) p.tpr *= 2;
+    // never more row slots than rows, but whole warps
+    uint32_t slots = static_cast<uint32_t>((backward ? kMaxThreads : 128) / p.tpr);
+    if (slots > rows_per_group) slots = rows_per_group;
+    if (slots < 1) slots = 1;
+    p.threads = (static_cast<int>(slots) * p.tpr + 31) / 32 * 32;
+    slots = static_cast<uint32_t>(p.threads / p.tpr);
     const uint64_t need = (rows_per_group + slots - 1) / slots;
-    uint64_t blocks = (static_cast<uint64_t>(sms) * 512 / p.threads + groups - 1) / groups;
+    uint64_t blocks = (static_cast<uint64_t>(sms) * (512 / p.threads) + groups - 1) / groups;
     if (blocks > need) blocks = need;
     p.blocks = static_cast<int>(blocks < 1 ? 1 : blocks);
     return p;
