@@ -196,8 +196,9 @@ struct Item {
 
 // Items count pieces fastest, then tiles, then heads, so that the CTAs at work
 // share a few heads' tiles in L2; with a mask heads before tiles, since masks
-// tend to load some tiles of every head (the first frame's, the first keys')
-// more than others, and those then begin together.
+// tend to load some tiles of every head more than others, and those then begin
+// together: key items from the first (the keys that all rows attend), query
+// items from the last (rows behind the masked ones, late rows of a causal mask).
 template <bool KEY, bool MASK>
 __device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int id) {
     Item<KEY> it;
@@ -208,7 +209,7 @@ __device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int id) {
     const uint32_t item = (KEY ? a.div_f_kv : a.div_f_q).divmod(static_cast<uint32_t>(slot), piece);
     const uint32_t outer = (MASK ? a.div_bh : (KEY ? a.div_kv_tiles : a.div_q_tiles)).divmod(item, inner);
     const uint32_t bh = MASK ? inner : outer;
-    it.fixed = static_cast<int>(MASK ? outer : inner);
+    it.fixed = static_cast<int>(!MASK ? inner : KEY ? outer : tiles - 1 - outer);
     it.b = static_cast<int>(a.div_h.divmod(bh, h));
     it.h = static_cast<int>(h);
     it.part_tile = (static_cast<int64_t>(bh) * tiles + it.fixed) * f + piece;
