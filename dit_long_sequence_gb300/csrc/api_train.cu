@@ -470,12 +470,13 @@ dit_status_t dit_rope(const void* x, dit_dtype_t dtype, const dit_strides4_t* x_
     a.inverse = inverse != 0;
     // The widest unit every pointer, stride and part of the head allows.
     const bool half = layout == DIT_ROPE_HALF;
-    int vec = 16 / static_cast<int>(size_of(dtype));
-    for (; vec > 1; vec /= 2) {
-        const bool ok = on(x, vec * size_of(dtype)) && on(y, vec * size_of(dtype)) && multiple(*x_strides, vec) &&
-                        multiple(*y_strides, vec) && D % vec == 0 && (!half || pairs % vec == 0);
-        if (ok) break;
-    }
+    const int full = 16 / static_cast<int>(size_of(dtype));
+    auto fits = [&](int v) {
+        return on(x, v * size_of(dtype)) && on(y, v * size_of(dtype)) && multiple(*x_strides, v) && multiple(*y_strides, v) && D % v == 0;
+    };
+    a.wide = fits(full);
+    int vec = full;
+    while (vec > 1 && !(fits(vec) && (!half || pairs % vec == 0))) vec /= 2;
     // one channel at a time: the half layout's kernel serves both, by where a pair's two channels lie
     a.lone_step = half ? 1 : 2;
     a.lone_partner = half ? pairs : 1;

@@ -41,6 +41,7 @@ constexpr int kMaxAngles = 2048;        // angles a block holds, cos and sin in 
 // The launch's index arithmetic.
 struct RopeGrid {
     int units, rot_units;           // units of a head, those that rotate
+    int wide_from, wide_at;         // copy units from this one on take 16 bytes, the first at this channel
     int step_u, step_h, step_n;     // kThreads units further
     int tokens, blocks_per_b, stride;
     FastDiv div_units, div_h, div_pairs;
@@ -117,13 +118,18 @@ struct Pack {
 // One unit of work is VEC channels (interleaved: whole pairs, VEC >= 2, the
 // pairs past the rotated ones passing through) or VEC pairs of the half layout
 // (VEC channels of the first half and their partners), or VEC channels to copy.
-// With VEC = 1 the HALF form takes single pairs of either layout.  A thread's
+// With VEC = 1 the HALF form takes single pairs of either layout.  Where the
+// half layout's pairs are no multiple of 16 bytes but the heads are, its copy
+// units are (13 pairs of 128 channels, 9,000 tokens x 32 heads: 47 us, with
+// single-channel copies 109).  A thread's
 // units are kThreads apart in (token, head, unit) order, so it steps from one to
 // the next with additions (`step`) instead of dividing.
 template <typename T, bool HALF, int VEC>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, const RopeGrid gr) {
     // units in flight per thread: a half-layout unit is two loads
     constexpr int kUnroll = unroll(HALF);
+    constexpr int kFull = 16 / static_cast<int>(sizeof(T));
+    constexpr bool kWide = HALF && VEC < kFull;
     extern __shared__ __align__(16) float angles[];     // cos [tokens][stride], then sin
     float* const cosv = angles;
     float* const sinv = angles + gr.tokens * gr.stride;
@@ -136,6 +142,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
     struct At { int n, h, u; };
     auto channel = [&](int u) {     // a half-layout copy unit starts behind both halves
+        if (kWide && u >= gr.wide_from) return gr.wide_at + (u - gr.wide_from) * kFull;
         return (!HALF || u < gr.rot_units) ? u * (VEC == 1 ? a.lone_step : VEC) : 2 * a.pairs + (u - gr.rot_units) * VEC;
     };
     auto advance = [&](At& t) {
@@ -146,6 +153,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         if (t.h >= a.H) { t.h -= a.H; ++t.n; }
     };
     Pack<T, VEC> p[kUnroll], q[kUnroll];
+    Pack<T, kFull> full[kUnroll];   // (kWide)
     At next;                        // the unit to load
     {
         const uint32_t nh = gr.div_units.div(threadIdx.x);
@@ -159,8 +167,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         for (int k = 0; k < kUnroll; ++k) {
             if (next.n < nt) {
                 const T* s = x + (next.n * a.sx.n + next.h * a.sx.h + channel(next.u));
-                p[k].load(s);
-                if (HALF && next.u < gr.rot_units) q[k].load(s + partner);
+                if (kWide && next.u >= gr.wide_from) {
+                    full[k].load(s);
+                } else {
+                    p[k].load(s);
+                    if (HALF && next.u < gr.rot_units) q[k].load(s + partner);
+                }
             }
             advance(next);
         }
@@ -230,7 +242,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     }
                     p[k].put_all(lo);
                 }
-                p[k].store(d);
+                if (kWide && cur.u >= gr.wide_from) full[k].store(d);
+                else p[k].store(d);
             }
             advance(cur);
         }
@@ -243,8 +256,16 @@ cudaError_t launch_vec(const RopeArgs& a, cudaStream_t s) {
     // Units of one head: interleaved ceil(2 pairs / VEC) that rotate (the last may
     // hold pass-through pairs) then copies; half layout pairs / VEC and copies.
     const int rot = HALF ? a.pairs / VEC : (2 * a.pairs + VEC - 1) / VEC;
-    const int units = HALF ? rot + (a.D - 2 * a.pairs) / VEC : a.D / VEC;
+    constexpr int kFull = 16 / static_cast<int>(sizeof(T));
+    int units = HALF ? rot + (a.D - 2 * a.pairs) / VEC : a.D / VEC;
     RopeGrid g;
+    g.wide_from = units;
+    g.wide_at = 0;
+    if (HALF && VEC < kFull && a.wide) {
+        g.wide_at = (2 * a.pairs + kFull - 1) / kFull * kFull;
+        g.wide_from = rot + (g.wide_at - 2 * a.pairs) / VEC;
+        units = g.wide_from + (a.D - g.wide_at) / kFull;
+    }
     g.units = units;
     g.rot_units = rot;
     g.div_units = FastDiv(units);

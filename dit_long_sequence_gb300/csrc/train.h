@@ -107,6 +107,7 @@ struct RopeArgs {
     int64_t offset;
     float mscale;
     bool inverse;
+    bool wide;                         // 16-byte copies are aligned wherever a head's channel is a multiple of them
     int lone_step, lone_partner;       // one-channel units: channel of pair i = i * step, its partner's distance
     uint8_t axis_end[kRopeMaxAxes];    // first pair past axis a
     uint64_t turns[kRopeMaxPairs];     // 2^64 * (inv_freq / 2 pi mod 1)
