@@ -42,6 +42,10 @@ bool multiple(const dit_strides4_t& s, int64_t k) { return s.b % k == 0 && s.n %
 bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool known(dit_dtype_t t) { return t == DIT_BF16 || t == DIT_F32; }
 uintptr_t size_of(dit_dtype_t t) { return t == DIT_F32 ? 4 : 2; }
+// Two views that begin at one address place every row alike.
+bool same_rows(const dit_strides4_t& s, const dit_strides4_t& t, int B, int N, int H) {
+    return (B == 1 || s.b == t.b) && (N == 1 || s.n == t.n) && (H == 1 || s.h == t.h);
+}
 
 struct BwdMask {
     const uint32_t* bits;
@@ -92,6 +96,15 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
         if (!multiple(st->o, out_dtype == DIT_F32 ? 4 : 8)) return DIT_ERR_ALIGNMENT;
         if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(out)) return DIT_ERR_ALIGNMENT;
         if (!on(lse, 4) || !on(dlse, 4)) return DIT_ERR_ALIGNMENT;
+    }
+    // (views may interleave, so of the forbidden overlaps only a shared base is refused)
+    const void* const grads[3] = {Nq > 0 ? dq : nullptr, Nkv > 0 ? dk : nullptr, Nkv > 0 ? dv : nullptr};
+    for (int i = 0; i < 3; ++i) {
+        if (grads[i] == nullptr) continue;
+        for (int j = 0; j < i; ++j)
+            if (grads[i] == grads[j]) return DIT_ERR_INVALID_ARG;
+        for (const void* in : {q, k, v, out, dout, static_cast<const void*>(lse), static_cast<const void*>(dlse), static_cast<const void*>(workspace)})
+            if (any_keys && grads[i] == in) return DIT_ERR_INVALID_ARG;
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DIT_ERR_CUDA;
@@ -295,6 +308,7 @@ dit_status_t dit_layer_norm_fwd(const void* x, dit_dtype_t x_dtype, const dit_st
     if ((e = check_out_strides(*y_strides, B, N, H)) != DIT_OK) return e;
     if (!on(x, size_of(x_dtype)) || !on(y, size_of(y_dtype)) || !on(weight, 4) || !on(bias, 4) || !on(mean, 4) || !on(rstd, 4))
         return DIT_ERR_ALIGNMENT;
+    if (x == y && (x_dtype != y_dtype || !same_rows(*x_strides, *y_strides, B, N, H))) return DIT_ERR_INVALID_ARG;
     if ((e = check_placement({x, y, weight, bias, center ? mean : nullptr, rstd}, stream)) != DIT_OK) return e;
     NormArgs a{};
     norm_fill(a, B, N, H, C, param_batches, center != 0);
@@ -324,8 +338,9 @@ size_t dit_layer_norm_bwd_workspace_bytes(int B, int N, int H, int C, int param_
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     const uint32_t rows = static_cast<uint32_t>(B) * static_cast<uint32_t>(N) * static_cast<uint32_t>(H);
     const uint32_t groups = static_cast<uint32_t>(param_batches);
-    const NormPlan p = norm_plan(C, groups, rows / groups, 1, device_sm_count(dev), true);   // blocks do not depend on vec
-    return p.blocks > 1 ? static_cast<size_t>(2) * groups * p.blocks * C * sizeof(float) : 0;
+    int blocks = 1;      // of whichever plan the pointers' alignment will allow
+    for (int vec : {8, 2, 1}) blocks = std::max(blocks, norm_plan(C, groups, rows / groups, vec, device_sm_count(dev), true).blocks);
+    return blocks > 1 ? static_cast<size_t>(2) * groups * blocks * C * sizeof(float) : 0;
 }
 
 dit_status_t dit_layer_norm_bwd(const void* dy, dit_dtype_t dy_dtype, const dit_strides4_t* dy_strides, const void* x,
@@ -352,6 +367,10 @@ dit_status_t dit_layer_norm_bwd(const void* dy, dit_dtype_t dy_dtype, const dit_
     if (!on(x, size_of(x_dtype)) || !on(dx, size_of(x_dtype)) || !on(dy, size_of(dy_dtype)) || !on(weight, 4) ||
         !on(mean, 4) || !on(rstd, 4) || !on(dweight, 4) || !on(dbias, 4))
         return DIT_ERR_ALIGNMENT;
+    if ((dx == x && !same_rows(*dx_strides, *x_strides, B, N, H)) ||
+        (dx == dy && (x_dtype != dy_dtype || !same_rows(*dx_strides, *dy_strides, B, N, H))) ||
+        (dweight != nullptr && dweight == dbias))
+        return DIT_ERR_INVALID_ARG;
     const bool wants = dweight != nullptr || dbias != nullptr;
     const size_t need = wants ? dit_layer_norm_bwd_workspace_bytes(B, N, H, C, param_batches) : 0;
     if (need > 0) {
@@ -452,6 +471,7 @@ dit_status_t dit_rope(const void* x, dit_dtype_t dtype, const dit_strides4_t* x_
     if ((e = check_in_strides(*x_strides)) != DIT_OK) return e;
     if ((e = check_out_strides(*y_strides, B, N, H)) != DIT_OK) return e;
     if (!on(x, size_of(dtype)) || !on(y, size_of(dtype)) || !on(positions, 4)) return DIT_ERR_ALIGNMENT;
+    if (x == y && !same_rows(*x_strides, *y_strides, B, N, H)) return DIT_ERR_INVALID_ARG;
     if ((e = check_placement({x, y, positions}, stream)) != DIT_OK) return e;
     a.x = x;
     a.y = y;

@@ -487,7 +487,8 @@ dit_status_t dit_attn_fwd_fp8_ws(const void *q, const void *k, const void *v,
  * dlse      fp32 [B, H, Nq] contiguous gradient of the LSE, or NULL (zero).
  * dq, dk, dv  gradients, grad_dtype, strides->dq / dk / dv: d contiguous, other
  *           strides 16-byte multiples, no two rows at one place.  They must not
- *           overlap one another or any input.  Rows j >= key_valid_len of dk and
+ *           overlap one another, any input or the workspace (a shared first
+ *           address is DIT_ERR_INVALID_ARG).  Rows j >= key_valid_len of dk and
  *           dv are written as zeros; those rows of k and v are never read.
  * A row with lse = -inf (no allowed key) contributes nothing.  All q, k, v and
  * dout that are read must be finite: 0 * inf is NaN in the products.
@@ -556,7 +557,8 @@ size_t dit_attn_bwd_workspace_bytes(int B, int Nq, int Nkv, int H, int D, int ke
  *           fp32 -> fp32 and fp32 -> bf16; bf16 -> fp32 is DIT_ERR_UNSUPPORTED.
  *           Any C, alignment and stride work; 8 channels are moved at a time when
  *           C and the strides are multiples of 8 and the pointers 16-byte
- *           aligned.  y may be x (same type and strides).
+ *           aligned.  y may be x in the same type and strides (otherwise a shared
+ *           first address is DIT_ERR_INVALID_ARG).
  * weight, bias  fp32 [param_batches, C] contiguous, or NULL (1 and 0);
  *           param_batches is 1 or B (one set per batch entry: modulation).
  * center    0: the mean is taken as 0 (RMS norm) and `mean` is not written.
@@ -579,7 +581,8 @@ dit_status_t dit_layer_norm_fwd(const void *x, dit_dtype_t x_dtype, const dit_st
  *   dweight = sum over the rows of a parameter set of dy * xh,  dbias = of dy.
  *
  * dy        dy_dtype (the forward's y_dtype), dx x_dtype; strides as x and y there.
- *           dx may be x or, in one type, dy (same strides).
+ *           dx may be x or, in one type, dy, with the same strides (otherwise a
+ *           shared first address is DIT_ERR_INVALID_ARG).
  * dweight, dbias  fp32 [param_batches, C] contiguous, either may be NULL (not formed).
  *           They are overwritten; with no rows they are zeros.
  * workspace device memory of dit_layer_norm_bwd_workspace_bytes, 16-byte aligned
@@ -610,9 +613,10 @@ typedef enum { DIT_ROPE_INTERLEAVED = 0, DIT_ROPE_HALF = 1 } dit_rope_layout_t;
  *
  * x, y      dtype, element (b, n, h, d) through their strides (s.d = 1; x strides
  *           >= 0, y rows distinct); q and k of a stacked [B, N, 3, H, D]
- *           projection are one call with 2 H heads.  y may be x (same strides).
+ *           projection are one call with 2 H heads.  y may be x with the same
+ *           strides (otherwise a shared first address is DIT_ERR_INVALID_ARG).
  *           Any alignment works; 16 bytes are moved at a time where pointers,
- *           strides, D and (half layout) rotary_dim / 2 allow.
+ *           strides, D and (half layout, turning channels) rotary_dim / 2 allow.
  * rotary_dim  even, 2 to min(D, 256); D at most 1024, H at most 65,535.
  * inv_freq  HOST array [rotary_dim / 2], fp64, read during the call; finite.
  * axis_pairs  HOST array [n_axes], n_axes 1 to 4: how many of the pairs, in

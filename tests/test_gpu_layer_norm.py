@@ -69,6 +69,13 @@ def test_forward_and_backward(dl, B, N, H, C, tx, ty, center, per_batch, strided
     assert all(torch.equal(s, t) for s, t in zip((dx, dw, db), again))
 
 
+@pytest.mark.parametrize("tx,ty", [(BF, BF), (F, BF)])
+@pytest.mark.parametrize("N,C", [(2500, 1152), (1300, 1501), (1200, 2560), (900, 1538), (300, 5120), (400, 6150), (170, 7001)])
+def test_rows_of_three_to_fifteen_warps(dl, N, C, tx, ty):
+    """Numbers of warps that are no power of two, in blocks of one to five rows."""
+    test_forward_and_backward(dl, 1, N, 1, C, tx, ty, True, False, False)
+
+
 def test_three_dimensions_and_no_parameters(dl):
     x, g = _data(2, 11, 1, 96, BF, 5, False)
     x = x[:, :, 0]
