@@ -568,6 +568,20 @@ def attn_bwd_workspace_bytes(B: int, Nq: int, Nkv: int, H: int, D: int, key_vali
                                                  1 if masked else 0))
 
 
+def _workspace_for(stream, nbytes: int) -> torch.Tensor:
+    """A call's own workspace on a stream that was given: of that stream's
+    memory, so that freeing it behind the call does not hand it to another
+    stream's work while the kernels run."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream.cuda_stream)):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def _attn_bwd_workspace_for(stream, q, k, key_valid_len, masked):
+    (B, Nq, H, D), Nkv = q.shape, k.shape[1]
+    return _workspace_for(stream, attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, Nkv if key_valid_len is None else key_valid_len,
+                                                           masked))
+
+
 def _is_fp32(dtype: torch.dtype) -> bool:
     if dtype is torch.float32:
         return True
@@ -589,6 +603,8 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     that of lse.  dq [B, Nq, H, D], dk and dv [B, Nkv, H, D] may be given (e.g.
     views of one fused [B, N, 3, H, D] gradient) or are allocated in grad_dtype;
     keys past key_valid_len get zeros.  Returns (dq, dk, dv)."""
+    if stream is not None and workspace is None:
+        workspace = _attn_bwd_workspace_for(stream, q, k, key_valid_len, False)
     rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv,
                                  _is_fp32(grad_dtype), workspace, _stream_ptr(stream))
     if rc != DIT_OK:
@@ -605,6 +621,8 @@ def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
     the forward call's mask_bits and mask_rows."""
     if mask_bits is None:
         raise ValueError("mask_bits is missing")
+    if stream is not None and workspace is None:
+        workspace = _attn_bwd_workspace_for(stream, q, k, key_valid_len, True)
     rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
                                  _is_fp32(grad_dtype), workspace, _stream_ptr(stream))
     if rc != DIT_OK:
@@ -645,6 +663,10 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor | None,
     in the forward call.  Returns (dx, dweight, dbias): dx in x's type; dweight
     and dbias fp32 in weight's shape, None without a weight (dbias also without
     has_bias) unless a tensor to fill is given."""
+    if stream is not None and workspace is None:
+        B, N, H, C = x.shape if x.dim() == 4 else (x.shape[0], x.shape[1], 1, x.shape[-1])
+        sets = B if any(t is not None and t.dim() == 2 for t in (weight, dweight, dbias)) else 1
+        workspace = _workspace_for(stream, layer_norm_bwd_workspace_bytes(B, N, H, C, sets))
     rc, dx, dw, db = _calls.norm_bwd(dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace,
                                      _stream_ptr(stream))
     if rc != DIT_OK:
