@@ -7,7 +7,7 @@
 
 namespace dit {
 
-// A tile pair costs a key CTA four products and a query CTA three.  With the
+// A tile pair costs a key item four products and a query item three.  With the
 // whole grid's cost spread evenly over the SMs, an item longer than that even
 // share is cut into pieces of about that length (at least kMinPieceTiles
 // streamed tiles, at most kMaxPieces); a grid of many items is not cut.
