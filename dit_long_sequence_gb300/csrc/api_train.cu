@@ -189,12 +189,12 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
         s.counter = a.counter = reinterpret_cast<unsigned int*>(ws + p.stat_bytes - 256);    // behind the statistics
         a.part_kv = reinterpret_cast<float*>(ws + p.stat_bytes);
         a.part_q = reinterpret_cast<float*>(ws + p.stat_bytes + p.part_kv_bytes);
+        OccArgs o{};
         if (with_mask) {
             a.mask = mask->bits;
             a.mask_sb = mask->batch_stride;
             a.mask_si = mask->row_stride;
             a.mask_rows = mask->rows;
-            OccArgs o{};
             o.mask = mask->bits;
             o.mask_sb = mask->batch_stride;
             o.mask_si = mask->row_stride;
@@ -209,9 +209,9 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
             a.occ = o.occ;
             a.occ_words = o.occ_words;
             a.occ_blocks = o.row_blocks;
-            if (launch_mask_occupancy(o, cs) != cudaSuccess) return DIT_ERR_CUDA;
         }
         if (launch_attn_bwd_stat(s, D, out_dtype == DIT_BF16, cs) != cudaSuccess) return DIT_ERR_CUDA;
+        if (with_mask && launch_mask_occupancy_behind(o, cs) != cudaSuccess) return DIT_ERR_CUDA;
     }
     if (launch_attn_bwd(tq, tk, tv, tdo, a, D, grad_bf16, cs) != cudaSuccess) return DIT_ERR_CUDA;
     return launch_attn_bwd_sum(a, D, grad_bf16, cs) == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;

@@ -666,6 +666,9 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
             const int tile = tile_next;
             const int st = J % C::kStats;
             const uint2 mw = mw_next;
+            // Most tiles of a mask that is made of blocks forbid nothing: those pass
+            // without the tests of single bits.
+            const bool some = MASK && !__all_sync(0xffffffffu, (mw.x & mw.y) == ~0u);
             tile_next = stream.next();
             mw_next = word_of(tile_next);
             ok = kDouble ? wait(C::kT0Full + (J & 1), turn(J, 2), SITE_T0_FULL) : wait(C::kT0Full, J & 1, SITE_T0_FULL);
@@ -698,7 +701,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) q[c] = ex2_approx(q[c]);
-                if constexpr (MASK && KEY) {
+                if (MASK && KEY && some) {
                     const uint32_t held = hf ? mw.y : mw.x;
                     const int row4 = lane >> 2, col = 2 * (lane & 3);
 #pragma unroll
@@ -712,7 +715,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
                         }
                     }
                 }
-                if constexpr (MASK && !KEY) {
+                if (MASK && !KEY && some) {
                     const uint32_t w = hf ? mw.y : mw.x;
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -929,19 +932,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // stat[b*H + h][0][i] = -lse * log2(e) (-inf for rows without a key and rows
 // past Nq, so that their P is 0), [1][i] = dlse - sum_d dO O.  One row per
-// D / 8 lanes, 16 bytes of dO each; HBM-bound (reads dO and O once).
+// D / 8 lanes, 16 bytes of dO each; a block's 2,048 / D rows are of one (b, h),
+// which divides a head's padded rows.  HBM-bound (reads dO and O once).
 template <int D, bool OUT_BF16>
 __global__ void __launch_bounds__(256) attn_bwd_stat_kernel(const AttnBwdStatArgs a) {
-    constexpr int LPR = D / 8;
-    const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    constexpr int LPR = D / 8, kRows = 256 / LPR;
+    static_assert(kT % kRows == 0, "rows of a block");
     if (threadIdx.x == 0) let_next();
-    if (g == 0) *a.counter = 0u;      // of the main kernel's items
-    const int64_t unit = g / LPR;
-    const int c = static_cast<int>(g % LPR);
-    const int64_t bh = unit / a.rows_pad;
-    const int i = static_cast<int>(unit % a.rows_pad);
-    if (bh >= static_cast<int64_t>(a.B) * a.H) return;     // a whole row's lanes (256 is a multiple of LPR)
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0u;      // of the main kernel's items
+    const int per_bh = a.rows_pad / kRows;
+    const unsigned unit = blockIdx.x / static_cast<unsigned>(per_bh);
+    const int64_t bh = unit;
+    const int c = static_cast<int>(threadIdx.x % LPR);
+    const int i = static_cast<int>(blockIdx.x - unit * per_bh) * kRows + static_cast<int>(threadIdx.x / LPR);
+    const int b = static_cast<int>(unit / static_cast<unsigned>(a.H)), h = static_cast<int>(unit - b * static_cast<unsigned>(a.H));
     float s = 0.f, nl = -INFINITY;
     if (i < a.Nq) {
         const int64_t od = b * a.sdo.b + static_cast<int64_t>(i) * a.sdo.n + h * a.sdo.h + 8 * c;
@@ -1028,8 +1032,7 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 }  // namespace
 
 cudaError_t launch_attn_bwd_stat(const AttnBwdStatArgs& a, int D, bool out_bf16, cudaStream_t s) {
-    const int64_t threads = static_cast<int64_t>(a.B) * a.H * a.rows_pad * (D / 8);
-    const unsigned blocks = static_cast<unsigned>((threads + 255) / 256);
+    const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H * (a.rows_pad / (2048 / D)));
     if (D == 128) {
         if (out_bf16) attn_bwd_stat_kernel<128, true><<<blocks, 256, 0, s>>>(a);
         else attn_bwd_stat_kernel<128, false><<<blocks, 256, 0, s>>>(a);

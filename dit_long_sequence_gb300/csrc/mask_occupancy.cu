@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "train.h"
 
 namespace dit {
 namespace {
@@ -27,6 +28,7 @@ constexpr int kWarps = kThreads / 32;
 
 __global__ void __launch_bounds__(kThreads) mask_occupancy_kernel(const OccArgs a) {
     __shared__ uint32_t words[kWarps];
+    if (threadIdx.x == 0) let_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = blockIdx.x;
     const int g = static_cast<int>(unit % a.occ_words);
@@ -63,9 +65,19 @@ __global__ void __launch_bounds__(kThreads) mask_occupancy_kernel(const OccArgs 
         for (int w = 0; w < kWarps; ++w) all |= words[w];
         a.occ[(static_cast<int64_t>(b) * a.row_blocks + rb) * a.occ_words + g] = all;
     }
+    // Launched behind another kernel, this one ends after it: who waits for this
+    // one has then waited for both.
+    after_previous();
 }
 
 }  // namespace
+
+cudaError_t launch_mask_occupancy_behind(const OccArgs& a, cudaStream_t stream) {
+    const int64_t units = static_cast<int64_t>(a.B) * a.row_blocks * a.occ_words;
+    if (units <= 0) return cudaSuccess;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_behind(mask_occupancy_kernel, dim3(static_cast<unsigned>(units)), dim3(kThreads), 0, stream, a);
+}
 
 cudaError_t launch_mask_occupancy(const OccArgs& a, cudaStream_t stream) {
     const int64_t units = static_cast<int64_t>(a.B) * a.row_blocks * a.occ_words;

@@ -117,6 +117,11 @@ cudaError_t launch_rope(const RopeArgs& a, bool f32, bool half, int vec, cudaStr
 
 // ------------------------------------------------------------ attention backward
 
+struct OccArgs;      // of the mask's occupancy pre-pass
+// launch_mask_occupancy beside the kernel before it on the stream: neither needs
+// the other, and whoever waits for this one waits for both.
+cudaError_t launch_mask_occupancy_behind(const OccArgs& a, cudaStream_t stream);
+
 struct AttnBwdArgs {
     int B, Nq, Nkv, H, kv_len;
     int q_tiles, kv_tiles;      // ceil(Nq / 128), ceil(kv_len / 128)
