@@ -108,8 +108,12 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DIT_ERR_CUDA;
-    const BwdPlan p = plan_attn_bwd(B, Nq, Nkv, H, D, any_keys ? key_valid_len : 0, device_sm_count(dev));
+    BwdPlan p = plan_attn_bwd(B, Nq, Nkv, H, D, any_keys ? key_valid_len : 0, device_sm_count(dev));
     const bool with_mask = mask != nullptr && mask->rows > 0 && any_keys;
+    if (with_mask && p.q_whole > 0) {      // items of unknown lengths: none of the last ones is cut
+        p.q_whole = p.query_items;
+        p.f_q = 1;
+    }
     // Items and partial tiles are counted in 32-bit ints on the device.
     if (p.key_items * p.f_kv + p.query_items * p.f_q > 0x7ffffff0LL - device_sm_count(dev) ||
         static_cast<int64_t>(B) * H * 128 * (p.q_tiles > p.kv_out_tiles ? p.q_tiles : p.kv_out_tiles) > (int64_t(1) << 37))
@@ -156,8 +160,9 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     a.sdv = st->dv;
     a.f_kv = p.f_kv;
     a.f_q = p.f_q;
+    a.q_whole = static_cast<int>(p.q_whole);
     a.n_kv_items = static_cast<int>(p.key_items * p.f_kv);
-    a.n_q_items = static_cast<int>(p.query_items * p.f_q);
+    a.n_q_items = static_cast<int>(p.q_whole + (p.query_items - p.q_whole) * p.f_q);
     auto div = [](int64_t d) { return FastDiv(static_cast<uint32_t>(d > 0 ? d : 1)); };
     a.div_f_kv = div(p.f_kv);
     a.div_f_q = div(p.f_q);

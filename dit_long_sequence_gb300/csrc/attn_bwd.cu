@@ -196,7 +196,8 @@ struct Cfg {
 template <bool KEY>
 struct Item {
     int b, h, fixed, begin, end;
-    int64_t part_tile;          // its place among the partials
+    bool cut;                   // a piece: its result goes to the partials
+    int64_t part_tile;          // its place among them
 };
 
 // Items count pieces fastest, then tiles, then heads, so that the CTAs at work
@@ -210,18 +211,26 @@ __device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int id) {
     const int slot = KEY ? id : id - a.n_kv_items;
     const uint32_t f = static_cast<uint32_t>(KEY ? a.f_kv : a.f_q);
     const int tiles = KEY ? a.kv_out_tiles : a.q_tiles;
-    uint32_t piece, inner, h;
-    const uint32_t item = (KEY ? a.div_f_kv : a.div_f_q).divmod(static_cast<uint32_t>(slot), piece);
+    uint32_t piece = 0, inner, h, item = static_cast<uint32_t>(slot);
+    it.cut = KEY ? f > 1 : slot >= a.q_whole;
+    if (it.cut) {
+        const uint32_t first = static_cast<uint32_t>(KEY ? 0 : a.q_whole);
+        item = first + (KEY ? a.div_f_kv : a.div_f_q).divmod(static_cast<uint32_t>(slot) - first, piece);
+    }
     const uint32_t outer = (MASK ? a.div_bh : (KEY ? a.div_kv_tiles : a.div_q_tiles)).divmod(item, inner);
     const uint32_t bh = MASK ? inner : outer;
     it.fixed = static_cast<int>(!MASK ? inner : KEY ? outer : tiles - 1 - outer);
     it.b = static_cast<int>(a.div_h.divmod(bh, h));
     it.h = static_cast<int>(h);
-    it.part_tile = (static_cast<int64_t>(bh) * tiles + it.fixed) * f + piece;
+    it.part_tile = (static_cast<int64_t>(bh) * tiles + it.fixed - (KEY ? 0 : a.q_whole)) * f + piece;
     // a key tile wholly past kv_len has nothing to stream: its gradient is zero
     const uint32_t x_tiles = static_cast<uint32_t>(KEY ? (it.fixed < a.kv_tiles ? a.q_tiles : 0) : a.kv_tiles);
-    it.begin = static_cast<int>((KEY ? a.div_f_kv : a.div_f_q).div(piece * x_tiles));
-    it.end = static_cast<int>((KEY ? a.div_f_kv : a.div_f_q).div((piece + 1) * x_tiles));
+    it.begin = 0;
+    it.end = static_cast<int>(x_tiles);
+    if (it.cut) {
+        it.begin = static_cast<int>((KEY ? a.div_f_kv : a.div_f_q).div(piece * x_tiles));
+        it.end = static_cast<int>((KEY ? a.div_f_kv : a.div_f_q).div((piece + 1) * x_tiles));
+    }
     return it;
 }
 
@@ -795,7 +804,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
             constexpr int kChunks = KEY ? D / 32 : D / 64;
             const int c0 = KEY ? 0 : g * kChunks;
             const uint32_t tA = s.tmem + lane_off + (KEY && g == 0 ? C::kColAcc1 : C::kColAcc0);
-            const bool split = (KEY ? a.f_kv : a.f_q) > 1;
+            const bool split = it.cut;
             const float mult = split ? 1.f : (KEY && g == 0 ? 1.f : a.scale);
             const bool zero_row = n_tiles == 0 || row >= (KEY ? a.kv_len : a.Nq);    // (key item: rows past kv_len are zeros)
             const bool inside = split || row < (KEY ? a.Nkv : a.Nq);
@@ -997,14 +1006,15 @@ __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const AttnBwdArgs a, 
     const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t unit = g / (D / 4);
     const int c4 = static_cast<int>(g % (D / 4));
-    const int item = static_cast<int>(unit / kT), r = static_cast<int>(unit % kT);
-    if (unit >= static_cast<int64_t>(a.B) * a.H * tiles * kT) return;
+    const int nth = static_cast<int>(unit / kT), r = static_cast<int>(unit % kT);
+    const int item = nth + (key ? 0 : a.q_whole);
+    if (unit >= (static_cast<int64_t>(a.B) * a.H * tiles - (key ? 0 : a.q_whole)) * kT) return;
     const int row = (item % tiles) * kT + r;
     const int h = (item / tiles) % a.H, b = item / tiles / a.H;
     if (row >= (key ? a.Nkv : a.Nq)) return;
     const int64_t stride = static_cast<int64_t>(key ? 2 : 1) * kT * D;
-    const float* p = (key ? a.part_kv + (static_cast<int64_t>(item) * f * 2 + which) * kT * D
-                          : a.part_q + static_cast<int64_t>(item) * f * kT * D) + r * D + 4 * c4;
+    const float* p = (key ? a.part_kv + (static_cast<int64_t>(nth) * f * 2 + which) * kT * D
+                          : a.part_q + static_cast<int64_t>(nth) * f * kT * D) + r * D + 4 * c4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < f; ++k) {
         const float4 v = __ldcs(reinterpret_cast<const float4*>(p + k * stride));
@@ -1060,8 +1070,9 @@ cudaError_t launch_attn_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const 
 cudaError_t launch_attn_bwd_sum(const AttnBwdArgs& a, int D, bool grad_bf16, cudaStream_t s) {
     const bool kv = a.f_kv > 1, q = a.f_q > 1;
     if (!kv && !q) return cudaSuccess;
-    const int tiles = kv && q ? (a.kv_out_tiles > a.q_tiles ? a.kv_out_tiles : a.q_tiles) : (kv ? a.kv_out_tiles : a.q_tiles);
-    const int64_t threads = static_cast<int64_t>(a.B) * a.H * tiles * kT * (D / 4);
+    const int64_t bh = static_cast<int64_t>(a.B) * a.H;
+    const int64_t kv_items = kv ? bh * a.kv_out_tiles : 0, q_items = q ? bh * a.q_tiles - a.q_whole : 0;
+    const int64_t threads = (kv_items > q_items ? kv_items : q_items) * kT * (D / 4);
     const dim3 grid(static_cast<unsigned>((threads + 255) / 256), (kv ? 2 : 0) + (q ? 1 : 0));
     const int first = kv ? 0 : 2;
     if (D == 128) {

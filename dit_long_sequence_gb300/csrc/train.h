@@ -136,11 +136,11 @@ struct AttnBwdArgs {
     void *dq, *dk, *dv;
     dit_strides4_t sdq, sdk, sdv;
     // Key items (b, h, 128-key tile), each cut into f_kv ranges of query tiles,
-    // and query items (b, h, 128-row tile), each cut into f_q ranges of key
-    // tiles, over `grid` CTAs.  f > 1: pieces write fp32 partials
-    // ([tile][piece][2][128][D] for dv, dk; [tile][piece][128][D] for dq) that a
-    // second kernel sums in piece order.
-    int f_kv, f_q;
+    // and query items (b, h, 128-row tile), those from q_whole on cut into f_q
+    // ranges of key tiles, over `grid` CTAs.  Pieces write fp32 partials
+    // ([tile][piece][2][128][D] for dv, dk; [cut item][piece][128][D] for dq) that
+    // a second kernel sums in piece order.
+    int f_kv, f_q, q_whole;
     int n_kv_items, n_q_items;  // pieces counted
     FastDiv div_f_kv, div_f_q, div_kv_tiles, div_q_tiles, div_bh, div_h;   // item -> piece, tile, head
     int grid;

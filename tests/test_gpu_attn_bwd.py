@@ -255,6 +255,30 @@ def test_longer_than_the_ring(dl):
                D ** -0.5, allow)
 
 
+@pytest.mark.parametrize("D,grad_dtype", [(64, torch.bfloat16), (128, torch.float32), (128, torch.bfloat16)])
+def test_last_query_items_cut(dl, D, grad_dtype):
+    """256 key and 256 query items on 152 SMs: the last query items run in pieces
+    (the workspace then holds more than the statistics and the counter)."""
+    B, N, H, kvl = 1, 4070, 8, 4001
+    q, k, v, dout, _ = _inputs(B, N, N, H, D, 93)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert dl.attn_bwd_workspace_bytes(B, N, N, H, D, kvl) > H * 2 * 32 * 128 * 4 + 512
+    scale, allow = D ** -0.5, _allow(B, N, N, kvl)
+    out, lse = _forward(q, k, v, scale, allow, torch.bfloat16)
+    grads = dl.attn_bwd(q, k, v, out, lse, dout, key_valid_len=kvl, grad_dtype=grad_dtype)
+    for h in (0, 4, 5, 6, 7):
+        s = slice(h, h + 1)
+        _check([g[:, :, s] for g in grads], q[:, :, s], k[:, :, s], v[:, :, s], out[:, :, s], lse[:, s], dout[:, :, s], scale, allow)
+    again = dl.attn_bwd(q, k, v, out, lse, dout, key_valid_len=kvl, grad_dtype=grad_dtype)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    # a mask over the same rows: none of them is cut
+    m = torch.ones((1, N, kvl), dtype=torch.bool)
+    bits = wl.pack_mask_bits(m).to(DEV)
+    masked = dl.attn_bwd_masked(q, k, v, out, lse, dout, bits, key_valid_len=kvl, grad_dtype=grad_dtype)
+    assert torch.equal(masked[1], grads[1]) and torch.equal(masked[2], grads[2])
+    _check([g[:, :, 7:] for g in masked], q[:, :, 7:], k[:, :, 7:], v[:, :, 7:], out[:, :, 7:], lse[:, 7:], dout[:, :, 7:], scale, allow)
+
+
 def test_refusals(dl):
     from dit_long_sequence_gb300 import binding as E
     B, N, H, D = 1, 64, 2, 64
