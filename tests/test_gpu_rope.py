@@ -140,6 +140,28 @@ def test_in_place_neighbours_streams_and_capture(dl):
     assert torch.equal(x, want) and (buf[:, 50:] == 9).all() and (buf[:, :, 2] == 9).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("D,R", [(128, 26), (192, 166), (128, 20), (40, 36), (64, 62), (48, 2), (256, 250), (8, 6), (184, 184)])
+def test_half_layout_of_any_pairs_in_and_out_of_place(dl, dtype, D, R):
+    """Halves that begin inside 16 bytes, chunks that hold both halves or the end
+    of the turned channels; the same bits in place, and in a view that leaves
+    its neighbours alone."""
+    x, g = _x((2, 333, 5, D), dtype, D + R, 1)
+    freq, _ = dl.rope_inv_freq(R)
+    y = dl.rope(x, freq, layout="half", offset=17)
+    pos = torch.arange(17, 350, dtype=torch.int32, device=DEV)[None, :, None]
+    _check(y, x, freq, pos, (R // 2,), True)
+    buf = torch.full((2, 340, 7, D), 4.0, dtype=dtype, device=DEV)
+    dl.rope(x, freq, layout="half", offset=17, out=buf[:, 3:336, 1:6])
+    assert torch.equal(buf[:, 3:336, 1:6], y)
+    rest = buf.clone()
+    rest[:, 3:336, 1:6] = 4.0
+    assert (rest == 4.0).all()
+    z = x.clone()
+    dl.rope(z, freq, layout="half", offset=17, out=z)
+    assert torch.equal(z, y)
+
+
 def test_refusals(dl):
     from dit_long_sequence_gb300 import binding as E
     x, _ = _x((1, 4, 2, 64), BF, 41)
