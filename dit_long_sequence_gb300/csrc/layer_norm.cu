@@ -31,6 +31,7 @@ namespace dit {
 namespace {
 
 constexpr int kMaxThreads = 512;
+constexpr int kTwoRowThreads = 384;     // 168 registers a thread: two rows' values beside the sums over rows
 // Cross-warp sums of a block, in 8 bytes a warp; a row's warps are padded to an
 // even number (5 rows of 3 warps take 20).
 constexpr int kSums = 24;
@@ -252,20 +253,26 @@ struct RowGroup {
         for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    // The sums of lanes_two over the row's warps, to every thread.
-    __device__ __forceinline__ f2 across_two(float v) {
-        float* const b = reinterpret_cast<float*>(buf + flip * kSums + id * pitch);
+    // The sums of lanes_two over the row's warps, to every thread; of ROWS rows at once.
+    template <int ROWS>
+    __device__ __forceinline__ void across_two(const float (&v)[ROWS], f2 (&sum)[ROWS]) {
+        float2* const b = buf + flip * kSums + id * ROWS * pitch;
         flip ^= 1;
-        if ((threadIdx.x & 15) == 0) b[t >> 4] = v;
-        sync();
-        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(b);
-        ulonglong2 q = p[0];
-        f2 s = add2(q.x, q.y);
-        for (int w = 1; w < (pitch >> 1); ++w) {
-            q = p[w];
-            s = add2(s, add2(q.x, q.y));
+        if ((threadIdx.x & 15) == 0) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) reinterpret_cast<float*>(b + j * pitch)[t >> 4] = v[j];
         }
-        return s;
+        sync();
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const ulonglong2* p = reinterpret_cast<const ulonglong2*>(b + j * pitch);
+            ulonglong2 q = p[0];
+            sum[j] = add2(q.x, q.y);
+            for (int w = 1; w < (pitch >> 1); ++w) {
+                q = p[w];
+                sum[j] = add2(sum[j], add2(q.x, q.y));
+            }
+        }
     }
     // Each warp's pair to the row's other warps: lane l gets that of warp
     // l mod span (0 past the last).  One barrier among the row's threads; the other buffer is
@@ -448,10 +455,12 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
     }
 }
 
-template <typename TX, typename TY, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormArgs a, int tpr) {
-    using RX = Ring<TX, VEC, NV>;
-    using RD = Ring<TY, VEC, NV>;
+// ROWS rows of a group of threads at a time: two where a block holds one such group,
+// whose chain of loads, sums and barrier is then as long for two rows as for one.
+template <typename TX, typename TY, int VEC, int NV, int ROWS>
+__global__ void __launch_bounds__(ROWS == 1 ? kMaxThreads : kTwoRowThreads) layer_norm_bwd_kernel(const NormArgs a, int tpr) {
+    using RX = Ring<TX, VEC, NV * ROWS>;
+    using RD = Ring<TY, VEC, NV * ROWS>;
     constexpr int P = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
     __shared__ __align__(16) float2 buf[2 * kSums];
     for (int i = threadIdx.x; i < 2 * kSums; i += blockDim.x) buf[i] = make_float2(0.f, 0.f);
@@ -466,10 +475,10 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
     rd.init(ring_mem + P * RX::kStageBytes * blockDim.x);
     const RowAt x_at(a, a.sx), d_at(a, a.sdy), y_at(a, a.sy);
     const uint32_t slots = blockDim.x / tpr;
-    const uint32_t step = gridDim.x * slots;
+    const uint32_t step = gridDim.x * slots * ROWS;
     const uint32_t row0 = blockIdx.y * a.rows_per_group;
-    const uint32_t rounds = (a.rows_per_group - blockIdx.x * slots + step - 1) / step;
-    const uint32_t first = blockIdx.x * slots + g.id;
+    const uint32_t rounds = (a.rows_per_group - blockIdx.x * slots * ROWS + step - 1) / step;
+    const uint32_t first = (blockIdx.x * slots + g.id) * ROWS;
     bool live[NV];
     int col[NV];
 #pragma unroll
@@ -477,24 +486,30 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
         col[i] = (i * tpr + g.t) * VEC;
         live[i] = col[i] < a.C;
     }
-    float nmean = 0.f, nrstd = 0.f;
+    float nmean[ROWS], nrstd[ROWS];
     auto stats = [&](uint32_t k) {       // of round k, read one round ahead
-        const uint32_t r = first + k * step;
-        const bool ok = k < rounds && r < a.rows_per_group;
-        nmean = ok && a.center ? __ldg(a.mean + row0 + r) : 0.f;
-        nrstd = ok ? __ldg(a.rstd + row0 + r) : 0.f;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const uint32_t r = first + k * step + j;
+            const bool ok = k < rounds && r < a.rows_per_group;
+            nmean[j] = ok && a.center ? __ldg(a.mean + row0 + r) : 0.f;
+            nrstd[j] = ok ? __ldg(a.rstd + row0 + r) : 0.f;
+        }
     };
     auto fetch = [&](uint32_t k) {
-        const uint32_t r = first + k * step;
-        if (k < rounds && r < a.rows_per_group) {
-            const TX* p = static_cast<const TX*>(a.x) + x_at(a, row0 + r);
-            const TY* d = static_cast<const TY*>(a.dy) + d_at(a, row0 + r);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (live[i]) {
-                    rx.fetch(k % P, i, p + col[i]);
-                    rd.fetch(k % P, i, d + col[i]);
-                }
+        for (int j = 0; j < ROWS; ++j) {
+            const uint32_t r = first + k * step + j;
+            if (k < rounds && r < a.rows_per_group) {
+                const TX* p = static_cast<const TX*>(a.x) + x_at(a, row0 + r);
+                const TY* d = static_cast<const TY*>(a.dy) + d_at(a, row0 + r);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (live[i]) {
+                        rx.fetch(k % P, j * NV + i, p + col[i]);
+                        rd.fetch(k % P, j * NV + i, d + col[i]);
+                    }
+            }
         }
         ring_commit();
     };
@@ -514,50 +529,65 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormA
         } else {
             ring_wait<0>();
         }
-        const bool ok = r < a.rows_per_group;
-        const float rstd = nrstd, mr = -nmean * nrstd;
-        Row<TX, VEC> x[NV];
-        Row<TY, VEC> d[NV];
+        bool ok[ROWS];
+        float rstd[ROWS], mr[ROWS];
+        Row<TX, VEC> x[ROWS][NV];
+        Row<TY, VEC> d[ROWS][NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            x[i].zero();
-            d[i].zero();
-            if (ok && live[i]) { x[i] = rx.take(k % P, i); d[i] = rd.take(k % P, i); }
+        for (int j = 0; j < ROWS; ++j) {
+            ok[j] = r + j < a.rows_per_group;
+            rstd[j] = nrstd[j];
+            mr[j] = -nmean[j] * nrstd[j];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                x[j][i].zero();
+                d[j][i].zero();
+                if (ok[j] && live[i]) {
+                    x[j][i] = rx.take(k % P, j * NV + i);
+                    d[j][i] = rd.take(k % P, j * NV + i);
+                }
+            }
         }
         if constexpr (!kAsync) fetch(k + 1);
         stats(k + 1);
-        f2 xh[NP], gr[NP];      // xh and g, kept for dx
-        f2 s2 = 0ull, t2 = 0ull;
-        const f2 r2 = pk(rstd, rstd), m2 = pk(mr, mr);
+        f2 xh[ROWS][NP], gr[ROWS][NP];      // xh and g, kept for dx
+        f2 sum[ROWS];                       // of g and of g xh
+        float both[ROWS];
 #pragma unroll
-        for (int e = 0; e < NP; ++e) {
-            const f2 dy = pair_of(d, e);
-            xh[e] = fma2(pair_of(x, e), r2, m2);
-            gr[e] = mul2(dy, w[e]);
-            s2 = add2(s2, gr[e]);
-            t2 = fma2(gr[e], xh[e], t2);
-            dw[e] = fma2(dy, xh[e], dw[e]);
-            db[e] = add2(db[e], dy);
+        for (int j = 0; j < ROWS; ++j) {
+            f2 s2 = 0ull, t2 = 0ull;
+            const f2 r2 = pk(rstd[j], rstd[j]), m2 = pk(mr[j], mr[j]);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const f2 dy = pair_of(d[j], e);
+                xh[j][e] = fma2(pair_of(x[j], e), r2, m2);
+                gr[j][e] = mul2(dy, w[e]);
+                s2 = add2(s2, gr[j][e]);
+                t2 = fma2(gr[j][e], xh[j][e], t2);
+                dw[e] = fma2(dy, xh[j][e], dw[e]);
+                db[e] = add2(db[e], dy);
+            }
+            if (tpr > 32) both[j] = g.lanes_two(sum2(s2), sum2(t2));
+            else sum[j] = pk(g.lanes(sum2(s2)), g.lanes(sum2(t2)));
         }
-        float sg, st;
-        if (tpr > 32) {
-            unpk(g.across_two(g.lanes_two(sum2(s2), sum2(t2))), sg, st);
-        } else {
-            sg = g.lanes(sum2(s2));
-            st = g.lanes(sum2(t2));
-        }
-        if (!a.center) sg = 0.f;
-        // dx = rstd g - rstd c1 - xh (rstd c2)
-        const float n1 = -sg * a.inv_c * rstd, n2 = -st * a.inv_c * rstd;
-        if (ok) {
-            TX* const p = static_cast<TX*>(a.y) + y_at(a, row0 + r);
-            const f2 c1 = pk(n1, n1), c2 = pk(n2, n2);
-            f2 v[NP];
+        if (tpr > 32) g.across_two(both, sum);
 #pragma unroll
-            for (int e = 0; e < NP; ++e) v[e] = fma2(gr[e], r2, fma2(xh[e], c2, c1));
+        for (int j = 0; j < ROWS; ++j) {
+            float sg, st;
+            unpk(sum[j], sg, st);
+            if (!a.center) sg = 0.f;
+            // dx = rstd g - rstd c1 - xh (rstd c2)
+            const float n1 = -sg * a.inv_c * rstd[j], n2 = -st * a.inv_c * rstd[j];
+            if (ok[j]) {
+                TX* const p = static_cast<TX*>(a.y) + y_at(a, row0 + r + j);
+                const f2 r2 = pk(rstd[j], rstd[j]), c1 = pk(n1, n1), c2 = pk(n2, n2);
+                f2 v[NP];
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (live[i]) store_row<TX, VEC, NV>(p + col[i], i, v);
+                for (int e = 0; e < NP; ++e) v[e] = fma2(gr[j][e], r2, fma2(xh[j][e], c2, c1));
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (live[i]) store_row<TX, VEC, NV>(p + col[i], i, v);
+            }
         }
     }
     ring_wait<0>();
@@ -631,15 +661,15 @@ cudaError_t fwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename TX, typename TY, int VEC, int NV>
+template <typename TX, typename TY, int VEC, int NV, int ROWS>
 cudaError_t bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-    using RX = Ring<TX, VEC, NV>;
-    using RD = Ring<TY, VEC, NV>;
+    using RX = Ring<TX, VEC, NV * ROWS>;
+    using RD = Ring<TY, VEC, NV * ROWS>;
     const int depth = ring_depth(RX::kStageBytes + RD::kStageBytes, RX::kAsync && RD::kAsync);
     const int rings = (RX::kStageBytes + RD::kStageBytes) * depth * p.threads;
     const int sums = p.threads > p.tpr ? p.threads * NV * VEC * static_cast<int>(sizeof(float)) : 0;
     const int smem = rings > sums ? rings : sums;
-    auto kern = layer_norm_bwd_kernel<TX, TY, VEC, NV>;
+    auto kern = layer_norm_bwd_kernel<TX, TY, VEC, NV, ROWS>;
     if (smem > 47 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -653,9 +683,11 @@ cudaError_t bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
 
 template <typename TX, typename TY, bool BWD>
 cudaError_t pick(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+    if constexpr (BWD)
+        if (p.two_rows) return bwd<TX, TY, 8, 2, 2>(a, p, s);
 #define DIT_NORM_CASE(V, N) \
     if (p.vec == V && p.nv == N) {                                                                 \
-        if constexpr (BWD) return bwd<TX, TY, V, N>(a, p, s);                                      \
+        if constexpr (BWD) return bwd<TX, TY, V, N, 1>(a, p, s);                                   \
         else return fwd<TX, TY, V, N>(a, p, s);                                                    \
     }
     DIT_NORM_CASE(8, 1)
@@ -689,8 +721,9 @@ cudaError_t pick_types(const NormArgs& a, const NormPlan& p, bool x_f32, bool y_
 // 512 threads an SM either way: forward in blocks of up to 128 (a row's threads
 // when those are more), backward in one block, which leaves one partial (1,024
 // threads an SM measured 127 us, for its partials).  Above 4,096 channels the
-// backward pass has one row at a time on an SM and is bound by its chain of sums:
-// 195 us for 24,576 x 5,120 (floor 111); 640 threads of 8 channels took 205.
+// backward pass has one group of threads on an SM; up to 6,144 it takes two rows
+// at a time: 24,576 x 5,120 168 us (floor 111) against 188 one by one, 205 with 640
+// threads of 8 channels and 240 with two rows of those.
 NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max, int sms, bool backward) {
     NormPlan p;
     p.vec = vec_max;
@@ -709,6 +742,8 @@ NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max,
     if (slots < 1) slots = 1;
     p.threads = (static_cast<int>(slots) * p.tpr + 31) / 32 * 32;
     slots = static_cast<uint32_t>(p.threads / p.tpr);
+    p.two_rows = backward && p.vec == 8 && p.nv == 2 && p.tpr > kMaxThreads / 2 && p.tpr <= kTwoRowThreads && rows_per_group > 1;
+    if (p.two_rows) slots *= 2;
     const uint64_t need = (rows_per_group + slots - 1) / slots;
     uint64_t blocks = (static_cast<uint64_t>(sms) * (512 / p.threads) + groups - 1) / groups;
     if (blocks > need) blocks = need;

@@ -85,6 +85,7 @@ struct NormArgs {
 // per thread and row, `tpr` threads per row, `blocks` blocks per group.
 struct NormPlan {
     int vec, nv, tpr, threads, blocks;
+    bool two_rows;              // backward: a row group takes two rows at a time
 };
 NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max, int sms, bool backward);
 
