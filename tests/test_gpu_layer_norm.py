@@ -70,7 +70,8 @@ def test_forward_and_backward(dl, B, N, H, C, tx, ty, center, per_batch, strided
 
 
 @pytest.mark.parametrize("tx,ty", [(BF, BF), (F, BF)])
-@pytest.mark.parametrize("N,C", [(2500, 1152), (1300, 1501), (1200, 2560), (900, 1538), (300, 5120), (400, 6150), (170, 7001)])
+@pytest.mark.parametrize("N,C", [(2500, 1152), (1300, 1501), (1200, 2560), (900, 1538), (300, 5120), (400, 6150), (170, 7001), (1, 5120),
+                                 (301, 6144), (2, 4104), (1201, 4616)])
 def test_rows_of_three_to_fifteen_warps(dl, N, C, tx, ty):
     """Numbers of warps that are no power of two, in blocks of one to five rows."""
     test_forward_and_backward(dl, 1, N, 1, C, tx, ty, True, False, False)
