@@ -11,8 +11,8 @@
 // rounded to their type once.
 //
 // HBM-bound: the forward pass reads x and writes y, the backward pass reads x
-// and dy and writes dx (24,576 x 4,096 bf16: 69 us forward, 5.8 TB/s or 86% of a
-// plain copy; 113 us backward, 79%, the parameters' sums included).  A row is
+// and dy and writes dx (24,576 x 4,096 bf16: 68 us forward, 5.9 TB/s or 87% of a
+// plain copy; 111 us backward, 80%, the parameters' sums included).  A row is
 // held in the registers of `tpr` threads, at most 32 channels each, so the
 // variance takes a second pass over registers and not over memory.  A thread
 // keeps its channels while it walks over rows: their weights stay in registers,
@@ -148,6 +148,8 @@ __device__ __forceinline__ void store_row(T* p, int i, const f2 (&v)[NV * VEC / 
 // copies of its channels (no other thread reads them, so waiting for its own
 // copies is all the synchronisation there is).  Loads of single bf16 channels
 // are below the smallest asynchronous copy: those wait in registers, a row ahead.
+// What a thread does not have is zeros in the ring, written once or where a row is
+// missing, so that nothing is tested where rows are taken.
 template <typename T, int VEC, int NV>
 struct Ring {
     using R = Row<T, VEC>;
@@ -175,6 +177,22 @@ struct Ring {
             }
         } else {
             reg[i].load(p);
+        }
+    }
+    // Zeros in place of a load: channels past the row's end, rows past the last.
+    __device__ __forceinline__ void clear(int stage, int i) {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if constexpr (kChunk == 16)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(slot(stage, i, c)), "r"(0u) : "memory");
+                else if constexpr (kChunk == 8)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(slot(stage, i, c)), "r"(0u) : "memory");
+                else
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot(stage, i, c)), "r"(0u) : "memory");
+            }
+        } else {
+            reg[i].zero();
         }
     }
     __device__ __forceinline__ R take(int stage, int i) const {
@@ -366,9 +384,16 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live[i]) ring.fetch(k % P, i, p + col[i]);
+        } else if (k < rounds) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) ring.clear(k % P, i);
         }
         ring_commit();
     };
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (!live[i])
+            for (int k = 0; k < P; ++k) ring.clear(k, i);
     for (int k = 0; k < (RX::kAsync ? P - 1 : 1); ++k) fetch(k);
     constexpr int NP = NV * VEC / 2;
     f2 w[NP], bi[NP];
@@ -397,10 +422,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormA
         const bool ok = r < a.rows_per_group;
         Row<TX, VEC> raw[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            raw[i].zero();
-            if (ok && live[i]) raw[i] = ring.take(k % P, i);
-        }
+        for (int i = 0; i < NV; ++i) raw[i] = ring.take(k % P, i);
         if constexpr (!RX::kAsync) fetch(k + 1);
         f2 x[NP];
 #pragma unroll
@@ -509,10 +531,23 @@ __global__ void __launch_bounds__(ROWS == 1 ? kMaxThreads : kTwoRowThreads) laye
                         rx.fetch(k % P, j * NV + i, p + col[i]);
                         rd.fetch(k % P, j * NV + i, d + col[i]);
                     }
+            } else if (k < rounds) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    rx.clear(k % P, j * NV + i);
+                    rd.clear(k % P, j * NV + i);
+                }
             }
         }
         ring_commit();
     };
+#pragma unroll
+    for (int i = 0; i < NV * ROWS; ++i)
+        if (!live[i % NV])
+            for (int k = 0; k < P; ++k) {
+                rx.clear(k, i);
+                rd.clear(k, i);
+            }
     constexpr bool kAsync = RX::kAsync && RD::kAsync;
     for (int k = 0; k < (kAsync ? P - 1 : 1); ++k) fetch(k);
     stats(0);
@@ -540,12 +575,8 @@ __global__ void __launch_bounds__(ROWS == 1 ? kMaxThreads : kTwoRowThreads) laye
             mr[j] = -nmean[j] * nrstd[j];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                x[j][i].zero();
-                d[j][i].zero();
-                if (ok[j] && live[i]) {
-                    x[j][i] = rx.take(k % P, j * NV + i);
-                    d[j][i] = rd.take(k % P, j * NV + i);
-                }
+                x[j][i] = rx.take(k % P, j * NV + i);
+                d[j][i] = rd.take(k % P, j * NV + i);
             }
         }
         if constexpr (!kAsync) fetch(k + 1);
@@ -711,18 +742,18 @@ cudaError_t pick_types(const NormArgs& a, const NormPlan& p, bool x_f32, bool y_
 
 // Channels a thread: forward 32 (16 without 16-byte loads), so that a row of
 // 4,096 is four warps' and one of 1,024 a single warp's, without a barrier:
-// 69 us for 24,576 x 4,096 bf16 against 101 with 16 a thread and 167 with 8;
+// 68 us for 24,576 x 4,096 bf16 against 101 with 16 a thread and 167 with 8;
 // halved while rows are so few that the SMs would not get 512 threads each.
-// Backward 16: its sums over rows hold two registers a channel (113 us there; 32
+// Backward 16: its sums over rows hold two registers a channel (111 us there; 32
 // spill), and 8 where rows are read channel by channel (24,576 x 4,095: 240 us
 // against 550, whose prefetched row spills).
 // A row's threads are whole warps and not a power of two: 24,576 x 2,560 takes
-// 56 and 76 us (floor 37 and 56) against 61 and 101 with 128 and 256 threads.
+// 54 and 75 us (floor 37 and 56) against 61 and 101 with 128 and 256 threads.
 // 512 threads an SM either way: forward in blocks of up to 128 (a row's threads
 // when those are more), backward in one block, which leaves one partial (1,024
 // threads an SM measured 127 us, for its partials).  Above 4,096 channels the
 // backward pass has one group of threads on an SM; up to 6,144 it takes two rows
-// at a time: 24,576 x 5,120 168 us (floor 111) against 188 one by one, 205 with 640
+// at a time: 24,576 x 5,120 157 us (floor 111) against 188 one by one, 205 with 640
 // threads of 8 channels and 240 with two rows of those.
 NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max, int sms, bool backward) {
     NormPlan p;
