@@ -67,7 +67,7 @@ def build_calls() -> str:
     for d in dirs:
         cmd += ["-isystem", d]
     cmd += [os.path.join(CSRC, "py_calls.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
-            "-ltorch_cpu", "-lc10"]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for py_calls.cpp:\n{r.stderr}")

@@ -12,11 +12,13 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/cuda/EmptyTensor.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/types.h>
 
 #include <cmath>
 #include <cstdint>
+#include <optional>
 #include <vector>
 
 #include "dit_attn.h"
@@ -84,8 +86,9 @@ dit_strides4_t strides4(const at::Tensor& t) {
 bool contiguous_f32(const at::Tensor& t, at::IntArrayRef shape) {
     return is(t, at::kFloat) && t.sizes() == shape && t.is_contiguous();
 }
+// (PyTorch's allocation without its dispatcher: 0.3 to 0.5 us less a tensor)
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(shape, like.options().dtype(type));
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 // (status, tensors...), None for those not there
 PyObject* result(int status, std::initializer_list<const at::Tensor*> ts) {
