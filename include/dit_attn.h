@@ -538,7 +538,8 @@ dit_status_t dit_attn_bwd_masked(const void *q, const void *k, const void *v,
  * dit_attn_bwd_workspace_bytes -- workspace of dit_attn_bwd (masked = 0) or
  * dit_attn_bwd_masked (masked != 0) on the CURRENT device (the plan depends on
  * its SM count): per-row statistics, the fp32 partial gradients of items that
- * are cut into pieces because there are few of them, the mask's occupancy map.
+ * are cut into pieces (all of them where there are few, the last query items of
+ * a middle-sized grid), the mask's occupancy map.
  * 0 when there is nothing to compute.  Host only.
  */
 size_t dit_attn_bwd_workspace_bytes(int B, int Nq, int Nkv, int H, int D, int key_valid_len, int masked);
