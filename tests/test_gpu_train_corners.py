@@ -1,0 +1,47 @@
+"""The training operators in corners of what their documentation allows that the
+other tests do not reach."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dl():
+    import dit_long_sequence_gb300 as m
+    return m
+
+
+@pytest.fixture(autouse=True)
+def no_wait_ran_out(dl):
+    yield
+    rc, info = dl.check_watchdog()
+    assert rc == 0, info
+
+
+# ---------------------------------------------------------------- layer norm
+
+@pytest.mark.parametrize("shape", [(0, 5, 64), (0, 5, 2, 64), (2, 0, 2, 64), (2, 5, 0, 64), (0, 0, 64)])
+@pytest.mark.parametrize("given", [False, True])
+def test_parameter_gradients_over_no_rows_are_zeros(dl, shape, given):
+    x = torch.empty(shape, dtype=BF, device=DEV)
+    w = torch.ones(64, device=DEV)
+    rows = torch.empty(shape[:-1], device=DEV)
+    dw, db = torch.full_like(w, 3.0), torch.full_like(w, 3.0)
+    if given:
+        _, a, b = dl.layer_norm_bwd(x, x, rows, rows, w, dweight=dw, dbias=db)
+        assert a is dw and b is db
+    else:
+        del dw, db      # (fresh results would take this memory)
+        _, a, b = dl.layer_norm_bwd(x, x, rows, rows, w)
+    torch.cuda.synchronize()
+    assert bool((a == 0).all() and (b == 0).all())
+
+
+def test_a_set_of_parameters_for_each_of_no_batch_entries(dl):
+    x, w = torch.empty((0, 5, 64), device=DEV), torch.empty((0, 64), device=DEV)
+    dx, dw, db = dl.layer_norm_bwd(x, x, x[..., 0], x[..., 0], w)
+    assert dx.shape == x.shape and dw.shape == w.shape and db.shape == w.shape
