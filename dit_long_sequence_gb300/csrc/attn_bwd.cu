@@ -821,8 +821,9 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = zero_row ? 0u : __float_as_uint(__uint_as_float(o[i]) * mult);
-                if (!inside) continue;
-                if (!OUT_BF16 || split) {
+                if (!inside) {
+                    // nothing to store: past the last row
+                } else if (!OUT_BF16 || split) {
                     float* dst = (split ? part : static_cast<float*>(out) + off) + cc * 32;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
@@ -840,6 +841,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
                         store8(dst + i, v, a.wide);
                     }
                 }
+                __syncwarp();       // the next load is the whole warp's
             }
         }
         if (n_tiles > 0) {

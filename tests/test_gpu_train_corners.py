@@ -4,6 +4,8 @@ other tests do not reach."""
 import pytest
 import torch
 
+from test_gpu_attn_bwd import _allow, _check, _forward, _inputs
+
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 BF, F = torch.bfloat16, torch.float32
@@ -45,3 +47,22 @@ def test_a_set_of_parameters_for_each_of_no_batch_entries(dl):
     x, w = torch.empty((0, 5, 64), device=DEV), torch.empty((0, 64), device=DEV)
     dx, dw, db = dl.layer_norm_bwd(x, x, x[..., 0], x[..., 0], w)
     assert dx.shape == x.shape and dw.shape == w.shape and db.shape == w.shape
+
+
+# ---------------------------------------------------------------- attention backward
+
+@pytest.mark.parametrize("Nq,Nkv,kvl", [(1, 1, 1), (33, 65, 64), (127, 129, 97), (161, 255, 250), (1000, 31, 31)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("grad_dtype", [BF, F])
+def test_tiles_that_end_inside_a_warps_rows(dl, Nq, Nkv, kvl, D, grad_dtype):
+    """The rows of one warp that are there and those that are not: gradients in
+    the middle of a larger buffer, whose other rows stay."""
+    q, k, v, dout, _ = _inputs(2, Nq, Nkv, 2, D, 23 + Nq)
+    allow = _allow(2, Nq, Nkv, kvl)
+    out, lse = _forward(q, k, v, D ** -0.5, allow, BF)
+    bufs = [torch.full((2, n + 256, 2, D), 5.0, dtype=grad_dtype, device=DEV) for n in (Nq, Nkv, Nkv)]
+    views = [b[:, :b.shape[1] - 256] for b in bufs]
+    dl.attn_bwd(q, k, v, out, lse, dout, key_valid_len=kvl, dq=views[0], dk=views[1], dv=views[2])
+    torch.cuda.synchronize()
+    _check(views, q, k, v, out, lse, dout, D ** -0.5, allow)
+    assert all(bool((b[:, b.shape[1] - 256:] == 5.0).all()) for b in bufs)
