@@ -942,7 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // stat[b*H + h][0][i] = -lse * log2(e) (-inf for rows without a key and rows
-// past Nq, so that their P is 0), [1][i] = dlse - sum_d dO O.  One row per
+// past Nq, so that their P is 0), [1][i] = dlse - sum_d dO O (0 for those rows,
+// whose O and dlse may be anything: 0 * NaN would reach every key).  One row per
 // D / 8 lanes, 16 bytes of dO each; a block's 2,048 / D rows are of one (b, h),
 // which divides a head's padded rows.  HBM-bound (reads dO and O once).
 template <int D, bool OUT_BF16>
@@ -992,7 +993,7 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_kernel(const AttnBwdStatArg
         float* const dst = a.stat + bh * 2 * a.rows_pad + i;
         if (a.dlse != nullptr && i < a.Nq) s -= __ldg(a.dlse + bh * a.Nq + i);
         dst[0] = nl;
-        dst[a.rows_pad] = -s;
+        dst[a.rows_pad] = nl == -INFINITY ? 0.f : -s;
     }
 }
 

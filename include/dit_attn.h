@@ -490,8 +490,9 @@ dit_status_t dit_attn_fwd_fp8_ws(const void *q, const void *k, const void *v,
  *           overlap one another, any input or the workspace (a shared first
  *           address is DIT_ERR_INVALID_ARG).  Rows j >= key_valid_len of dk and
  *           dv are written as zeros; those rows of k and v are never read.
- * A row with lse = -inf (no allowed key) contributes nothing.  All q, k, v and
- * dout that are read must be finite: 0 * inf is NaN in the products.
+ * A row with lse = -inf (no allowed key) contributes nothing, whatever its out
+ * and dlse hold.  All q, k, v and dout that are read must be finite: 0 * inf is
+ * NaN in the products.
  * workspace device memory of dit_attn_bwd_workspace_bytes, 16-byte aligned, not
  *           used by anything else until the stream has passed the call.  Needed
  *           unless there is no key or no query.

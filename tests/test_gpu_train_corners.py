@@ -1,10 +1,12 @@
 """The training operators in corners of what their documentation allows that the
 other tests do not reach."""
+import math
 
 import pytest
 import torch
 
-from test_gpu_attn_bwd import _allow, _check, _forward, _inputs
+from dit_long_sequence_gb300 import workloads as wl
+from test_gpu_attn_bwd import _allow, _check, _forward, _inputs, _mask
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -50,6 +52,31 @@ def test_a_set_of_parameters_for_each_of_no_batch_entries(dl):
 
 
 # ---------------------------------------------------------------- attention backward
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("junk", [math.nan, math.inf])
+def test_rows_without_a_key_contribute_nothing_whatever_they_hold(dl, D, junk):
+    """A merge of two LSE of -inf has NaN gradients, and O of such a row may be
+    anything: the same bits as with zeros there."""
+    B, N, H = 2, 300, 2
+    q, k, v, dout, g = _inputs(B, N, N, H, D, 15)
+    m = _mask("holes", B, N, N, g)
+    allow = _allow(B, N, N, N, m)
+    out, lse = _forward(q, k, v, D ** -0.5, allow, F)
+    bits = wl.pack_mask_bits(m).to(DEV)
+    dlse = torch.randn((B, H, N), generator=g, device=DEV)
+    none = torch.isinf(lse)
+    assert bool(none.any())
+    got = []
+    for fill in (0.0, junk):
+        o = out.masked_fill(none.transpose(1, 2)[..., None], fill)
+        d = dlse.masked_fill(none, fill)
+        got.append(dl.attn_bwd_masked(q, k, v, o, lse, dout, bits, dlse=d))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    empty = ~allow[:, 0].any(-1)
+    assert bool((got[1][0][empty] == 0).all())
+
 
 @pytest.mark.parametrize("Nq,Nkv,kvl", [(1, 1, 1), (33, 65, 64), (127, 129, 97), (161, 255, 250), (1000, 31, 31)])
 @pytest.mark.parametrize("D", [64, 128])
