@@ -565,14 +565,14 @@ __global__ void __launch_bounds__(ROWS == 1 ? kMaxThreads : kTwoRowThreads) laye
             ring_wait<0>();
         }
         bool ok[ROWS];
-        float rstd[ROWS], mr[ROWS];
+        float rstd[ROWS], nm[ROWS];
         Row<TX, VEC> x[ROWS][NV];
         Row<TY, VEC> d[ROWS][NV];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             ok[j] = r + j < a.rows_per_group;
             rstd[j] = nrstd[j];
-            mr[j] = -nmean[j] * nrstd[j];
+            nm[j] = -nmean[j];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 x[j][i] = rx.take(k % P, j * NV + i);
@@ -587,11 +587,12 @@ __global__ void __launch_bounds__(ROWS == 1 ? kMaxThreads : kTwoRowThreads) laye
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             f2 s2 = 0ull, t2 = 0ull;
-            const f2 r2 = pk(rstd[j], rstd[j]), m2 = pk(mr[j], mr[j]);
+            const f2 r2 = pk(rstd[j], rstd[j]), m2 = pk(nm[j], nm[j]);
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 const f2 dy = pair_of(d[j], e);
-                xh[j][e] = fma2(pair_of(x[j], e), r2, m2);
+                // (the mean first: x rstd - mean rstd is off by 2^-24 |mean| rstd)
+                xh[j][e] = mul2(add2(pair_of(x[j], e), m2), r2);
                 gr[j][e] = mul2(dy, w[e]);
                 s2 = add2(s2, gr[j][e]);
                 t2 = fma2(gr[j][e], xh[j][e], t2);
@@ -753,7 +754,7 @@ cudaError_t pick_types(const NormArgs& a, const NormPlan& p, bool x_f32, bool y_
 // when those are more), backward in one block, which leaves one partial (1,024
 // threads an SM measured 127 us, for its partials).  Above 4,096 channels the
 // backward pass has one group of threads on an SM; up to 6,144 it takes two rows
-// at a time: 24,576 x 5,120 157 us (floor 111) against 188 one by one, 205 with 640
+// at a time: 24,576 x 5,120 159 us (floor 111) against 188 one by one, 205 with 640
 // threads of 8 channels and 240 with two rows of those.
 NormPlan norm_plan(int C, uint32_t groups, uint32_t rows_per_group, int vec_max, int sms, bool backward) {
     NormPlan p;

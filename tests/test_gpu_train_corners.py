@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import train_ref as ref
 from dit_long_sequence_gb300 import workloads as wl
 from test_gpu_attn_bwd import _allow, _check, _forward, _inputs, _mask
 
@@ -49,6 +50,30 @@ def test_a_set_of_parameters_for_each_of_no_batch_entries(dl):
     x, w = torch.empty((0, 5, 64), device=DEV), torch.empty((0, 64), device=DEV)
     dx, dw, db = dl.layer_norm_bwd(x, x, x[..., 0], x[..., 0], w)
     assert dx.shape == x.shape and dw.shape == w.shape and db.shape == w.shape
+
+
+@pytest.mark.parametrize("tx,ty,spread", [(F, F, 0.01), (F, BF, 0.01), (BF, BF, 8.0)])
+@pytest.mark.parametrize("B,N,H,C", [(1, 64, 1, 500), (2, 40, 1, 4096), (1, 50, 3, 128), (1, 30, 1, 5120), (1, 20, 1, 4097)])
+def test_backward_of_rows_far_from_zero(dl, B, N, H, C, tx, ty, spread):
+    """Rows around 1,000.  x - mean is one rounding of the difference and its
+    product with rstd another, so xh is good to 2^-23 of itself, however far the
+    mean is: train_ref's bounds with |xh| in the place of (|x| + |mean|) rstd."""
+    g = wl.generator(DEV, 7 + C)
+    x = (1000.0 + spread * torch.randn((B, N, H, C), generator=g, device=DEV)).to(tx)
+    w = 1 + 0.3 * torch.randn(C, generator=g, device=DEV)
+    _, mean, rstd = dl.layer_norm_fwd(x, w, out_dtype=ty)
+    dy = torch.randn(x.shape, generator=g, device=DEV).to(ty)
+    dx, dw, db = dl.layer_norm_bwd(dy, x, mean, rstd, w)
+    x64, d, r, w64 = x.double(), dy.double(), rstd.double()[..., None], w.double()
+    xh = (x64 - mean.double()[..., None]) * r
+    gr = d * w64
+    c1, c2 = gr.mean(-1, keepdim=True), (gr * xh).mean(-1, keepdim=True)
+    want = r * (gr - c1 - xh * c2)
+    bound = 64 * ref.EPS32 * r * (gr.abs() + gr.abs().mean(-1, keepdim=True) + 2 * xh.abs() * (gr * xh).abs().mean(-1, keepdim=True))
+    ref.check(dx, want, 1.01 * bound + (ref.BF16 if tx == BF else 2.0 ** -24) * want.abs(), "dx")
+    chain = B * N * H // 100 + 300      # as in the layer norm's own test
+    ref.check(dw, (d * xh).sum((0, 1, 2)), ref.EPS32 * (chain + 4) * (d * xh).abs().sum((0, 1, 2)) + 1e-30, "dweight")
+    ref.check(db, d.sum((0, 1, 2)), ref.EPS32 * chain * d.abs().sum((0, 1, 2)) + 1e-30, "dbias")
 
 
 # ---------------------------------------------------------------- attention backward
