@@ -17,6 +17,7 @@
 #include "bwd_plan.h"
 #include "dit_attn.h"
 #include "internal.h"
+#include "rope_turns.h"
 #include "train.h"
 
 using namespace dit;
@@ -469,11 +470,8 @@ dit_status_t dit_rope(const void* x, dit_dtype_t dtype, const dit_strides4_t* x_
                                        positions_batch_stride < static_cast<int64_t>(N) * n_axes))
         return DIT_ERR_INVALID_ARG;
     for (int i = 0; i < pairs; ++i) {
-        // 2^64 * (inv_freq / 2 pi mod 1), the sum of a rounded-down 53-bit fraction
-        double t = inv_freq[i] / 6.283185307179586476925;
-        if (!std::isfinite(t)) return DIT_ERR_INVALID_ARG;
-        t -= std::floor(t);
-        a.turns[i] = t >= 1.0 ? 0u : static_cast<uint64_t>(std::ldexp(t, 64));
+        if (!std::isfinite(inv_freq[i])) return DIT_ERR_INVALID_ARG;
+        a.turns[i] = turns_per_step(inv_freq[i]);
     }
     if (B == 0 || N == 0 || H == 0) return DIT_OK;
     if (!x || !y || !x_strides || !y_strides) return DIT_ERR_INVALID_ARG;

@@ -9,9 +9,9 @@
 //
 // Angles: only theta / 2 pi modulo 1 matters, so inv_freq_i / 2 pi modulo 1 is
 // held as a 64-bit fraction and multiplied by the integer position modulo
-// 2^64 -- the wrap-around is the range reduction, exact at any 32-bit
-// position (the fraction's rounding moves an angle by at most 2 pi * 2^-65
-// per step, and the caller's fp64 frequency by 2^-53 of itself).  The upper
+// 2^64 -- the wrap-around is the range reduction, exact at any position.  The
+// fraction's own rounding (2^-65 of a turn) moves an angle by at most
+// 2 pi 2^-65 a step: 2^-31 rad at 2^31, 2^-22 at 2^40.  The upper
 // 32 bits, rounded, split into a quarter turn and a signed rest of at most an
 // eighth, whose sine and cosine are their Taylor polynomials of degree 9 and 10
 // (the first terms left out are below 2^-28 of an eighth turn's values).
@@ -190,9 +190,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         int axis = 0;
 #pragma unroll
         for (int k = 0; k + 1 < kRopeMaxAxes; ++k) axis += (k + 1 < a.axes && pr >= a.axis_end[k]) ? 1 : 0;
-        const int64_t pos = a.offset + (a.pos != nullptr ? static_cast<int64_t>(__ldg(a.pos + b * a.pos_sb + static_cast<int64_t>(n0 + n) * a.axes + axis))
-                                                        : static_cast<int64_t>(n0 + n));
-        const uint64_t t = static_cast<uint64_t>(pos) * turns[pr] + 0x80000000ull;
+        const int64_t at = a.pos != nullptr ? static_cast<int64_t>(__ldg(a.pos + b * a.pos_sb + static_cast<int64_t>(n0 + n) * a.axes + axis))
+                                            : static_cast<int64_t>(n0 + n);
+        const uint64_t pos = static_cast<uint64_t>(a.offset) + static_cast<uint64_t>(at);      // modulo 2^64, as the product
+        const uint64_t t = pos * turns[pr] + 0x80000000ull;
         float s, c;
         sincos_turns(static_cast<uint32_t>(t >> 32), s, c);
         cosv[n * gr.stride + pr] = c * a.mscale;

@@ -627,11 +627,14 @@ typedef enum { DIT_ROPE_INTERLEAVED = 0, DIT_ROPE_HALF = 1 } dit_rope_layout_t;
  * positions int32 device array, element (b, n, axis) at
  *           b*positions_batch_stride + n*n_axes + axis (batch stride 0 shares
  *           them), any sign; NULL (one axis only) is n itself.
- * offset    added to every position (any 64-bit value).
+ * offset    added to every position (64 bits; see the accuracy below).
  * inverse   turns by -theta, still times mscale: the gradient of the forward
  *           call (its transpose), and with mscale = 1 also its inverse.
- * Angles are reduced exactly (integer arithmetic modulo one turn), so far
- * positions lose nothing; fp32 arithmetic, y rounded once.
+ * Angles are reduced in integer arithmetic modulo one turn.  A frequency is held
+ * to 2^-65 of a turn (|inv_freq| < 2^60), so at position p (offset included) an
+ * angle is off by 2 pi |p| 2^-65 rad at most: 32-bit positions lose nothing,
+ * 2^40 is at fp32's own rounding, and far beyond the angle loses its meaning.
+ * fp32 arithmetic, y rounded once.
  */
 dit_status_t dit_rope(const void *x, dit_dtype_t dtype, const dit_strides4_t *x_strides,
                       int B, int N, int H, int D, int rotary_dim, dit_rope_layout_t layout,

@@ -1,6 +1,7 @@
 """The training operators in corners of what their documentation allows that the
 other tests do not reach."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -74,6 +75,30 @@ def test_backward_of_rows_far_from_zero(dl, B, N, H, C, tx, ty, spread):
     chain = B * N * H // 100 + 300      # as in the layer norm's own test
     ref.check(dw, (d * xh).sum((0, 1, 2)), ref.EPS32 * (chain + 4) * (d * xh).abs().sum((0, 1, 2)) + 1e-30, "dweight")
     ref.check(db, d.sum((0, 1, 2)), ref.EPS32 * chain * d.abs().sum((0, 1, 2)) + 1e-30, "dbias")
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def test_far_offsets(dl):
+    """Offsets far past 32 bits, frequencies above one and below zero: each is
+    held to 2^-65 of a turn a step, so an angle is off by 2 pi |position| 2^-65,
+    and the rotation by 2^-20 besides (train_ref)."""
+    two_pi = Fraction("6.28318530717958647692528676655900576839433879875021")
+    freq = torch.tensor([1.0, 3.75, -0.3, 1e-4, 100.1, 0.7071067811865476], dtype=torch.float64)
+    x = torch.zeros((1, 3, 1, 12), device=DEV)
+    x[..., 0::2] = 1.0
+    pos = torch.tensor([0, 1, -5], dtype=torch.int32, device=DEV)
+    for offset in (2 ** 31 + 9, 2 ** 36 + 12_345, -(2 ** 40) - 77, 2 ** 44 + 3):
+        for inverse in (False, True):
+            y = dl.rope(x, freq, pos, offset=offset, inverse=inverse).cpu().double()
+            for n in range(3):
+                p = offset + int(pos[n])
+                for i in range(6):
+                    ang = float((Fraction(float(freq[i])) * p) % two_pi)
+                    tol = 2.0 ** -20 + 2 * math.pi * abs(p) * 2.0 ** -65
+                    assert abs(float(y[0, n, 0, 2 * i]) - math.cos(ang)) <= tol, (offset, i)
+                    sign = -1 if inverse else 1
+                    assert abs(float(y[0, n, 0, 2 * i + 1]) - sign * math.sin(ang)) <= tol, (offset, i)
 
 
 # ---------------------------------------------------------------- attention backward
