@@ -200,6 +200,7 @@ dit_status_t check_tma_strides(const dit_strides4_t& s, bool fp8) {
 
 #ifdef DIT_DEBUG
 unsigned long long debug_wait_limit_ns() { return g_dbg_limit_ns.load(); }
+int64_t debug_extent_shrink() { return g_dbg_out_shrink.load(); }
 #endif
 
 int device_sm_count(int dev) {

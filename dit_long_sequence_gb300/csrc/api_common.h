@@ -35,8 +35,9 @@ dit_status_t encode_view(CUtensorMap* map, const void* base, const dit_strides4_
 dit_status_t check_tma_strides(const dit_strides4_t& s, bool fp8 = false);
 
 #ifdef DIT_DEBUG
-// The wait limit dit_debug_configure set (0: the default).
+// The wait limit (0: the default) and the extent shrink dit_debug_configure set.
 unsigned long long debug_wait_limit_ns();
+int64_t debug_extent_shrink();
 #endif
 
 }  // namespace dit

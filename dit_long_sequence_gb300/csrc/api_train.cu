@@ -142,6 +142,7 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     a.timeout_ns = kWatchdogNs;
 #ifdef DIT_DEBUG
     if (debug_wait_limit_ns() != 0) a.timeout_ns = debug_wait_limit_ns();
+    a.dbg_rows_short = static_cast<int>(std::min<int64_t>(debug_extent_shrink(), std::max(Nq, Nkv)));
 #endif
     a.B = B;
     a.Nq = Nq;

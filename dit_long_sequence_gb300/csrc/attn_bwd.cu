@@ -381,8 +381,14 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f
         const float* const stat = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
         for (int j = 0; j < n; ++j, ++J) {
             const int x_row = stream.next() * kT;
-            ok = in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len), a.status, ROLE_LOAD, BND_KEY) &&
-                 wait(C::kX0Empty + J % R0, turn(J, R0) ^ 1u, SITE_X_EMPTY);
+            // A tile that is not there ends the CTA's work, as a wait that ran out
+            // does: the flag tells every role, this one's query items among them.
+            if (!in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len) - a.dbg_rows_short, a.status, ROLE_LOAD, BND_KEY)) {
+                *s.wd.abort_flag = 1;
+                ok = false;
+                break;
+            }
+            ok = wait(C::kX0Empty + J % R0, turn(J, R0) ^ 1u, SITE_X_EMPTY);
             if (!ok) break;
             const int full = C::kXFull + J % R0;
             if (leader) {

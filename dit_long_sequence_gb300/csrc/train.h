@@ -150,6 +150,7 @@ struct AttnBwdArgs {
     float *part_kv, *part_q;
     unsigned int* status;
     unsigned long long timeout_ns;
+    int dbg_rows_short;         // debug library: rows the bounds check takes off the streamed tensors
 };
 
 struct AttnBwdStatArgs {

@@ -5,7 +5,7 @@
  * The pages have no counterpart: this is test instrumentation for the
  * kernels' own failure handling and addressing.
  *
- * What the debug library adds to every attention call (dit_attn_fwd and its
+ * What the debug library adds to every forward attention call (dit_attn_fwd and its
  * _ws, _masked, _masked_noalloc, _accumulate and _fp8 forms):
  *   - In-kernel bounds checks.  The work item and key range a CTA decodes, the
  *     key tile of every K/V load, the shared-memory ring slots the products
@@ -19,6 +19,9 @@
  *     stops the other roles, copies and products already in flight are waited
  *     for (with a limit), tensor memory is released and the kernel returns.
  *     The context stays usable; the next call runs normally.
+ * dit_attn_bwd and dit_attn_bwd_masked check the rows of every tile they load:
+ * a tile outside its tensor is not loaded, records DIT_ERR_BOUNDS, and its CTA
+ * winds down as after a wait that ran out (its gradients are then incomplete).
  * dit_check_watchdog() (dit_attn.h) reads and clears the report.
  *
  * The product library exports none of these calls and reports neither
@@ -61,7 +64,8 @@ typedef enum {
  *                  allow (0: the true extent).  A positive value makes the
  *                  stores to the last elements fail their check and be
  *                  skipped -- a way to see the checks fire without any access
- *                  outside the caller's buffer.
+ *                  outside the caller's buffer.  dit_attn_bwd takes as many
+ *                  rows off the extents of q and dout, and of k and v.
  * Returns DIT_ERR_INVALID_ARG for values outside these ranges.  Host only.
  */
 dit_status_t dit_debug_configure(uint32_t fault, int fault_block, int fault_index, uint32_t wait_limit_us,
