@@ -13,11 +13,13 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/types.h>
 
 #include <cmath>
 #include <cstdint>
+#include <exception>
 #include <optional>
 #include <vector>
 
@@ -111,8 +113,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
         return f();
     } catch (const Refused& r) {
         if (r.type != nullptr) PyErr_SetString(r.type, r.what);
-    } catch (const std::exception& e) {      // of PyTorch: out of memory and the like
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {      // PyTorch's own, as the Python errors its functions raise (torch.OutOfMemoryError)
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

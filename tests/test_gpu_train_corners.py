@@ -143,3 +143,19 @@ def test_tiles_that_end_inside_a_warps_rows(dl, Nq, Nkv, kvl, D, grad_dtype):
     torch.cuda.synchronize()
     _check(views, q, k, v, out, lse, dout, D ** -0.5, allow)
     assert all(bool((b[:, b.shape[1] - 256:] == 5.0).all()) for b in bufs)
+
+
+# ---------------------------------------------------------------- calls
+
+def test_no_memory_left_has_its_own_type(dl):
+    x = torch.empty((1, 1, 1, 64), dtype=BF, device=DEV).expand(64, 4096, 64, 64)      # a result of 2 GB
+    freq = dl.rope_inv_freq(64)[0]
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 28)) / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        for call in (lambda: dl.rope(x, freq), lambda: dl.layer_norm_fwd(x)):
+            with pytest.raises(torch.OutOfMemoryError):
+                call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert dl.rope(x[:1, :4], freq).shape == (1, 4, 64, 64)
