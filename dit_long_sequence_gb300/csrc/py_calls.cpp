@@ -92,6 +92,17 @@ bool contiguous_f32(const at::Tensor& t, at::IntArrayRef shape) {
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
     return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
+// f() with the interpreter's lock let go: allocations and launches can wait for
+// the device, and other Python threads run meanwhile.  f touches no Python object
+// and takes no reference of a tensor that has one.
+template <typename F>
+int unlocked(F&& f) {
+    struct Lock {
+        PyThreadState* const state = PyEval_SaveThread();
+        ~Lock() { PyEval_RestoreThread(state); }
+    } lock;
+    return f();
+}
 // (status, tensors...), None for those not there
 PyObject* result(int status, std::initializer_list<const at::Tensor*> ts) {
     PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(1 + ts.size()));
@@ -162,40 +173,38 @@ PyObject* attn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 break;
             }
         at::Tensor grads[3];
-        for (int i = 0; i < 3; ++i) {
-            const at::Tensor& like = i == 0 ? q : k;
-            if (given[i] == nullptr) {
-                grads[i] = fresh(like.sizes(), type, q);
-            } else {
-                if (!bf16_or_f32(*given[i]) || !is(*given[i], type) || given[i]->sizes() != like.sizes())
+        for (int i = 0; i < 3; ++i)
+            if (given[i] != nullptr) {
+                if (!bf16_or_f32(*given[i]) || !is(*given[i], type) || given[i]->sizes() != (i == 0 ? q : k).sizes())
                     value_error("dq must be [B, Nq, H, D], dk and dv [B, Nkv, H, D] tensors of one type, fp32 or bf16");
                 grads[i] = *given[i];
             }
-        }
         const at::Tensor* workspace = maybe(a[15], "workspace must be a tensor");
-        at::Tensor own;
-        size_t ws_bytes = 0;
-        if (workspace != nullptr) {
-            ws_bytes = workspace->nbytes();
-        } else if ((ws_bytes = g_attn_bwd_ws(B, Nq, Nkv, H, D, kvl, mask != nullptr)) > 0) {
-            own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, q);
-            workspace = &own;
-        }
-        const dit_attn_bwd_strides_t st{strides4(q),        strides4(k),        strides4(v),        strides4(out), strides4(dout),
-                                        strides4(grads[0]), strides4(grads[1]), strides4(grads[2])};
         const dit_stream_t stream = stream_of(a[16]);
-        const dit_dtype_t gt = type == at::kFloat ? DIT_F32 : DIT_BF16;
-        int rc;
-        if (mask != nullptr)
-            rc = g_attn_bwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
-                                   dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, data<uint32_t>(mask),
-                                   mask->size(0) == 1 ? 0 : mask->stride(0), mask->stride(1), mask_rows, scale,
-                                   grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), gt,
-                                   data<void>(workspace), ws_bytes, stream);
-        else
-            rc = g_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
-                            dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, scale, grads[0].data_ptr(),
-                            grads[1].data_ptr(), grads[2].data_ptr(), gt, data<void>(workspace), ws_bytes, stream);
+        at::Tensor own;
+        const int rc = unlocked([&] {
+            for (int i = 0; i < 3; ++i)
+                if (given[i] == nullptr) grads[i] = fresh((i == 0 ? q : k).sizes(), type, q);
+            size_t ws_bytes = 0;
+            if (workspace != nullptr) {
+                ws_bytes = workspace->nbytes();
+            } else if ((ws_bytes = g_attn_bwd_ws(B, Nq, Nkv, H, D, kvl, mask != nullptr)) > 0) {
+                own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, q);
+                workspace = &own;
+            }
+            const dit_attn_bwd_strides_t st{strides4(q),        strides4(k),        strides4(v),        strides4(out), strides4(dout),
+                                            strides4(grads[0]), strides4(grads[1]), strides4(grads[2])};
+            const dit_dtype_t gt = type == at::kFloat ? DIT_F32 : DIT_BF16;
+            if (mask != nullptr)
+                return g_attn_bwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
+                                         dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, data<uint32_t>(mask),
+                                         mask->size(0) == 1 ? 0 : mask->stride(0), mask->stride(1), mask_rows, scale,
+                                         grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), gt,
+                                         data<void>(workspace), ws_bytes, stream);
+            return g_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
+                              dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, scale, grads[0].data_ptr(),
+                              grads[1].data_ptr(), grads[2].data_ptr(), gt, data<void>(workspace), ws_bytes, stream);
+        });
         return result(rc, {&grads[0], &grads[1], &grads[2]});
     });
 }
@@ -240,16 +249,19 @@ PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* given = maybe(a[5], "out must be a tensor");
         if (given != nullptr && (!bf16_or_f32(*given) || given->sizes() != x.sizes()))
             value_error("out must have x's shape, bf16 or fp32");
-        const at::Tensor y = given != nullptr ? *given
-                                              : fresh(x.sizes(), a[6] == Py_None ? x.scalar_type()
-                                                                                 : (integer(a[6]) ? at::kFloat : at::kBFloat16), x);
-        const at::IntArrayRef rows = x.sizes().slice(0, x.dim() - 1);
-        const at::Tensor rstd = fresh(rows, at::kFloat, x);
-        const at::Tensor mean = center ? fresh(rows, at::kFloat, x) : at::Tensor();
-        const dit_strides4_t sx = strides4(x), sy = strides4(y);
-        const int rc = g_norm_fwd(x.data_ptr(), code(x), &sx, r.B, r.N, r.H, r.C, data<float>(weight), data<float>(bias), groups,
-                                  eps, center, y.data_ptr(), code(y), &sy, center ? data<float>(&mean) : nullptr,
-                                  data<float>(&rstd), stream_of(a[7]));
+        const at::ScalarType type = a[6] == Py_None ? x.scalar_type() : (integer(a[6]) ? at::kFloat : at::kBFloat16);
+        const dit_stream_t stream = stream_of(a[7]);
+        at::Tensor y, mean, rstd;
+        if (given != nullptr) y = *given;
+        const int rc = unlocked([&] {
+            if (given == nullptr) y = fresh(x.sizes(), type, x);
+            const at::IntArrayRef rows = x.sizes().slice(0, x.dim() - 1);
+            rstd = fresh(rows, at::kFloat, x);
+            if (center) mean = fresh(rows, at::kFloat, x);
+            const dit_strides4_t sx = strides4(x), sy = strides4(y);
+            return g_norm_fwd(x.data_ptr(), code(x), &sx, r.B, r.N, r.H, r.C, data<float>(weight), data<float>(bias), groups, eps,
+                              center, y.data_ptr(), code(y), &sy, center ? data<float>(&mean) : nullptr, data<float>(&rstd), stream);
+        });
         return result(rc, {&y, center ? &mean : nullptr, &rstd});
     });
 }
@@ -273,29 +285,33 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (given != nullptr && (!is(*given, x.scalar_type()) || given->sizes() != x.sizes()))
             value_error("dx must have x's shape and type");
         const int groups = param_batches(r, {weight, dweight, dbias});
-        const at::Tensor dx = given != nullptr ? *given : fresh(x.sizes(), x.scalar_type(), x);
-        at::Tensor dw, db;
-        if (weight != nullptr && dweight == nullptr) {
-            dw = fresh(weight->sizes(), at::kFloat, x);
-            dweight = &dw;
-        }
-        if (weight != nullptr && dbias == nullptr && integer(a[5])) {
-            db = fresh(weight->sizes(), at::kFloat, x);
-            dbias = &db;
-        }
+        const bool own_dw = weight != nullptr && dweight == nullptr;
+        const bool own_db = weight != nullptr && dbias == nullptr && integer(a[5]) != 0;
         const at::Tensor* workspace = maybe(a[9], "workspace must be a tensor");
-        at::Tensor own;
-        size_t ws_bytes = workspace != nullptr ? workspace->nbytes() : 0;
-        if (workspace == nullptr && (dweight != nullptr || dbias != nullptr) &&
-            (ws_bytes = g_norm_bwd_ws(r.B, r.N, r.H, r.C, groups)) > 0) {
-            own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, x);
-            workspace = &own;
-        }
-        const dit_strides4_t sdy = strides4(dy), sx = strides4(x), sdx = strides4(dx);
-        const int rc = g_norm_bwd(dy.data_ptr(), code(dy), &sdy, x.data_ptr(), code(x), &sx, data<float>(mean),
-                                  data<float>(&rstd), data<float>(weight), r.B, r.N, r.H, r.C, groups, mean != nullptr,
-                                  dx.data_ptr(), &sdx, data<float>(dweight), data<float>(dbias), data<void>(workspace),
-                                  ws_bytes, stream_of(a[10]));
+        const dit_stream_t stream = stream_of(a[10]);
+        at::Tensor dx, dw, db, own;
+        if (given != nullptr) dx = *given;
+        const int rc = unlocked([&] {
+            if (given == nullptr) dx = fresh(x.sizes(), x.scalar_type(), x);
+            if (own_dw) {
+                dw = fresh(weight->sizes(), at::kFloat, x);
+                dweight = &dw;
+            }
+            if (own_db) {
+                db = fresh(weight->sizes(), at::kFloat, x);
+                dbias = &db;
+            }
+            size_t ws_bytes = workspace != nullptr ? workspace->nbytes() : 0;
+            if (workspace == nullptr && (dweight != nullptr || dbias != nullptr) &&
+                (ws_bytes = g_norm_bwd_ws(r.B, r.N, r.H, r.C, groups)) > 0) {
+                own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, x);
+                workspace = &own;
+            }
+            const dit_strides4_t sdy = strides4(dy), sx = strides4(x), sdx = strides4(dx);
+            return g_norm_bwd(dy.data_ptr(), code(dy), &sdy, x.data_ptr(), code(x), &sx, data<float>(mean), data<float>(&rstd),
+                              data<float>(weight), r.B, r.N, r.H, r.C, groups, mean != nullptr, dx.data_ptr(), &sdx,
+                              data<float>(dweight), data<float>(dbias), data<void>(workspace), ws_bytes, stream);
+        });
         return result(rc, {&dx, dweight, dbias});
     });
 }
@@ -351,12 +367,20 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* given = maybe(a[8], "out must be a tensor");
         if (given != nullptr && (!is(*given, x.scalar_type()) || given->sizes() != x.sizes()))
             value_error("out must have x's shape and type");
-        const at::Tensor y = given != nullptr ? *given : fresh(x.sizes(), x.scalar_type(), x);
-        const dit_strides4_t sx = strides4(x), sy = strides4(y);
-        const int rc = g_rope(x.data_ptr(), code(x), &sx, r.B, r.N, r.H, r.C, 2 * pairs,
-                              integer(a[3]) ? DIT_ROPE_HALF : DIT_ROPE_INTERLEAVED, data<const double>(&freq), axes.data(),
-                              extent(n_axes), data<const int32_t>(pos), pos_sb, integer(a[5]), static_cast<float>(real(a[6])),
-                              integer(a[7]) != 0, y.data_ptr(), &sy, stream_of(a[9]));
+        const int64_t offset = integer(a[5]);
+        const float mscale = static_cast<float>(real(a[6]));
+        const dit_rope_layout_t layout = integer(a[3]) ? DIT_ROPE_HALF : DIT_ROPE_INTERLEAVED;
+        const bool inverse = integer(a[7]) != 0;
+        const dit_stream_t stream = stream_of(a[9]);
+        const int axis_count = extent(n_axes);
+        at::Tensor y;
+        if (given != nullptr) y = *given;
+        const int rc = unlocked([&] {
+            if (given == nullptr) y = fresh(x.sizes(), x.scalar_type(), x);
+            const dit_strides4_t sx = strides4(x), sy = strides4(y);
+            return g_rope(x.data_ptr(), code(x), &sx, r.B, r.N, r.H, r.C, 2 * pairs, layout, data<const double>(&freq), axes.data(),
+                          axis_count, data<const int32_t>(pos), pos_sb, offset, mscale, inverse, y.data_ptr(), &sy, stream);
+        });
         return result(rc, {&y});
     });
 }

@@ -1,6 +1,10 @@
 """The training operators in corners of what their documentation allows that the
 other tests do not reach."""
+import ctypes
 import math
+import subprocess
+import threading
+import time
 from fractions import Fraction
 
 import pytest
@@ -159,3 +163,50 @@ def test_no_memory_left_has_its_own_type(dl):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert dl.rope(x[:1, :4], freq).shape == (1, 4, 64, 64)
+
+
+_WAITER = """
+#include <unistd.h>
+volatile int flag = 0;
+int wait_for_flag() { for (int i = 0; i < 3000; ++i) { if (flag) return 0; usleep(1000); } return 4; }
+"""
+
+
+def test_other_threads_run_while_a_call_waits(dl, tmp_path):
+    """The library's function is replaced by one that waits (3 s at most) for
+    another Python thread: a call that kept the interpreter's lock would wait in
+    vain, as it would for a full launch queue."""
+    from dit_long_sequence_gb300 import binding
+    src, lib = tmp_path / "waiter.c", tmp_path / "waiter.so"
+    src.write_text(_WAITER)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", str(src), "-o", str(lib)], check=True)
+    waiter = ctypes.CDLL(str(lib))
+    names = ("dit_attn_bwd", "dit_attn_bwd_masked", "dit_attn_bwd_workspace_bytes", "dit_layer_norm_fwd",
+             "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope")
+    real = [ctypes.cast(getattr(binding.raw(), n), ctypes.c_void_p).value for n in names]
+    wait = ctypes.cast(waiter.wait_for_flag, ctypes.c_void_p).value
+    flag = ctypes.c_int.in_dll(waiter, "flag")
+    x, w = wl.randn_bf16((1, 8, 2, 64), 64, DEV), torch.ones(64, device=DEV)
+    freq = dl.rope_inv_freq(64)[0]
+    o, lse = dl.attn_fwd(x, x, x, out_dtype=BF)
+    _, mean, rstd = dl.layer_norm_fwd(x, w)
+    bits = torch.full((1, 8, 4), -1, dtype=torch.int32, device=DEV)
+    dl.rope(x, freq)
+
+    def raise_flag():
+        time.sleep(0.05)
+        flag.value = 1
+    calls = {"dit_rope": lambda: dl.rope(x, freq), "dit_layer_norm_fwd": lambda: dl.layer_norm_fwd(x, w),
+             "dit_layer_norm_bwd": lambda: dl.layer_norm_bwd(x, x, mean, rstd, w),
+             "dit_attn_bwd": lambda: dl.attn_bwd(x, x, x, o, lse, x),
+             "dit_attn_bwd_masked": lambda: dl.attn_bwd_masked(x, x, x, o, lse, x, bits)}
+    for name, call in calls.items():
+        flag.value = 0
+        binding._calls.bind(*(wait if n == name else a for n, a in zip(names, real)))
+        t = threading.Thread(target=raise_flag)
+        try:
+            t.start()
+            call()      # (a wait that ran out is a DitError)
+        finally:
+            binding._calls.bind(*real)
+            t.join()
