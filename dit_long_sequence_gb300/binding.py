@@ -1,7 +1,8 @@
 """ctypes binding of libditattn.so (include/dit_attn.h).
 
 Argument marshalling only (for the training operators, whose small calls would
-be mostly marshalling, in the CPython extension csrc/py_calls.cpp): tensors are passed as device pointers with their
+be mostly marshalling, in the CPython extension csrc/py_calls.cpp, loaded at
+the first of them): tensors are passed as device pointers with their
 element strides and the current CUDA stream; every step of the computation
 runs in the library's kernels.  PyTorch supplies device memory and streams.
 There is no fallback: if the library is missing or a call fails, an exception
@@ -21,7 +22,7 @@ import os
 
 import torch
 
-from .build import CALLS as _CALLS_PATH
+from . import build as _build
 from .build import DEBUG_LIB as _DEBUG_LIB_PATH
 from .build import LIB as _PRODUCT_LIB_PATH
 
@@ -136,10 +137,11 @@ _lib = _declare(ctypes.CDLL(_LIB_PATH))
 
 def _load_calls():
     """The extension of csrc/py_calls.cpp, calling this library's functions."""
-    if not os.path.exists(_CALLS_PATH):
-        raise ImportError(f"dit_calls.so not found at {_CALLS_PATH}; build it first with "
+    path = _build.calls_path()
+    if not os.path.exists(path):
+        raise ImportError(f"the training operators' extension is not at {path}; build it first with "
                           "`python -m dit_long_sequence_gb300.build` (or __graft_entry__.build())")
-    loader = importlib.machinery.ExtensionFileLoader("dit_calls", _CALLS_PATH)
+    loader = importlib.machinery.ExtensionFileLoader("dit_calls", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dit_calls", loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
@@ -148,7 +150,26 @@ def _load_calls():
     return module
 
 
-_calls = _load_calls()
+class _Calls:
+    """The extension's functions, loaded when one is first asked for: the other
+    calls do without it (and without what it is built with)."""
+    _NAMES = ("attn_bwd", "norm_fwd", "norm_bwd", "rope", "bind")
+
+    def __getattr__(self, name):
+        if name not in self._NAMES:
+            raise AttributeError(name)
+        module = _load_calls()
+        for n in self._NAMES:
+            setattr(self, n, getattr(module, n))     # found without coming here from now on
+        return getattr(module, name)
+
+
+_calls = _Calls()
+
+
+def load_calls():
+    """Loads the training operators' extension now; ImportError if it is missing."""
+    return _calls.bind
 
 
 def load_debug_library():
