@@ -589,11 +589,20 @@ def attn_bwd_workspace_bytes(B: int, Nq: int, Nkv: int, H: int, D: int, key_vali
                                                  1 if masked else 0))
 
 
+def _as_stream(stream):
+    """A torch stream of a given one (any object with a cuda_stream).  The default
+    stream's handle is 0, of which ExternalStream would make a stream of its own."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream.cuda_stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
 def _workspace_for(stream, nbytes: int) -> torch.Tensor:
     """A call's own workspace on a stream that was given: of that stream's
     memory, so that freeing it behind the call does not hand it to another
     stream's work while the kernels run."""
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream.cuda_stream)):
+    with torch.cuda.stream(_as_stream(stream)):
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 

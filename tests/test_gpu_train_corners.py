@@ -5,6 +5,7 @@ import math
 import subprocess
 import threading
 import time
+import types
 from fractions import Fraction
 
 import pytest
@@ -150,6 +151,54 @@ def test_tiles_that_end_inside_a_warps_rows(dl, Nq, Nkv, kvl, D, grad_dtype):
 
 
 # ---------------------------------------------------------------- calls
+
+def _stream_of_memory(t):
+    """The stream whose pool a tensor's memory belongs to."""
+    at = t.data_ptr()
+    found = [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"]]
+    assert len(found) == 1
+    return found[0]
+
+
+@pytest.fixture
+def step(dl):
+    x, do = wl.randn_bf16((2, 200, 2, 64), 61, DEV), wl.randn_bf16((2, 200, 2, 64), 62, DEV)
+    w, freq = torch.ones(64, device=DEV), dl.rope_inv_freq(64)[0]
+    o, lse = dl.attn_fwd(x, x, x, out_dtype=BF)
+    m = torch.ones((1, 200, 200), dtype=torch.bool)
+    bits = wl.pack_mask_bits(m).to(DEV)
+    _, mean, rstd = dl.layer_norm_fwd(x, w)
+    torch.cuda.synchronize()
+
+    def calls(**kw):
+        return [*dl.layer_norm_fwd(x, w, **kw), *dl.layer_norm_bwd(do, x, mean, rstd, w, **kw), dl.rope(x, freq, **kw),
+                *dl.attn_bwd(x, x, x, o, lse, do, **kw), *dl.attn_bwd_masked(x, x, x, o, lse, do, bits, **kw)]
+    return calls
+
+
+def test_the_default_stream_given_from_beside_another(dl, step, monkeypatch):
+    from dit_long_sequence_gb300 import binding
+    want = step()
+    real, spaces = binding._calls, []
+
+    def spy(name, at):
+        def f(*a):
+            spaces.append(a[at])
+            return getattr(real, name)(*a)
+        return f
+    monkeypatch.setattr(binding, "_calls", types.SimpleNamespace(attn_bwd=spy("attn_bwd", 15), norm_bwd=spy("norm_bwd", 9),
+                                                               norm_fwd=real.norm_fwd, rope=real.rope))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plain = types.SimpleNamespace(cuda_stream=0)        # any object with a handle
+    for given in (torch.cuda.default_stream(), plain):
+        spaces.clear()
+        with torch.cuda.stream(side):
+            got = step(stream=given)
+        torch.cuda.synchronize()
+        assert len(spaces) == 3 and {_stream_of_memory(t) for t in spaces} == {0}
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
 
 def test_no_memory_left_has_its_own_type(dl):
     x = torch.empty((1, 1, 1, 64), dtype=BF, device=DEV).expand(64, 4096, 64, 64)      # a result of 2 GB
