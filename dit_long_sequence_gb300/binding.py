@@ -598,18 +598,37 @@ def _as_stream(stream):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
-def _workspace_for(stream, nbytes: int) -> torch.Tensor:
-    """A call's own workspace on a stream that was given: of that stream's
-    memory, so that freeing it behind the call does not hand it to another
-    stream's work while the kernels run."""
+def _launch(function, args, stream, given, workspace_bytes=None):
+    """function(*args, stream) of the extension: (status, results).
+
+    What a call on a given stream allocates is that stream's memory: a workspace
+    (the last of `args` where there is one), freed when the call returns, and a
+    result, dropped at any time, must not be handed to the current stream's work
+    while the given stream writes it, nor be memory that the current stream still
+    reads.  Results (those not among `given`) count as used by the current stream
+    too, which reads them once it has waited."""
+    if stream is None:
+        return function(*args, _stream_ptr(None))
+    handle, here = int(stream.cuda_stream), torch.cuda.current_stream()
+    if handle == here.cuda_stream:
+        return function(*args, handle)
     with torch.cuda.stream(_as_stream(stream)):
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        if workspace_bytes is not None and args[-1] is None:
+            args = (*args[:-1], torch.empty(workspace_bytes(), dtype=torch.uint8, device="cuda"))
+        status, *results = function(*args, handle)
+    for t in results:
+        if t is not None and not any(t is g for g in given):
+            t.record_stream(here)
+    return (status, *results)
 
 
-def _attn_bwd_workspace_for(stream, q, k, key_valid_len, masked):
-    (B, Nq, H, D), Nkv = q.shape, k.shape[1]
-    return _workspace_for(stream, attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, Nkv if key_valid_len is None else key_valid_len,
-                                                           masked))
+def _attn_bwd_call(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv, grad_dtype,
+                   workspace, stream):
+    def workspace_bytes():
+        (B, Nq, H, D), Nkv = q.shape, k.shape[1]
+        return attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, Nkv if key_valid_len is None else key_valid_len, mask_bits is not None)
+    return _launch(_calls.attn_bwd, (q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
+                                     _is_fp32(grad_dtype), workspace), stream, (dq, dk, dv), workspace_bytes)
 
 
 def _is_fp32(dtype: torch.dtype) -> bool:
@@ -633,10 +652,8 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     that of lse.  dq [B, Nq, H, D], dk and dv [B, Nkv, H, D] may be given (e.g.
     views of one fused [B, N, 3, H, D] gradient) or are allocated in grad_dtype;
     keys past key_valid_len get zeros.  Returns (dq, dk, dv)."""
-    if stream is not None and workspace is None:
-        workspace = _attn_bwd_workspace_for(stream, q, k, key_valid_len, False)
-    rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv,
-                                 _is_fp32(grad_dtype), workspace, _stream_ptr(stream))
+    rc, *grads = _attn_bwd_call(q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv, grad_dtype,
+                                workspace, stream)
     if rc != DIT_OK:
         raise DitError(rc, "dit_attn_bwd")
     return tuple(grads)
@@ -651,10 +668,8 @@ def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
     the forward call's mask_bits and mask_rows."""
     if mask_bits is None:
         raise ValueError("mask_bits is missing")
-    if stream is not None and workspace is None:
-        workspace = _attn_bwd_workspace_for(stream, q, k, key_valid_len, True)
-    rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
-                                 _is_fp32(grad_dtype), workspace, _stream_ptr(stream))
+    rc, *grads = _attn_bwd_call(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
+                                grad_dtype, workspace, stream)
     if rc != DIT_OK:
         raise DitError(rc, "dit_attn_bwd_masked")
     return tuple(grads)
@@ -671,8 +686,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     (modulation).  Returns (y, mean, rstd): y in out_dtype (default x's; fp32 x
     may give bf16 y), mean (None without center) and rstd fp32 without the
     channel dimension."""
-    rc, y, mean, rstd = _calls.norm_fwd(x, weight, bias, eps, center, out,
-                                        None if out_dtype is None else _is_fp32(out_dtype), _stream_ptr(stream))
+    rc, y, mean, rstd = _launch(_calls.norm_fwd, (x, weight, bias, eps, center, out,
+                                                  None if out_dtype is None else _is_fp32(out_dtype)), stream, (out,))
     if rc != DIT_OK:
         raise DitError(rc, "dit_layer_norm_fwd")
     return y, mean, rstd
@@ -693,15 +708,15 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor | None,
     in the forward call.  Returns (dx, dweight, dbias): dx in x's type; dweight
     and dbias fp32 in weight's shape, None without a weight (dbias also without
     has_bias) unless a tensor to fill is given."""
-    if stream is not None and workspace is None:
+    def workspace_bytes():
         B, N, H, C = x.shape if x.dim() == 4 else (x.shape[0], x.shape[1], 1, x.shape[-1])
         sets = B if any(t is not None and t.dim() == 2 for t in (weight, dweight, dbias)) else 1
-        workspace = _workspace_for(stream, layer_norm_bwd_workspace_bytes(B, N, H, C, sets))
-    rc, dx, dw, db = _calls.norm_bwd(dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace,
-                                     _stream_ptr(stream))
+        return layer_norm_bwd_workspace_bytes(B, N, H, C, sets)
+    rc, *grads = _launch(_calls.norm_bwd, (dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace), stream,
+                         (dx, dweight, dbias), workspace_bytes)
     if rc != DIT_OK:
         raise DitError(rc, "dit_layer_norm_bwd")
-    return dx, dw, db
+    return tuple(grads)
 
 
 def rope_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -737,8 +752,8 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions: torch.Tensor | None
     axis.  inverse turns back (the gradient).  out may be x."""
     if layout not in _ROPE_LAYOUTS:
         raise ValueError('layout must be "interleaved" or "half"')
-    rc, y = _calls.rope(x, inv_freq, positions, _ROPE_LAYOUTS[layout], axis_pairs, offset, mscale, inverse, out,
-                        _stream_ptr(stream))
+    rc, y = _launch(_calls.rope, (x, inv_freq, positions, _ROPE_LAYOUTS[layout], axis_pairs, offset, mscale, inverse, out),
+                    stream, (out,))
     if rc != DIT_OK:
         raise DitError(rc, "dit_rope")
     return y

@@ -176,6 +176,31 @@ def step(dl):
     return calls
 
 
+def test_results_of_a_given_stream_are_that_streams_memory(dl, step):
+    """A result that is dropped early must not be handed out to the current
+    stream's work while the other stream still writes it, nor may a result reused
+    by the other stream be one that the current stream still reads."""
+    want = step()
+    side = torch.cuda.Stream()
+    got = step(stream=side)
+    assert {_stream_of_memory(t) for t in got} == {side.cuda_stream}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # dropped while the current stream still has work with it: the given stream does not get it back
+    torch.cuda._sleep(200_000_000)
+    held = {t.data_ptr() for t in got}
+    del got
+    again = step(stream=side)
+    torch.cuda.current_stream().synchronize()
+    assert not held & {t.data_ptr() for t in again}
+    torch.cuda.synchronize()
+    # a stream that is the current one is like none
+    with torch.cuda.stream(side):
+        same = step(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(same, want))
+
+
 def test_the_default_stream_given_from_beside_another(dl, step, monkeypatch):
     from dit_long_sequence_gb300 import binding
     want = step()
@@ -198,6 +223,17 @@ def test_the_default_stream_given_from_beside_another(dl, step, monkeypatch):
         torch.cuda.synchronize()
         assert len(spaces) == 3 and {_stream_of_memory(t) for t in spaces} == {0}
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_given_results_on_a_given_stream_stay_the_callers(dl):
+    x = wl.randn_bf16((1, 50, 2, 64), 63, DEV)
+    freq = dl.rope_inv_freq(64)[0]
+    out = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert dl.rope(x, freq, out=out, stream=side) is out
+    torch.cuda.synchronize()
+    assert torch.equal(out, dl.rope(x, freq))
 
 
 def test_no_memory_left_has_its_own_type(dl):
