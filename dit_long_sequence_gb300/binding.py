@@ -598,23 +598,22 @@ def _as_stream(stream):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
-def _launch(function, args, stream, given, workspace_bytes=None):
-    """function(*args, stream) of the extension: (status, results).
+def _on_stream(function, args, stream, given, workspace_bytes=None):
+    """function(*args, stream) of the extension on a stream that was given:
+    (status, results).
 
-    What a call on a given stream allocates is that stream's memory: a workspace
-    (the last of `args` where there is one), freed when the call returns, and a
-    result, dropped at any time, must not be handed to the current stream's work
+    What it allocates is that stream's memory: a workspace (the last of `args`
+    where there is one, of workspace_bytes(args)), freed when the call returns, and
+    a result, dropped at any time, must not be handed to the current stream's work
     while the given stream writes it, nor be memory that the current stream still
     reads.  Results (those not among `given`) count as used by the current stream
     too, which reads them once it has waited."""
-    if stream is None:
-        return function(*args, _stream_ptr(None))
     handle, here = int(stream.cuda_stream), torch.cuda.current_stream()
     if handle == here.cuda_stream:
         return function(*args, handle)
     with torch.cuda.stream(_as_stream(stream)):
         if workspace_bytes is not None and args[-1] is None:
-            args = (*args[:-1], torch.empty(workspace_bytes(), dtype=torch.uint8, device="cuda"))
+            args = (*args[:-1], torch.empty(workspace_bytes(args), dtype=torch.uint8, device="cuda"))
         status, *results = function(*args, handle)
     for t in results:
         if t is not None and not any(t is g for g in given):
@@ -622,13 +621,17 @@ def _launch(function, args, stream, given, workspace_bytes=None):
     return (status, *results)
 
 
-def _attn_bwd_call(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv, grad_dtype,
-                   workspace, stream):
-    def workspace_bytes():
-        (B, Nq, H, D), Nkv = q.shape, k.shape[1]
-        return attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, Nkv if key_valid_len is None else key_valid_len, mask_bits is not None)
-    return _launch(_calls.attn_bwd, (q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
-                                     _is_fp32(grad_dtype), workspace), stream, (dq, dk, dv), workspace_bytes)
+def _attn_bwd_space(args):
+    q, k, mask_bits, key_valid_len = args[0], args[1], args[7], args[9]
+    (B, Nq, H, D), Nkv = q.shape, k.shape[1]
+    return attn_bwd_workspace_bytes(B, Nq, Nkv, H, D, Nkv if key_valid_len is None else key_valid_len, mask_bits is not None)
+
+
+def _norm_bwd_space(args):
+    x, parameters = args[1], (args[4], args[7], args[8])
+    B, N, H, C = x.shape if x.dim() == 4 else (x.shape[0], x.shape[1], 1, x.shape[-1])
+    sets = B if any(t is not None and t.dim() == 2 for t in parameters) else 1
+    return layer_norm_bwd_workspace_bytes(B, N, H, C, sets)
 
 
 def _is_fp32(dtype: torch.dtype) -> bool:
@@ -652,8 +655,12 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     that of lse.  dq [B, Nq, H, D], dk and dv [B, Nkv, H, D] may be given (e.g.
     views of one fused [B, N, 3, H, D] gradient) or are allocated in grad_dtype;
     keys past key_valid_len get zeros.  Returns (dq, dk, dv)."""
-    rc, *grads = _attn_bwd_call(q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv, grad_dtype,
-                                workspace, stream)
+    if stream is None:
+        rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv,
+                                     _is_fp32(grad_dtype), workspace, _stream_ptr(None))
+    else:
+        args = (q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv, _is_fp32(grad_dtype), workspace)
+        rc, *grads = _on_stream(_calls.attn_bwd, args, stream, (dq, dk, dv), _attn_bwd_space)
     if rc != DIT_OK:
         raise DitError(rc, "dit_attn_bwd")
     return tuple(grads)
@@ -668,8 +675,12 @@ def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
     the forward call's mask_bits and mask_rows."""
     if mask_bits is None:
         raise ValueError("mask_bits is missing")
-    rc, *grads = _attn_bwd_call(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
-                                grad_dtype, workspace, stream)
+    if stream is None:
+        rc, *grads = _calls.attn_bwd(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv,
+                                     _is_fp32(grad_dtype), workspace, _stream_ptr(None))
+    else:
+        args = (q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale, dq, dk, dv, _is_fp32(grad_dtype), workspace)
+        rc, *grads = _on_stream(_calls.attn_bwd, args, stream, (dq, dk, dv), _attn_bwd_space)
     if rc != DIT_OK:
         raise DitError(rc, "dit_attn_bwd_masked")
     return tuple(grads)
@@ -686,8 +697,11 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     (modulation).  Returns (y, mean, rstd): y in out_dtype (default x's; fp32 x
     may give bf16 y), mean (None without center) and rstd fp32 without the
     channel dimension."""
-    rc, y, mean, rstd = _launch(_calls.norm_fwd, (x, weight, bias, eps, center, out,
-                                                  None if out_dtype is None else _is_fp32(out_dtype)), stream, (out,))
+    fp32 = None if out_dtype is None else _is_fp32(out_dtype)
+    if stream is None:
+        rc, y, mean, rstd = _calls.norm_fwd(x, weight, bias, eps, center, out, fp32, _stream_ptr(None))
+    else:
+        rc, y, mean, rstd = _on_stream(_calls.norm_fwd, (x, weight, bias, eps, center, out, fp32), stream, (out,))
     if rc != DIT_OK:
         raise DitError(rc, "dit_layer_norm_fwd")
     return y, mean, rstd
@@ -708,15 +722,14 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor | None,
     in the forward call.  Returns (dx, dweight, dbias): dx in x's type; dweight
     and dbias fp32 in weight's shape, None without a weight (dbias also without
     has_bias) unless a tensor to fill is given."""
-    def workspace_bytes():
-        B, N, H, C = x.shape if x.dim() == 4 else (x.shape[0], x.shape[1], 1, x.shape[-1])
-        sets = B if any(t is not None and t.dim() == 2 for t in (weight, dweight, dbias)) else 1
-        return layer_norm_bwd_workspace_bytes(B, N, H, C, sets)
-    rc, *grads = _launch(_calls.norm_bwd, (dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace), stream,
-                         (dx, dweight, dbias), workspace_bytes)
+    if stream is None:
+        rc, gx, gw, gb = _calls.norm_bwd(dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace, _stream_ptr(None))
+    else:
+        args = (dy, x, mean, rstd, weight, has_bias, dx, dweight, dbias, workspace)
+        rc, gx, gw, gb = _on_stream(_calls.norm_bwd, args, stream, (dx, dweight, dbias), _norm_bwd_space)
     if rc != DIT_OK:
         raise DitError(rc, "dit_layer_norm_bwd")
-    return tuple(grads)
+    return gx, gw, gb
 
 
 def rope_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -752,8 +765,11 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions: torch.Tensor | None
     axis.  inverse turns back (the gradient).  out may be x."""
     if layout not in _ROPE_LAYOUTS:
         raise ValueError('layout must be "interleaved" or "half"')
-    rc, y = _launch(_calls.rope, (x, inv_freq, positions, _ROPE_LAYOUTS[layout], axis_pairs, offset, mscale, inverse, out),
-                    stream, (out,))
+    half = _ROPE_LAYOUTS[layout]
+    if stream is None:
+        rc, y = _calls.rope(x, inv_freq, positions, half, axis_pairs, offset, mscale, inverse, out, _stream_ptr(None))
+    else:
+        rc, y = _on_stream(_calls.rope, (x, inv_freq, positions, half, axis_pairs, offset, mscale, inverse, out), stream, (out,))
     if rc != DIT_OK:
         raise DitError(rc, "dit_rope")
     return y
