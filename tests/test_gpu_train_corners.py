@@ -133,6 +133,40 @@ def test_rows_without_a_key_contribute_nothing_whatever_they_hold(dl, D, junk):
     assert bool((got[1][0][empty] == 0).all())
 
 
+@pytest.mark.parametrize("kind", ["frames", "holes"])
+@pytest.mark.parametrize("B,Nq,Nkv,H,D,rows,kvl", [(2, 300, 300, 2, 64, 300, 300), (1, 513, 1000, 1, 128, 513, 999), (2, 200, 77, 3, 64, 150, 70)])
+def test_a_mask_with_a_gradient_of_the_lse_and_fp32_results(dl, kind, B, Nq, Nkv, H, D, rows, kvl):
+    q, k, v, dout, g = _inputs(B, Nq, Nkv, H, D, 17 + Nq)
+    m = _mask(kind, B, rows, kvl, g)
+    allow = _allow(B, Nq, Nkv, kvl, m)
+    out, lse = _forward(q, k, v, 0.11, allow, F)
+    dlse = torch.randn((B, H, Nq), generator=g, device=DEV)
+    grads = dl.attn_bwd_masked(q, k, v, out, lse, dout, wl.pack_mask_bits(m).to(DEV), dlse=dlse, key_valid_len=kvl, scale=0.11,
+                               grad_dtype=F)
+    torch.cuda.synchronize()
+    _check(grads, q, k, v, out, lse, dout, 0.11, allow, dlse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("grad_dtype", [BF, F])
+@pytest.mark.parametrize("N,H", [(333, 3), (1700, 40)])      # items in pieces, whole items
+def test_gradients_on_16_byte_boundaries(dl, D, grad_dtype, N, H):
+    """Rows a 16-byte multiple apart that is none of 32 bytes: the same bits as
+    packed, and nothing beside the rows is touched."""
+    B = 1
+    q, k, v, dout, _ = _inputs(B, N, N, H, D, 19)
+    out, lse = dl.attn_fwd(q, k, v, key_valid_len=N - 3)
+    want = dl.attn_bwd(q, k, v, out, lse, dout, key_valid_len=N - 3, grad_dtype=grad_dtype)
+    step = D + (8 if grad_dtype == BF else 4)
+    bufs = [torch.full((B, N, H, step), -7.0, dtype=grad_dtype, device=DEV) for _ in range(3)]
+    views = [b[..., step - D:] for b in bufs]
+    assert all(t.data_ptr() % 32 == 16 for t in views)
+    dl.attn_bwd(q, k, v, out, lse, dout, key_valid_len=N - 3, dq=views[0], dk=views[1], dv=views[2])
+    torch.cuda.synchronize()
+    for b, t, w in zip(bufs, views, want):
+        assert torch.equal(t, w) and bool((b[..., :step - D] == -7.0).all())
+
+
 @pytest.mark.parametrize("Nq,Nkv,kvl", [(1, 1, 1), (33, 65, 64), (127, 129, 97), (161, 255, 250), (1000, 31, 31)])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("grad_dtype", [BF, F])
