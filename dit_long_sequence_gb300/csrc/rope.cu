@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         int axis = 0;
 #pragma unroll
         for (int k = 0; k + 1 < kRopeMaxAxes; ++k) axis += (k + 1 < a.axes && pr >= a.axis_end[k]) ? 1 : 0;
-        const int64_t at = a.pos != nullptr ? static_cast<int64_t>(__ldg(a.pos + b * a.pos_sb + static_cast<int64_t>(n0 + n) * a.axes + axis))
-                                            : static_cast<int64_t>(n0 + n);
-        const uint64_t pos = static_cast<uint64_t>(a.offset) + static_cast<uint64_t>(at);      // modulo 2^64, as the product
+        const uint64_t offset = static_cast<uint64_t>(a.offset);      // (the sum modulo 2^64, as the product)
+        const uint64_t pos = a.pos != nullptr ? offset + static_cast<int64_t>(__ldg(a.pos + b * a.pos_sb + static_cast<int64_t>(n0 + n) * a.axes + axis))
+                                              : offset + static_cast<uint32_t>(n0 + n);
         const uint64_t t = pos * turns[pr] + 0x80000000ull;
         float s, c;
         sincos_turns(static_cast<uint32_t>(t >> 32), s, c);
