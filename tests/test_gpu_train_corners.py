@@ -329,3 +329,46 @@ def test_other_threads_run_while_a_call_waits(dl, tmp_path):
         finally:
             binding._calls.bind(*real)
             t.join()
+
+
+def test_a_given_stream_inside_a_capture(dl, step):
+    """A side stream that the captured one forks and joins: its results are of the
+    graph's memory, dropped ones among them, and replays give the same bits."""
+    want = step()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        step(stream=side)
+        got = step(stream=side)
+        main.wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(3):
+        for t in got + copies:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(got, want, copies))
+
+
+def test_threads_with_streams_of_their_own(dl, step):
+    want = step()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = step()
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    wrong.append(1)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
