@@ -6,7 +6,8 @@ the first of them): tensors are passed as device pointers with their
 element strides and the current CUDA stream; every step of the computation
 runs in the library's kernels.  PyTorch supplies device memory and streams.
 There is no fallback: if the library is missing or a call fails, an exception
-is raised.
+is raised.  No call is part of an autograd graph: results carry no gradient
+function, and gradients are what the *_bwd calls (rope: inverse) return.
 
 With the environment variable DIT_ATTN_DEBUG=1 at import, the binding loads
 the debug library instead (libditattn_debug.so: the same kernels with

@@ -59,7 +59,7 @@
 // 16 softmax warps of half as many columns were 5 to 10% slower.
 //
 // Rows without an allowed key have LSE = -inf; they, and the rows past Nq, get
-// P = 0 through a stored -LSE of -inf.  Keys past kv_len are zero-filled by the
+// P = 0 through a stored -LSE of -inf (and a stored delta of 0).  Keys past kv_len are zero-filled by the
 // tensor maps and masked (query item) or not stored (key item: their gradients
 // are written as zeros).
 #include <cuda.h>

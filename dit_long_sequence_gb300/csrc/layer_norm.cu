@@ -238,7 +238,7 @@ struct RowGroup {
     int tpr, t, id;             // threads per row, index in the row, row slot of the block
     int warps;                  // warps of a row (1 when tpr <= 32), at most 16
     int span;                   // the next power of two: across() adds over that many lanes
-    float2* buf;                // [2][kSums], zeroed
+    float2* buf;                // [2][kSums]; zeroed for across_two(), which adds a row's padding too
     int pitch;                  // a row's place in it: its warps, rounded up to even
     int flip;
     __device__ RowGroup(int tpr_, float2* b)

@@ -20,7 +20,7 @@
 // bytes a token.  A block takes `tokens` tokens: the cos/sin of their pairs
 // are computed once into shared memory and used by all heads, while the first
 // loads of x are already in flight.  Measured, bf16, interleaved, 24,576 tokens
-// x 64 heads x 128: 123 us, 6.5 TB/s (97% of a plain copy); the half layout 121
+// x 64 heads x 128: 125 us, 6.4 TB/s (95% of a plain copy); the half layout 123
 // us.  Two loads of a thread in flight were 134 us interleaved, eight 122; half
 // layout units of two loads each: two in flight 121 us, four 139, eight 159.
 // Blocks of 4 or 8 rounds were no faster, and slower in the half layout.

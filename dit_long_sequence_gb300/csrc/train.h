@@ -15,8 +15,9 @@ namespace dit {
 
 // n / d and n % d for 0 <= n < 2^31 and a fixed 1 <= d < 2^31 by one multiply:
 // with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1,
-// n / d = (umulhi(n, m) + n) >> s (round-up reciprocal; the sum stays below
-// 2^32 because umulhi(n, m) <= n < 2^31).
+// n / d = (umulhi(n, m) + n) >> s: the round-up reciprocal of Granlund and
+// Montgomery, "Division by invariant integers using multiplication" (1994); the
+// sum stays below 2^32 because umulhi(n, m) <= n < 2^31.
 struct FastDiv {
     uint32_t d, m, s;
     FastDiv() : d(1), m(1), s(0) {}
