@@ -188,6 +188,24 @@ dit_status_t encode_view(CUtensorMap* map, const void* base, const dit_strides4_
     return r == CUDA_SUCCESS ? DIT_OK : DIT_ERR_INVALID_ARG;
 }
 
+dit_status_t encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                          const uint32_t* box) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return DIT_ERR_CUDA;
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        one[i] = 1;
+        if (i > 0) st[i - 1] = strides[i - 1];
+    }
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DIT_OK : DIT_ERR_INVALID_ARG;
+}
+
 dit_status_t check_tma_strides(const dit_strides4_t& s, bool fp8) {
     if (s.d != 1) return DIT_ERR_UNSUPPORTED;
     const int64_t st[3] = {s.b, s.n, s.h};

@@ -19,40 +19,23 @@
 #include "internal.h"
 #include "rope_turns.h"
 #include "train.h"
+#include "window_plan.h"
 
 using namespace dit;
 
 namespace {
-
-// Strides of an output: d contiguous, no two rows of a dimension at one place.
-dit_status_t check_out_strides(const dit_strides4_t& s, int64_t B, int64_t N, int64_t H) {
-    if (s.d != 1) return DIT_ERR_UNSUPPORTED;
-    const int64_t st[3] = {s.b, s.n, s.h}, ext[3] = {B, N, H};
-    for (int i = 0; i < 3; ++i)
-        if (st[i] < 0 || st[i] >= (int64_t(1) << 39) || (ext[i] > 1 && st[i] == 0)) return DIT_ERR_INVALID_ARG;
-    return DIT_OK;
-}
-// Strides of an input read with plain loads (0 broadcasts).
-dit_status_t check_in_strides(const dit_strides4_t& s) {
-    if (s.d != 1) return DIT_ERR_UNSUPPORTED;
-    for (int64_t x : {s.b, s.n, s.h})
-        if (x < 0 || x >= (int64_t(1) << 39)) return DIT_ERR_INVALID_ARG;
-    return DIT_OK;
-}
-bool multiple(const dit_strides4_t& s, int64_t k) { return s.b % k == 0 && s.n % k == 0 && s.h % k == 0; }
-bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-bool known(dit_dtype_t t) { return t == DIT_BF16 || t == DIT_F32; }
-uintptr_t size_of(dit_dtype_t t) { return t == DIT_F32 ? 4 : 2; }
-// Two views that begin at one address place every row alike.
-bool same_rows(const dit_strides4_t& s, const dit_strides4_t& t, int B, int N, int H) {
-    return (B == 1 || s.b == t.b) && (N == 1 || s.n == t.n) && (H == 1 || s.h == t.h);
-}
 
 struct BwdMask {
     const uint32_t* bits;
     int64_t batch_stride, row_stride;
     int rows;
 };
+// A window, the K/V heads and the position of query 0 (none: all keys, a head each).
+struct BwdWindow {
+    Window w;
+    int Hkv, offset;
+};
+constexpr int64_t kMaxWindowTokens = int64_t(1) << 29;
 
 int64_t occ_bytes(int B, const BwdPlan& p) {
     return (static_cast<int64_t>(B) * ((p.q_tiles + 1) / 2) * ((p.kv_tiles + 31) / 32) * 4 + 255) / 256 * 256;
@@ -60,9 +43,9 @@ int64_t occ_bytes(int B, const BwdPlan& p) {
 
 dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const void* out, dit_dtype_t out_dtype,
                              const float* lse, const void* dout, const float* dlse, const dit_attn_bwd_strides_t* st,
-                             int B, int Nq, int Nkv, int H, int D, int key_valid_len, const BwdMask* mask, float scale,
-                             void* dq, void* dk, void* dv, dit_dtype_t grad_dtype, void* workspace,
-                             size_t workspace_bytes, dit_stream_t stream) {
+                             int B, int Nq, int Nkv, int H, int D, int key_valid_len, const BwdMask* mask,
+                             const BwdWindow* window, float scale, void* dq, void* dk, void* dv, dit_dtype_t grad_dtype,
+                             void* workspace, size_t workspace_bytes, dit_stream_t stream) {
     if (st == nullptr) return DIT_ERR_INVALID_ARG;
     if (B < 0 || Nq < 0 || Nkv < 0 || H < 0) return DIT_ERR_INVALID_ARG;
     if (key_valid_len < 0 || key_valid_len > Nkv) return DIT_ERR_INVALID_ARG;
@@ -71,6 +54,7 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     if (D != 64 && D != 128) return DIT_ERR_UNSUPPORTED;
     if (B > 65535 || H > 65535) return DIT_ERR_UNSUPPORTED;
     if (B == 0 || H == 0 || (Nq == 0 && Nkv == 0)) return DIT_OK;
+    const int Hkv = window != nullptr ? window->Hkv : H;
     const bool any_keys = key_valid_len > 0 && Nq > 0;   // otherwise every gradient is zero
     if (Nq > 0 && dq == nullptr) return DIT_ERR_INVALID_ARG;
     if (Nkv > 0 && (dk == nullptr || dv == nullptr)) return DIT_ERR_INVALID_ARG;
@@ -83,8 +67,8 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
         if (!multiple(st->dq, g_align) || !aligned16(dq)) return DIT_ERR_ALIGNMENT;
     }
     if (Nkv > 0) {
-        if ((e = check_out_strides(st->dk, B, Nkv, H)) != DIT_OK) return e;
-        if ((e = check_out_strides(st->dv, B, Nkv, H)) != DIT_OK) return e;
+        if ((e = check_out_strides(st->dk, B, Nkv, Hkv)) != DIT_OK) return e;
+        if ((e = check_out_strides(st->dv, B, Nkv, Hkv)) != DIT_OK) return e;
         if (!multiple(st->dk, g_align) || !multiple(st->dv, g_align) || !aligned16(dk) || !aligned16(dv))
             return DIT_ERR_ALIGNMENT;
     }
@@ -109,7 +93,9 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DIT_ERR_CUDA;
-    BwdPlan p = plan_attn_bwd(B, Nq, Nkv, H, D, any_keys ? key_valid_len : 0, device_sm_count(dev));
+    const int sms = device_sm_count(dev), keys = any_keys ? key_valid_len : 0;
+    BwdPlan p = window != nullptr ? plan_attn_bwd_window(B, Nq, Nkv, H, Hkv, D, keys, window->w, window->offset, sms)
+                                  : plan_attn_bwd(B, Nq, Nkv, H, D, keys, sms);
     const bool with_mask = mask != nullptr && mask->rows > 0 && any_keys;
     if (with_mask && p.q_whole > 0) {      // items of unknown lengths: none of the last ones is cut
         p.q_whole = p.query_items;
@@ -132,8 +118,8 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
         return e;
     if (any_keys) {
         if ((e = encode_view(&tq, q, st->q, B, Nq, H, D)) != DIT_OK) return e;
-        if ((e = encode_view(&tk, k, st->k, B, key_valid_len, H, D)) != DIT_OK) return e;
-        if ((e = encode_view(&tv, v, st->v, B, key_valid_len, H, D)) != DIT_OK) return e;
+        if ((e = encode_view(&tk, k, st->k, B, key_valid_len, Hkv, D)) != DIT_OK) return e;
+        if ((e = encode_view(&tv, v, st->v, B, key_valid_len, Hkv, D)) != DIT_OK) return e;
         if ((e = encode_view(&tdo, dout, st->dout, B, Nq, H, D)) != DIT_OK) return e;
     }
     AttnBwdArgs a{};
@@ -163,12 +149,24 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     a.f_kv = p.f_kv;
     a.f_q = p.f_q;
     a.q_whole = static_cast<int>(p.q_whole);
-    a.n_kv_items = static_cast<int>(p.key_items * p.f_kv);
+    a.Hkv = Hkv;
+    a.group = H / Hkv;
+    a.kv_cut = p.kv_cut;
+    a.n_kv_cut = static_cast<int>(static_cast<int64_t>(B) * Hkv * p.kv_cut * p.f_kv);
+    a.n_kv_items = a.n_kv_cut + static_cast<int>(static_cast<int64_t>(B) * Hkv * (p.kv_out_tiles - p.kv_cut));
+    if (window != nullptr) {
+        a.windowed = true;
+        a.window = window->w;
+        a.offset = window->offset;
+    }
     a.n_q_items = static_cast<int>(p.q_whole + (p.query_items - p.q_whole) * p.f_q);
     auto div = [](int64_t d) { return FastDiv(static_cast<uint32_t>(d > 0 ? d : 1)); };
     a.div_f_kv = div(p.f_kv);
     a.div_f_q = div(p.f_q);
-    a.div_kv_tiles = div(p.kv_out_tiles);
+    a.div_kv_tiles = div(window != nullptr ? p.kv_out_tiles - p.kv_cut : p.kv_out_tiles);
+    a.div_kv_cut = div(p.kv_cut);
+    a.div_hkv = div(Hkv);
+    a.div_group = div(a.group);
     a.div_q_tiles = div(p.q_tiles);
     a.div_bh = div(static_cast<int64_t>(B) * H);
     a.div_h = div(H);
@@ -281,7 +279,7 @@ dit_status_t dit_attn_bwd(const void* q, const void* k, const void* v, const voi
                           void* dv, dit_dtype_t grad_dtype, void* workspace, size_t workspace_bytes,
                           dit_stream_t stream) {
     return attn_bwd_common(q, k, v, out, out_dtype, lse, dout, dlse, strides, B, Nq, Nkv, H, D, key_valid_len, nullptr,
-                           scale, dq, dk, dv, grad_dtype, workspace, workspace_bytes, stream);
+                           nullptr, scale, dq, dk, dv, grad_dtype, workspace, workspace_bytes, stream);
 }
 
 dit_status_t dit_attn_bwd_masked(const void* q, const void* k, const void* v, const void* out, dit_dtype_t out_dtype,
@@ -298,7 +296,31 @@ dit_status_t dit_attn_bwd_masked(const void* q, const void* k, const void* v, co
         if (mask_row_stride % 4 || mask_batch_stride % 4 || !aligned16(mask)) return DIT_ERR_ALIGNMENT;
     }
     const BwdMask m{mask, mask_batch_stride, mask_row_stride, mask_rows};
-    return attn_bwd_common(q, k, v, out, out_dtype, lse, dout, dlse, strides, B, Nq, Nkv, H, D, key_valid_len, &m, scale,
+    return attn_bwd_common(q, k, v, out, out_dtype, lse, dout, dlse, strides, B, Nq, Nkv, H, D, key_valid_len, &m, nullptr, scale,
+                           dq, dk, dv, grad_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t dit_attn_bwd_window_workspace_bytes(int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len, const dit_window_t* window,
+                                           int q_offset) {
+    if (B <= 0 || Nq <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || key_valid_len <= 0 || key_valid_len > Nkv || (D != 64 && D != 128)) return 0;
+    if (!sound_window(window) || Nkv > kMaxWindowTokens || std::abs(static_cast<int64_t>(q_offset)) + Nq > kMaxWindowTokens) return 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const BwdPlan p = plan_attn_bwd_window(B, Nq, Nkv, H, Hkv, D, key_valid_len, make_window(*window), q_offset, device_sm_count(dev));
+    return static_cast<size_t>(p.stat_bytes + p.part_kv_bytes + p.part_q_bytes);
+}
+
+dit_status_t dit_attn_bwd_window(const void* q, const void* k, const void* v, const void* out, dit_dtype_t out_dtype,
+                                 const float* lse, const void* dout, const float* dlse, const dit_attn_bwd_strides_t* strides,
+                                 int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len, const dit_window_t* window,
+                                 int q_offset, float scale, void* dq, void* dk, void* dv, dit_dtype_t grad_dtype,
+                                 void* workspace, size_t workspace_bytes, dit_stream_t stream) {
+    if (!sound_window(window) || Hkv < 0) return DIT_ERR_INVALID_ARG;
+    if (H > 0 && (Hkv == 0 || H % Hkv != 0)) return DIT_ERR_INVALID_ARG;
+    if (H > 0 && H / Hkv > 128) return DIT_ERR_UNSUPPORTED;
+    if (Nkv > kMaxWindowTokens || std::abs(static_cast<int64_t>(q_offset)) + std::max(Nq, 0) > kMaxWindowTokens) return DIT_ERR_UNSUPPORTED;
+    const BwdWindow w{make_window(*window), Hkv, q_offset};
+    return attn_bwd_common(q, k, v, out, out_dtype, lse, dout, dlse, strides, B, Nq, Nkv, H, D, key_valid_len, nullptr, &w, scale,
                            dq, dk, dv, grad_dtype, workspace, workspace_bytes, stream);
 }
 

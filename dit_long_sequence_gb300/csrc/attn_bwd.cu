@@ -192,10 +192,18 @@ struct Cfg {
     static_assert(kR0 >= 3, "ring");
 };
 
+// Which keys a row attends: all of them, those of a bit mask, those of a window
+// (window_span.h), whose heads may share K and V.
+enum Mode { kAll = 0, kBits = 1, kWindow = 2 };
+
 // One item: its fixed tile, and the streamed tiles [begin, end) of its piece.
 template <bool KEY>
 struct Item {
-    int b, h, fixed, begin, end;
+    int b, h, fixed, begin, end;    // h: a key item's K/V head, a query item's own
+    // With a window the streamed tiles are counted through: a key item's from
+    // `base` on, `per_head` of them for each query head of its group, of which
+    // [full, full_end) see the whole key tile; a query item's as KeyTiles has them.
+    int base, per_head, full, full_end;
     bool cut;                   // a piece: its result goes to the partials
     int64_t part_tile;          // its place among them
 };
@@ -205,8 +213,75 @@ struct Item {
 // tend to load some tiles of every head more than others, and those then begin
 // together: key items from the first (the keys that all rows attend), query
 // items from the last (rows behind the masked ones, late rows of a causal mask).
-template <bool KEY, bool MASK>
+template <bool KEY>
+__device__ __forceinline__ Item<KEY> decode_window(const AttnBwdArgs& a, int id) {
+    Item<KEY> it;
+    uint32_t piece = 0, tile, bh, h, item = static_cast<uint32_t>(KEY ? id : id - a.n_kv_items);
+    if constexpr (KEY) {
+        // the leading kv_cut tiles of every head in pieces, then the others whole
+        const uint32_t cut = static_cast<uint32_t>(a.n_kv_cut);
+        it.cut = item < cut;
+        if (it.cut) {
+            item = a.div_f_kv.divmod(item, piece);
+            bh = a.div_kv_cut.divmod(item, tile);
+            it.part_tile = static_cast<int64_t>(item) * a.f_kv + piece;
+        } else {
+            bh = a.div_kv_tiles.divmod(item - cut, tile);
+            tile += static_cast<uint32_t>(a.kv_cut);
+            it.part_tile = 0;
+        }
+        it.fixed = static_cast<int>(tile);
+    } else {
+        it.cut = a.f_q > 1;
+        if (it.cut) item = a.div_f_q.divmod(item, piece);
+        bh = a.div_q_tiles.divmod(item, tile);
+        it.fixed = a.q_tiles - 1 - static_cast<int>(tile);
+        it.part_tile = (static_cast<int64_t>(bh) * a.q_tiles + it.fixed) * a.f_q + piece;
+    }
+    it.b = static_cast<int>((KEY ? a.div_hkv : a.div_h).divmod(bh, h));
+    it.h = static_cast<int>(h);
+    it.base = it.per_head = it.full = it.full_end = 0;
+    uint32_t n = 0;
+    const Window& w = a.window;
+    if constexpr (KEY) {
+        const int k0 = it.fixed * kT, k1 = min(k0 + kT, a.kv_len);
+        if (k0 < k1) {
+            // The queries that see a key of the tile, and those that see them all, are
+            // ranges: hi grows with the position and so does lo (but for the sinks).
+            auto from = [&](int64_t s) {        // first query whose frame starts at s or later
+                const int64_t f = (s >= 0 ? s + w.frame - 1 : s) / w.frame;      // (rounds up)
+                return min(max(f * w.frame - a.offset, int64_t(0)), static_cast<int64_t>(a.Nq));
+            };
+            const bool all = w.ahead >= kUnbounded, ever = w.back >= kUnbounded;
+            const int64_t first = all ? 0 : from(k0 - w.ahead + 1), first_full = all ? 0 : from(k1 - w.ahead);
+            const int64_t last = ever || k0 < w.sinks ? a.Nq : from(k1 + w.back);
+            const int64_t last_full = ever || k1 <= w.sinks ? a.Nq : from(k0 + w.back + 1);
+            it.base = static_cast<int>(first / kT);
+            it.per_head = first < last ? static_cast<int>((last + kT - 1) / kT) - it.base : 0;
+            it.full = static_cast<int>((first_full + kT - 1) / kT);
+            it.full_end = last_full >= a.Nq ? a.q_tiles : static_cast<int>(last_full / kT);
+            n = static_cast<uint32_t>(it.per_head) * static_cast<uint32_t>(a.group);
+        }
+    } else {
+        const int row = it.fixed * kT;
+        const KeyTiles t = key_tiles(w, a.offset + row, a.offset + min(row + kT, a.Nq) - 1, a.kv_len);
+        it.base = t.w0;
+        it.per_head = t.ns;
+        n = static_cast<uint32_t>(t.n);
+    }
+    it.begin = 0;
+    it.end = static_cast<int>(n);
+    if (it.cut) {
+        const FastDiv& f = KEY ? a.div_f_kv : a.div_f_q;
+        it.begin = static_cast<int>(f.div(piece * n));
+        it.end = static_cast<int>(f.div((piece + 1) * n));
+    }
+    return it;
+}
+template <bool KEY, int MODE>
 __device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int id) {
+    if constexpr (MODE == kWindow) return decode_window<KEY>(a, id);
+    constexpr bool MASK = MODE == kBits;
     Item<KEY> it;
     const int slot = KEY ? id : id - a.n_kv_items;
     const uint32_t f = static_cast<uint32_t>(KEY ? a.f_kv : a.f_q);
@@ -240,12 +315,24 @@ __device__ __forceinline__ Item<KEY> decode(const AttnBwdArgs& a, int id) {
 // words.  A warp holds the bits in its lanes (lane w: bits 32 w ..), 1,024 of
 // them; items beyond that many blocks (key) or key tiles (query) are streamed
 // whole.  Every call is made by a whole, converged warp.
-template <bool KEY, bool MASK>
+template <bool KEY, int MODE>
 struct Stream {
+    static constexpr bool MASK = MODE == kBits;
     int t, end;
     uint32_t bits;
     bool whole;
+    int at, group;      // window, key item: the next tile within its head, the head of the group
+    int base, per_head;
     __device__ Stream(const AttnBwdArgs& a, const Item<KEY>& it) : t(it.begin), end(it.end), bits(0u), whole(true) {
+        if constexpr (MODE == kWindow) {
+            base = it.base;
+            per_head = it.per_head;
+            at = group = 0;
+            if (KEY && t < end) {
+                group = t / per_head;
+                at = t - group * per_head;
+            }
+        }
         if constexpr (MASK) {
             const int n = KEY ? (a.q_tiles + 1) >> 1 : a.kv_tiles;
             if (a.occ == nullptr || n > 1024 || t >= end) return;
@@ -264,8 +351,29 @@ struct Stream {
             }
         }
     }
-    // the next tile, or -1
+    // the next tile, or -1 (a window's key item: of query head `head` of the group)
+    __device__ __forceinline__ int next(int& head) {
+        head = group;
+        if (t >= end) return -1;
+        const int tile = base + at;
+        if (++at == per_head) {
+            at = 0;
+            ++group;
+        }
+        ++t;
+        return tile;
+    }
     __device__ __forceinline__ int next() {
+        if constexpr (MODE == kWindow) {
+            if constexpr (KEY) {
+                int head;
+                return next(head);
+            } else {
+                if (t >= end) return -1;
+                const int i = t++;
+                return i < per_head ? i : base + (i - per_head);
+            }
+        }
         if constexpr (MASK) {
             while (!whole && t < end) {
                 const int i = KEY ? t >> 1 : t;
@@ -344,7 +452,7 @@ __device__ __forceinline__ int next_item(const AttnBwdArgs& a, int last) {
 __device__ __forceinline__ uint32_t turn(int n, int r) { return static_cast<uint32_t>(n / r) & 1u; }
 
 // ------------------------------------------------------------ TMA producer (a warp; lane 0 issues)
-template <int D, bool KEY, bool MASK>
+template <int D, bool KEY, int MODE>
 __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f0, const CUtensorMap& tm_f1,
                                         const CUtensorMap& tm_x0, const CUtensorMap& tm_x1, const AttnBwdArgs& a,
                                         Queue& queue, int& id) {
@@ -362,8 +470,8 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f
     bool ok = true;
     const int last = KEY ? a.n_kv_items : a.n_kv_items + a.n_q_items;
     for (int next; ok && id < last; id = next) {
-        const Item<KEY> it = decode<KEY, MASK>(a, id);
-        Stream<KEY, MASK> stream(a, it);
+        const Item<KEY> it = decode<KEY, MODE>(a, id);
+        Stream<KEY, MODE> stream(a, it);
         const int n = stream.count();
         if (n > 0) {
             ok = wait(C::kFixEmpty, (I & 1) ^ 1u, SITE_FIX_EMPTY);
@@ -378,9 +486,19 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f
         next = next_item(a, id);        // (its latency behind the copies)
         ok = publish(s, queue, next);
         if (!ok) break;
-        const float* const stat = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
+        const float* stat = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
+        int x_head = it.h;      // of the streamed tiles
+        if constexpr (MODE == kWindow && !KEY) x_head = static_cast<int>(a.div_group.div(static_cast<uint32_t>(it.h)));
         for (int j = 0; j < n; ++j, ++J) {
-            const int x_row = stream.next() * kT;
+            int x_tile;
+            if constexpr (MODE == kWindow && KEY) {
+                x_tile = stream.next(x_head);
+                x_head += it.h * a.group;
+                stat = a.stat + (static_cast<int64_t>(it.b) * a.H + x_head) * 2 * (static_cast<int64_t>(a.q_tiles) * kT);
+            } else {
+                x_tile = stream.next();
+            }
+            const int x_row = x_tile * kT;
             // A tile that is not there ends the CTA's work, as a wait that ran out
             // does: the flag tells every role, this one's query items among them.
             if (!in_bounds(x_row >= 0 && x_row < (KEY ? a.Nq : a.kv_len) - a.dbg_rows_short, a.status, ROLE_LOAD, BND_KEY)) {
@@ -393,7 +511,7 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f
             const int full = C::kXFull + J % R0;
             if (leader) {
                 mbar_arrive_expect_tx(bar(full), 2 * C::kTile + (KEY ? C::kStatBytes : 0));
-                copy(&tm_x0, s.x0(J), full, x_row, it.h, it.b);
+                copy(&tm_x0, s.x0(J), full, x_row, x_head, it.b);
             }
             half = J;
             ok = wait(C::kX1Empty + J % R1, turn(J, R1) ^ 1u, SITE_X_EMPTY);
@@ -405,7 +523,7 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_f
             }
             if (!ok) break;
             if (leader) {
-                copy(&tm_x1, s.x1(J), full, x_row, it.h, it.b);
+                copy(&tm_x1, s.x1(J), full, x_row, x_head, it.b);
                 if constexpr (KEY) {
                     const uint32_t sd = s.base + C::kStatOffset + J % C::kStats * C::kStatBytes;
                     bulk_load(sd, stat + x_row, kT * 4, bar(full));
@@ -455,7 +573,7 @@ struct RingPos {
 
 // Returns the items worked on; `before`: the key items this CTA worked on, whose
 // accumulators must have been read before the query items' products overwrite them.
-template <int D, bool KEY, bool MASK>
+template <int D, bool KEY, int MODE>
 __device__ __forceinline__ int multiply(const Cta<D>& s, const AttnBwdArgs& a, Queue& queue, int& id, int before) {
     using C = Cfg<D>;
     constexpr uint32_t kIdescT = idesc_bf16_f32(kT, kT, false);
@@ -522,7 +640,7 @@ __device__ __forceinline__ int multiply(const Cta<D>& s, const AttnBwdArgs& a, Q
     uint32_t J = 0;
     int I = 0;
     for (; ok && id < (KEY ? a.n_kv_items : a.n_kv_items + a.n_q_items); id = take(s, a, queue, ROLE_MMA)) {
-        const int n = Stream<KEY, MASK>(a, decode<KEY, MASK>(a, id)).count();
+        const int n = Stream<KEY, MODE>(a, decode<KEY, MODE>(a, id)).count();
         if (n == 0) continue;
         // the item's first T0, T1 (the previous item's last products are done with
         // T0, and its dS(last) was written after dP(last) had been read: in order)
@@ -603,9 +721,10 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&v)[8], bool wid
     }
 }
 
-template <int D, bool KEY, bool OUT_BF16, bool MASK>
+template <int D, bool KEY, bool OUT_BF16, int MODE>
 __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Queue& queue, int& id) {
     using C = Cfg<D>;
+    constexpr bool MASK = MODE == kBits, WINDOW = MODE == kWindow;
     constexpr int R0 = C::kR0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = warp >> 2;    // column half
@@ -637,7 +756,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
     const int last = KEY ? a.n_kv_items : a.n_kv_items + a.n_q_items;
     auto ask = [&](int which) {
         if (KEY || which >= last || a.stat == nullptr) return;    // (without keys there are no statistics)
-        const Item<KEY> it = decode<KEY, MASK>(a, which);
+        const Item<KEY> it = decode<KEY, MODE>(a, which);
         const float* p = a.stat + (static_cast<int64_t>(it.b) * a.H + it.h) * 2 * (static_cast<int64_t>(a.q_tiles) * kT) + it.fixed * kT + wq * 32 + lane;
         next_nlse = __ldg(p);
         next_ndelta = __ldg(p + static_cast<int64_t>(a.q_tiles) * kT);
@@ -648,10 +767,10 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
     ask(id);
     for (int next; ok && id < last; id = next) {
         next = take(s, a, queue, ROLE_SOFTMAX);
-        const Item<KEY> it = decode<KEY, MASK>(a, id);
+        const Item<KEY> it = decode<KEY, MODE>(a, id);
         const int row0 = it.fixed * kT;
         const int row = row0 + wq * 32 + lane;      // this thread's row of the fixed tile
-        Stream<KEY, MASK> stream(a, it);
+        Stream<KEY, MODE> stream(a, it);
         const int n_tiles = stream.count();
         const float nlse = next_nlse, ndelta = next_ndelta;
         ask(next);
@@ -676,14 +795,35 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
         };
         int tile_next = stream.next();
         uint2 mw_next = word_of(tile_next);
+        // A window's words are computed, and only for tiles that it cuts: the same
+        // words as a mask's.
+        Span span{0, 0};
+        if (WINDOW && !KEY) span = span_of(a.window, a.offset + row, a.kv_len);
+        auto cut_words = [&](int tile, uint2& w) {
+            if constexpr (KEY) {
+                const int k0 = row0 + wq * 32, i = tile * kT + 64 * g + lane;
+                const Span s0 = span_of(a.window, a.offset + i, a.kv_len), s1 = span_of(a.window, a.offset + i + 32, a.kv_len);
+                w.x = seen_word(s0.lo, s0.hi, a.window.sinks, k0);
+                w.y = seen_word(s1.lo, s1.hi, a.window.sinks, k0);
+            } else {
+                const int k0 = tile * kT + 64 * g;
+                w.x = seen_word(span.lo, span.hi, a.window.sinks, k0);
+                w.y = seen_word(span.lo, span.hi, a.window.sinks, k0 + 32);
+            }
+        };
 
         for (int j = 0; j < n_tiles; ++j, ++J) {
             const int tile = tile_next;
             const int st = J % C::kStats;
-            const uint2 mw = mw_next;
+            uint2 mw = mw_next;
             // Most tiles of a mask that is made of blocks forbid nothing: those pass
             // without the tests of single bits.
-            const bool some = MASK && !__all_sync(0xffffffffu, (mw.x & mw.y) == ~0u);
+            bool some = MASK && !__all_sync(0xffffffffu, (mw.x & mw.y) == ~0u);
+            if constexpr (WINDOW) {
+                some = KEY ? tile < it.full || tile >= it.full_end
+                           : !__all_sync(0xffffffffu, sees_all(span.lo, span.hi, a.window.sinks, tile * kT));
+                if (some) cut_words(tile, mw);
+            }
             tile_next = stream.next();
             mw_next = word_of(tile_next);
             ok = kDouble ? wait(C::kT0Full + (J & 1), turn(J, 2), SITE_T0_FULL) : wait(C::kT0Full, J & 1, SITE_T0_FULL);
@@ -716,7 +856,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) q[c] = ex2_approx(q[c]);
-                if (MASK && KEY && some) {
+                if ((MASK || WINDOW) && KEY && some) {
                     const uint32_t held = hf ? mw.y : mw.x;
                     const int row4 = lane >> 2, col = 2 * (lane & 3);
 #pragma unroll
@@ -730,7 +870,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
                         }
                     }
                 }
-                if (MASK && !KEY && some) {
+                if ((MASK || WINDOW) && !KEY && some) {
                     const uint32_t w = hf ? mw.y : mw.x;
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -804,7 +944,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
             // the item decoded anew: nothing of it is held across the tiles but its number
             int again = id;
             asm volatile("" : "+r"(again));
-            const Item<KEY> it = decode<KEY, MASK>(a, again);
+            const Item<KEY> it = decode<KEY, MODE>(a, again);
             const int row0 = it.fixed * kT;
             const int row = row0 + wq * 32 + lane;
             constexpr int kChunks = KEY ? D / 32 : D / 64;
@@ -858,7 +998,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const AttnBwdArgs& a, Qu
     }
 }
 
-template <int D, bool OUT_BF16, bool MASK>
+template <int D, bool OUT_BF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -914,9 +1054,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_decrease<kOtherRegs>();
         if (warp == 8) {
             int id = take(s, a, queue, ROLE_MMA);
-            const int worked = multiply<D, true, MASK>(s, a, queue, id, 0);
+            const int worked = multiply<D, true, MODE>(s, a, queue, id, 0);
             __syncwarp();
-            if (!__any_sync(0xffffffffu, *abort_flag)) multiply<D, false, MASK>(s, a, queue, id, worked);
+            if (!__any_sync(0xffffffffu, *abort_flag)) multiply<D, false, MODE>(s, a, queue, id, worked);
         } else if (warp == 9) {
             if (lane_id() == 0) {
                 tma_prefetch_desc(&tm_q);
@@ -926,17 +1066,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             int id = static_cast<int>(blockIdx.x);       // (the grid is no larger than the items)
             publish(s, queue, id);
-            produce<D, true, MASK>(s, tm_k, tm_v, tm_q, tm_do, a, queue, id);
+            produce<D, true, MODE>(s, tm_k, tm_v, tm_q, tm_do, a, queue, id);
             __syncwarp();
-            if (!__any_sync(0xffffffffu, *abort_flag)) produce<D, false, MASK>(s, tm_q, tm_do, tm_k, tm_v, a, queue, id);
+            if (!__any_sync(0xffffffffu, *abort_flag)) produce<D, false, MODE>(s, tm_q, tm_do, tm_k, tm_v, a, queue, id);
         }
         __syncwarp();
     } else {
         regs_increase<kSoftmaxRegs>();
         int id = take(s, a, queue, ROLE_SOFTMAX);
-        soften<D, true, OUT_BF16, MASK>(s, a, queue, id);
+        soften<D, true, OUT_BF16, MODE>(s, a, queue, id);
         __syncwarp();
-        if (!__any_sync(0xffffffffu, *abort_flag)) soften<D, false, OUT_BF16, MASK>(s, a, queue, id);
+        if (!__any_sync(0xffffffffu, *abort_flag)) soften<D, false, OUT_BF16, MODE>(s, a, queue, id);
     }
 
     tc_fence_before();
@@ -1011,15 +1151,15 @@ __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const AttnBwdArgs a, 
     const int which = static_cast<int>(blockIdx.y) + first;
     const bool key = which < 2;
     const int f = key ? a.f_kv : a.f_q;
-    const int tiles = key ? a.kv_out_tiles : a.q_tiles;
+    const int tiles = key ? a.kv_cut : a.q_tiles, heads = key ? a.Hkv : a.H;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t unit = g / (D / 4);
     const int c4 = static_cast<int>(g % (D / 4));
     const int nth = static_cast<int>(unit / kT), r = static_cast<int>(unit % kT);
     const int item = nth + (key ? 0 : a.q_whole);
-    if (unit >= (static_cast<int64_t>(a.B) * a.H * tiles - (key ? 0 : a.q_whole)) * kT) return;
+    if (unit >= (static_cast<int64_t>(a.B) * heads * tiles - (key ? 0 : a.q_whole)) * kT) return;
     const int row = (item % tiles) * kT + r;
-    const int h = (item / tiles) % a.H, b = item / tiles / a.H;
+    const int h = (item / tiles) % heads, b = item / tiles / heads;
     if (row >= (key ? a.Nkv : a.Nq)) return;
     const int64_t stride = static_cast<int64_t>(key ? 2 : 1) * kT * D;
     const float* p = (key ? a.part_kv + (static_cast<int64_t>(nth) * f * 2 + which) * kT * D
@@ -1039,10 +1179,10 @@ __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const AttnBwdArgs a, 
         *reinterpret_cast<float4*>(static_cast<float*>(out) + off) = s;
 }
 
-template <int D, bool OUT_BF16, bool MASK>
+template <int D, bool OUT_BF16, int MODE>
 cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                         const AttnBwdArgs& a, cudaStream_t s) {
-    auto kern = attn_bwd_kernel<D, OUT_BF16, MASK>;
+    auto kern = attn_bwd_kernel<D, OUT_BF16, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
     return launch_behind(kern, a.grid, kThreads, Cfg<D>::kSmemBytes, s, tq, tk, tv, tdo, a);
@@ -1064,23 +1204,21 @@ cudaError_t launch_attn_bwd_stat(const AttnBwdStatArgs& a, int D, bool out_bf16,
 
 cudaError_t launch_attn_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                             const AttnBwdArgs& a, int D, bool grad_bf16, cudaStream_t s) {
-    if (a.mask != nullptr) {
-        if (D == 128) return grad_bf16 ? launch_impl<128, true, true>(tq, tk, tv, tdo, a, s)
-                                       : launch_impl<128, false, true>(tq, tk, tv, tdo, a, s);
-        return grad_bf16 ? launch_impl<64, true, true>(tq, tk, tv, tdo, a, s)
-                         : launch_impl<64, false, true>(tq, tk, tv, tdo, a, s);
-    }
-    if (D == 128) return grad_bf16 ? launch_impl<128, true, false>(tq, tk, tv, tdo, a, s)
-                                   : launch_impl<128, false, false>(tq, tk, tv, tdo, a, s);
-    return grad_bf16 ? launch_impl<64, true, false>(tq, tk, tv, tdo, a, s)
-                     : launch_impl<64, false, false>(tq, tk, tv, tdo, a, s);
+    auto go = [&](auto mode) {
+        constexpr int M = decltype(mode)::value;
+        if (D == 128) return grad_bf16 ? launch_impl<128, true, M>(tq, tk, tv, tdo, a, s) : launch_impl<128, false, M>(tq, tk, tv, tdo, a, s);
+        return grad_bf16 ? launch_impl<64, true, M>(tq, tk, tv, tdo, a, s) : launch_impl<64, false, M>(tq, tk, tv, tdo, a, s);
+    };
+    if (a.windowed) return go(std::integral_constant<int, kWindow>{});
+    if (a.mask != nullptr) return go(std::integral_constant<int, kBits>{});
+    return go(std::integral_constant<int, kAll>{});
 }
 
 cudaError_t launch_attn_bwd_sum(const AttnBwdArgs& a, int D, bool grad_bf16, cudaStream_t s) {
     const bool kv = a.f_kv > 1, q = a.f_q > 1;
     if (!kv && !q) return cudaSuccess;
-    const int64_t bh = static_cast<int64_t>(a.B) * a.H;
-    const int64_t kv_items = kv ? bh * a.kv_out_tiles : 0, q_items = q ? bh * a.q_tiles - a.q_whole : 0;
+    const int64_t kv_items = kv ? static_cast<int64_t>(a.B) * a.Hkv * a.kv_cut : 0;
+    const int64_t q_items = q ? static_cast<int64_t>(a.B) * a.H * a.q_tiles - a.q_whole : 0;
     const int64_t threads = (kv_items > q_items ? kv_items : q_items) * kT * (D / 4);
     const dim3 grid(static_cast<unsigned>((threads + 255) / 256), (kv ? 2 : 0) + (q ? 1 : 0));
     const int first = kv ? 0 : 2;

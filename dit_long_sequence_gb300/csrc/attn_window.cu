@@ -1,0 +1,572 @@
+// attn_window.cu -- attention over a sliding window of frames with sinks, forward,
+// sm_103a: TMA-fed tiles, tcgen05 products with TMEM accumulators, warp-specialised
+// roles that run on through a CTA's work items.
+//
+//     O_i = sum_j softmax_j(scale q_i . k_j) v_j,  LSE_i = ln sum_j exp(scale q_i . k_j)
+// over the keys [0, min(sinks, hi_i)) and [lo_i, hi_i) of row i (window_span.h).  K
+// and V are strided tensors, or the pages of a cache (PAGED).
+//
+// A work item is 256 query rows, two 128-row tiles, of one (batch entry, K/V head).
+// Rows are (token, query head of the group): heads that share K and V share their
+// tiles too.  The item walks the key tiles that some row of it sees, the sinks'
+// first; a tile that every row of a warp sees whole passes without a mask, others
+// through four mask words a row, computed from the row's bounds.
+//
+// 12 warps:
+//   warps 0-3, 4-7  softmax of query tile 0, 1 (one TMEM lane = one row per thread)
+//   warp 8          tcgen05.mma issuer (warp-wide); owns the TMEM allocation
+//   warp 9          TMA producer: Q, then K_0, V_0, K_1, V_1, ... through a ring
+//   warps 10, 11    idle (they complete the third warpgroup)
+// Registers: 168 at launch; softmax 208, the rest 88: 256*208 + 128*88 = 384*168.
+// TMEM (512 columns): S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D); P_t
+// (bf16) lies over the first half of S_t and is the PV product's TMEM operand.
+//
+// The grid has one CTA per item; a CTA that is done claims the next one that has not
+// begun (cluster launch control), so that its roles go on: while the softmax warps
+// write one item's result, the next one's first tiles are on their way and its
+// first products run.  The last blocks of a sequence, which see the most keys of a
+// causal mask, come first.
+//
+// Few items are cut into key ranges (f pieces), whose normalised partials
+// window_merge_kernel joins.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "window.cuh"
+
+namespace dit {
+namespace {
+
+constexpr int kT = kWinTile;
+constexpr int kThreads = 384;
+constexpr uint32_t kSoftmaxRegs = 208;
+constexpr uint32_t kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+
+template <int D>
+struct Cfg {
+    static constexpr int kTile = kT * D * 2;
+    static constexpr int kStages = D == 128 ? 4 : 8;     // K/V ring slots
+    static constexpr int kBlock = kT * 128;              // 128 rows x 64 bf16 (one swizzle column)
+    static constexpr int kQueue = 4;                     // items published ahead at most
+    // barriers
+    static constexpr int kQFull = 0, kQEmpty = 1;
+    static constexpr int kKVFull = 2;
+    static constexpr int kKVEmpty = kKVFull + kStages;
+    static constexpr int kSFull = kKVEmpty + kStages;    // two
+    static constexpr int kPFull = kSFull + 2;            // two
+    static constexpr int kOFinal = kPFull + 2;           // two
+    static constexpr int kDrain = kOFinal + 2;
+    static constexpr int kItemFull = kDrain + 1, kItemEmpty = kItemFull + kQueue;
+    static constexpr int kClaim = kItemEmpty + kQueue;
+    static constexpr int kNumBars = kClaim + 1;
+    static constexpr int kClaimOffset = (2 + kStages) * kTile;           // 16 bytes
+    static constexpr int kBarOffset = kClaimOffset + 16;
+    static constexpr int kItemOffset = kBarOffset + kNumBars * 8;
+    static constexpr int kSmemBytes = 1024 /*alignment slack*/ + kItemOffset + kQueue * 4 + 16;
+    static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+// Claims a CTA of the grid that has not begun: the answer arrives at `dst` (16
+// bytes) and counts on `bar`.
+__device__ __forceinline__ void claim_ask(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst), "r"(bar)
+                 : "memory");
+}
+// The claimed CTA's index, or -1 when none was left.
+__device__ __forceinline__ int claim_answer(uint32_t src) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+        : "=r"(x)
+        : "r"(src)
+        : "memory");
+    return x;
+}
+
+// One item, the same for every role.
+struct Item {
+    int b, hk, blk, id;         // id: with its piece
+    int first;                  // first token of the item
+    int tokens;                 // tokens of the sequence that are queries
+    int pos;                    // position of query 0
+    int kv_len;                 // keys
+    KeyTiles tiles;
+    int begin, end;             // the piece's tiles
+};
+template <bool PAGED>
+__device__ __forceinline__ Item decode(const WindowArgs& a, int id) {
+    Item it;
+    it.id = id;
+    uint32_t piece = 0, blk, hk, rest = static_cast<uint32_t>(id);
+    if (a.f > 1) rest = a.div_f.divmod(rest, piece);
+    rest = a.div_blk.divmod(rest, blk);
+    it.blk = a.n_blk - 1 - static_cast<int>(blk);
+    it.b = static_cast<int>(a.div_hkv.divmod(rest, hk));
+    it.hk = static_cast<int>(hk);
+    it.first = it.blk * 2 * a.tokens;
+    if constexpr (PAGED) {
+        const int len = max(__ldg(a.kv_lens + it.b), 0);
+        it.tokens = a.q_lens != nullptr ? min(max(__ldg(a.q_lens + it.b), 0), a.T) : a.T;
+        it.pos = len - it.tokens;
+        it.kv_len = min(len, a.capacity);
+    } else {
+        it.tokens = a.T;
+        it.pos = a.offset;
+        it.kv_len = a.kv_len;
+    }
+    it.begin = it.end = 0;
+    it.tiles.n = 0;
+    if (it.first < it.tokens) {
+        const int last = min(it.first + 2 * a.tokens, it.tokens) - 1;
+        it.tiles = key_tiles(a.win, it.pos + it.first, it.pos + last, it.kv_len);
+        it.end = it.tiles.n;
+        if (a.f > 1) {
+            it.begin = static_cast<int>(a.div_f.div(piece * static_cast<uint32_t>(it.tiles.n)));
+            it.end = static_cast<int>(a.div_f.div((piece + 1) * static_cast<uint32_t>(it.tiles.n)));
+        }
+    }
+    return it;
+}
+
+// What the roles of a CTA share.
+template <int D>
+struct Cta {
+    using C = Cfg<D>;
+    uint8_t* smem;
+    uint32_t base, bars, tmem;
+    Watchdog wd, wd_drain;      // wd_drain ignores the abort flag: it waits for work already in flight
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + i * 8; }
+    __device__ __forceinline__ uint32_t q(int t) const { return base + t * C::kTile; }
+    __device__ __forceinline__ uint32_t slot_offset(int i) const { return (2 + i % C::kStages) * C::kTile; }
+};
+__device__ __forceinline__ uint32_t turn(int n, int r) { return static_cast<uint32_t>(n / r) & 1u; }
+
+// The CTA's items, in order: the producer publishes them, the other roles' warps
+// take them.  a.n_items is the end.
+template <int D>
+__device__ __forceinline__ bool publish(const Cta<D>& s, int n, int id) {
+    using C = Cfg<D>;
+    const int slot = n % C::kQueue;
+    const bool ok = wait_bounded_warp(s.bar(C::kItemEmpty + slot), turn(n, C::kQueue) ^ 1u, s.wd, ROLE_LOAD, SITE_ITEM_EMPTY);
+    if (ok && lane_id() == 0) {
+        *reinterpret_cast<volatile int*>(s.smem + C::kItemOffset + slot * 4) = id;
+        mbar_arrive(s.bar(C::kItemFull + slot));
+    }
+    return ok;
+}
+template <int D>
+__device__ __forceinline__ int take(const Cta<D>& s, const WindowArgs& a, int n, uint32_t role) {
+    using C = Cfg<D>;
+    const int slot = n % C::kQueue;
+    const bool ok = wait_bounded_warp(s.bar(C::kItemFull + slot), turn(n, C::kQueue), s.wd, role, SITE_ITEM_FULL);
+    const int id = ok ? *reinterpret_cast<volatile int*>(s.smem + C::kItemOffset + slot * 4) : a.n_items;
+    __syncwarp();
+    if (ok && lane_id() == 0) mbar_arrive(s.bar(C::kItemEmpty + slot));
+    return id;
+}
+
+// ------------------------------------------------------------ TMA producer (a warp)
+template <int D, bool PAGED>
+__device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                        const WindowArgs& a) {
+    using C = Cfg<D>;
+    constexpr int S = C::kStages;
+    const bool leader = lane_id() == 0;
+    auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded_warp(s.bar(i), parity, s.wd, ROLE_LOAD, site); };
+    int I = 0, J = 0;                   // items with tiles, copies
+    int asked = 0, claims = 0;          // claims made and answered
+    bool ok = true;
+    int id = static_cast<int>(blockIdx.x);
+    for (int n = 0; ok; ++n) {
+        ok = publish(s, n, id);
+        if (!ok || id >= a.n_items) break;
+        const Item it = decode<PAGED>(a, id);
+        const int32_t* const row = PAGED ? a.table + it.b * a.table_sb : nullptr;
+        if (it.begin < it.end) {
+            ok = wait(C::kQEmpty, (I & 1) ^ 1u, SITE_Q_EMPTY);
+            if (!ok) break;
+            if (leader) {
+                mbar_arrive_expect_tx(s.bar(C::kQFull), 2 * a.tokens * a.group * D * 2);
+                for (int t = 0; t < 2; ++t)
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_5d(s.q(t) + c * C::kBlock, &tm_q, s.bar(C::kQFull), c * 64, 0, it.first + t * a.tokens, it.hk, it.b);
+            }
+            ++I;
+        }
+        const int ask_at = max(it.begin, it.end - 2);      // claim late: another CTA may be free earlier
+        int entry = PAGED && it.begin < it.end ? page_entry(a, row, it.tiles.at(it.begin), it.kv_len) : 0;
+        for (int i = it.begin; i <= it.end; ++i) {
+            if (i == ask_at) {
+                if (leader) {
+                    fence_async();      // (the previous answer has been read)
+                    mbar_arrive_expect_tx(s.bar(C::kClaim), 16);
+                    claim_ask(s.base + C::kClaimOffset, s.bar(C::kClaim));
+                }
+                ++asked;
+            }
+            if (i == it.end) break;
+            const int tile = it.tiles.at(i);
+            if (!in_bounds(tile >= 0 && tile * kT < it.kv_len, a.status, ROLE_LOAD, BND_KEY)) {
+                *s.wd.abort_flag = 1;
+                ok = false;
+                break;
+            }
+            const int entry_next = PAGED && i + 1 < it.end ? page_entry(a, row, it.tiles.at(i + 1), it.kv_len) : 0;
+            for (int kv = 0; kv < 2; ++kv, ++J) {
+                ok = wait(C::kKVEmpty + J % S, turn(J, S) ^ 1u, SITE_KV_EMPTY);
+                if (!ok) break;
+                const uint32_t full = s.bar(C::kKVFull + J % S), dst = s.base + s.slot_offset(J);
+                const CUtensorMap* const tm = kv ? &tm_v : &tm_k;
+                if (leader) mbar_arrive_expect_tx(full, C::kTile);
+                if constexpr (PAGED) {
+                    __syncwarp();
+                    copy_paged<D>(a, tm, dst, full, entry, tile, it.hk);
+                } else if (leader) {
+                    for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * C::kBlock, tm, full, c * 64, tile * kT, it.hk, it.b);
+                }
+            }
+            if (!ok) break;
+            entry = entry_next;
+        }
+        if (!ok) break;
+        ok = wait(C::kClaim, claims & 1, SITE_CLAIM);
+        if (!ok) break;
+        ++claims;
+        const int got = claim_answer(s.base + C::kClaimOffset);
+        id = got >= 0 ? got : a.n_items;
+        __syncwarp();
+    }
+    if (!ok) {
+        // Winding down: wait (bounded) until every copy issued has landed.
+        auto land = [&](int i, uint32_t parity) { wait_bounded_warp(s.bar(i), parity, s.wd_drain, ROLE_LOAD, SITE_LOAD_DRAIN); };
+        for (int j = J > S ? J - S : 0; j < J; ++j) land(C::kKVFull + j % S, turn(j, S));
+        if (I > 0) land(C::kQFull, (I - 1) & 1);
+        if (asked > claims) land(C::kClaim, claims & 1);
+    }
+}
+
+// ------------------------------------------------------------ MMA issuer (a warp)
+template <int D, bool PAGED>
+__device__ __forceinline__ void multiply(const Cta<D>& s, const WindowArgs& a) {
+    using C = Cfg<D>;
+    constexpr int S = C::kStages;
+    constexpr uint32_t kIdescQK = idesc_bf16_f32(kT, kT, false);
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(kT, D, true);
+    auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded_warp(s.bar(i), parity, s.wd, ROLE_MMA, site); };
+    auto commit = [&](int i) { umma_commit_warp(s.bar(i)); };
+    // S_t = Q_t K^T: both K-major, K = D channels
+    auto issue_qk = [&](int t, uint32_t k_addr) {
+        const uint64_t dq = sdesc_sw128(s.q(t), 16, 1024), dk = sdesc_sw128(k_addr, 16, 1024);
+        static_for<D / 16>([&](auto kk) {
+            constexpr uint32_t off = (kk.value >> 2) * C::kBlock + (kk.value & 3) * 32;
+            umma_ss_warp<off>(s.tmem + t * 128, dq, dk, kIdescQK, kk.value > 0 ? 1u : 0u);
+        });
+    };
+    // O_t (+)= P_t V: P from TMEM, V MN-major, K = 128 keys
+    auto issue_pv = [&](int t, uint32_t v_addr, bool accumulate) {
+        const uint64_t dv = sdesc_sw128(v_addr, C::kBlock, 1024);
+        static_for<kT / 16>([&](auto kk) {
+            umma_ts_warp<kk.value * 16 * 128>(s.tmem + 256 + t * D, s.tmem + t * 128 + kk.value * 8, dv, kIdescPV,
+                                              (accumulate || kk.value > 0) ? 1u : 0u);
+        });
+    };
+    int I = 0, R = 0;           // items with tiles, ring slots taken
+    int J = 0;                  // key tiles
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+        const int id = take(s, a, n, ROLE_MMA);
+        if (id >= a.n_items) break;
+        const Item it = decode<PAGED>(a, id);
+        if (it.begin >= it.end) continue;
+        ok = wait(C::kQFull, I & 1, SITE_Q_FULL) && wait(C::kKVFull + R % S, turn(R, S), SITE_KV_FULL);
+        if (!ok) break;
+        tc_fence_after();
+        issue_qk(0, s.base + s.slot_offset(R));
+        commit(C::kSFull + 0);
+        issue_qk(1, s.base + s.slot_offset(R));
+        commit(C::kSFull + 1);
+        commit(C::kKVEmpty + R % S);
+        if (it.begin + 1 == it.end) commit(C::kQEmpty);
+        ++R;
+        for (int i = it.begin; i < it.end; ++i, ++J) {
+            const bool more = i + 1 < it.end;
+            const int rv = R, rk = R + 1;
+            const uint32_t v_addr = s.base + s.slot_offset(rv), k_addr = s.base + s.slot_offset(rk);
+            ok = wait(C::kKVFull + rv % S, turn(rv, S), SITE_KV_FULL);
+            if (!ok) break;
+            clear_unseen<D>(s.smem + s.slot_offset(rv), it.tiles, it.tiles.at(i) * kT);
+            ok = wait(C::kPFull + 0, J & 1, SITE_P_FULL);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(0, v_addr, i > it.begin);
+            if (more) {
+                ok = wait(C::kKVFull + rk % S, turn(rk, S), SITE_KV_FULL);
+                if (!ok) break;
+                tc_fence_after();
+                issue_qk(0, k_addr);
+                commit(C::kSFull + 0);
+            } else {
+                commit(C::kOFinal + 0);
+            }
+            ok = wait(C::kPFull + 1, J & 1, SITE_P_FULL);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, v_addr, i > it.begin);
+            commit(C::kKVEmpty + rv % S);
+            if (more) {
+                issue_qk(1, k_addr);
+                commit(C::kSFull + 1);
+                commit(C::kKVEmpty + rk % S);
+                if (i + 2 == it.end) commit(C::kQEmpty);
+                R += 2;
+            } else {
+                commit(C::kOFinal + 1);
+                R += 1;
+            }
+        }
+        ++I;
+    }
+    // Every product issued must finish before TMEM is released.
+    commit(C::kDrain);
+    wait_bounded_warp(s.bar(C::kDrain), 0, s.wd_drain, ROLE_MMA, SITE_DRAIN);
+}
+
+// ------------------------------------------------------------ softmax warps (0-7)
+template <int D, bool PAGED>
+__device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
+    using C = Cfg<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = warp >> 2;    // query tile
+    const int wq = warp & 3;    // TMEM lane quadrant
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = s.tmem + lane_off + t * 128, tO = s.tmem + lane_off + 256 + t * D;
+    const int r = wq * 32 + lane;                       // this thread's row of the tile
+    uint32_t g;                                         // its query head of the group
+    const int token = static_cast<int>(a.div_group.divmod(static_cast<uint32_t>(r), g));
+    int I = 0, J = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+        const int id = take(s, a, n, ROLE_SOFTMAX);
+        if (id >= a.n_items) break;
+        const Item it = decode<PAGED>(a, id);
+        const int q_at = it.first + t * a.tokens + token;                   // this row's token
+        const bool mine = token < a.tokens && q_at < it.tokens;
+        // rows that are not there see everything, so that they mask no tile
+        int lo = 0, hi = kNoBound, sinks = 0;
+        if (mine) {
+            const Span sp = span_of(a.win, it.pos + q_at, it.kv_len);
+            lo = sp.lo;
+            hi = sp.hi;
+            sinks = a.win.sinks;
+        }
+        const int32_t* const row = PAGED ? a.table + it.b * a.table_sb : nullptr;
+        int entry = PAGED && it.begin < it.end ? page_entry(a, row, it.tiles.at(it.begin), it.kv_len) : 0;
+        float m = -INFINITY, l = 0.f;
+        for (int i = it.begin; i < it.end; ++i, ++J) {
+            const int tile = it.tiles.at(i), k0 = tile * kT;
+            uint32_t there = ~0u;
+            if constexpr (PAGED) {
+                there = pages_there(a, entry, tile, it.kv_len);
+                if (i + 1 < it.end) entry = page_entry(a, row, it.tiles.at(i + 1), it.kv_len);
+            }
+            const bool masked = !__all_sync(0xffffffffu, sees_all(lo, hi, sinks, k0)) || there != ~0u;
+            uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+            if (masked) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    words[w] = seen_word(lo, hi, sinks, k0 + 32 * w);
+                    if (PAGED && there != ~0u) words[w] &= paged_word(there, a.chunk, w);
+                }
+            }
+            ok = wait_bounded(s.bar(C::kSFull + t), J & 1, s.wd, ROLE_SOFTMAX, SITE_S_FULL);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            soften_tile<D>(tS, tO, a.scale_log2, i == it.begin, masked, words, m, l);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(s.bar(C::kPFull + t));
+        }
+        if (!ok) break;
+        const bool any_tile = it.begin < it.end;
+        if (any_tile) {
+            ok = wait_bounded(s.bar(C::kOFinal + t), I & 1, s.wd, ROLE_SOFTMAX, SITE_O_FINAL);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            ++I;
+        }
+        // The result, from this thread's row: whole 32-byte sectors.  (PV of the
+        // next item's first tile overwrites O only after this thread's next P.)
+        const bool any_key = l > 0.f || l != l;
+        const float inv = any_key ? 1.f / l : 0.f;
+        const float lse = any_key ? (m + log2f(l)) * kWinLn2 : -INFINITY;
+        const int h = it.hk * a.group + static_cast<int>(g);
+        const int64_t off = it.b * a.o_sb + static_cast<int64_t>(q_at) * a.o_sn + h * a.o_sh;
+        const int64_t part = static_cast<int64_t>(it.id) * (2 * kT) + t * kT + r;
+        const bool stored = mine && in_bounds(a.f > 1 || (off >= 0 && off + D <= a.dbg_o_elems), a.status, ROLE_SOFTMAX, BND_OUT);
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            if (any_tile) {
+                tmem_ld32(tO + cc * 32, o);
+                tmem_ld_wait_dep(o);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = any_key ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+            if (stored) store_32(a, a.f > 1 ? a.ws_o + part * D + cc * 32 : nullptr, off + cc * 32, o);
+            __syncwarp();
+        }
+        if (stored) {
+            if (a.f > 1) a.ws_lse[part] = lse;
+            else a.lse[(static_cast<int64_t>(it.b) * a.H + h) * a.T + q_at] = lse;
+        }
+        tc_fence_before();
+    }
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    Cta<D> s;
+    s.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    s.base = smem_u32(s.smem);
+    s.bars = s.base + C::kBarOffset;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s.smem + C::kItemOffset + C::kQueue * 4);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* const never_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    s.wd = Watchdog{a.status, a.timeout_ns, abort_flag};
+    s.wd_drain = Watchdog{a.status, a.timeout_ns, never_flag};
+    const int warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kNumBars; ++i) {
+            const bool all = i == C::kPFull || i == C::kPFull + 1;
+            const bool takers = i >= C::kItemEmpty && i < C::kItemEmpty + C::kQueue;     // the MMA and softmax warps
+            mbar_init(s.bar(i), all ? 128 : (takers ? 9 : 1));
+        }
+        *abort_flag = 0;
+        *never_flag = 0;
+        fence_mbar_init();
+        if (a.f > 1) let_next();
+    }
+    // Rows of a query tile past its last whole token hold nothing that is copied:
+    // zeros, so that they make no NaN and no rescale.
+    const int spare = kT - a.tokens * a.group;
+    for (int u = threadIdx.x; u < 2 * (D / 64) * spare * 8; u += kThreads) {
+        const int block = u / (spare * 8), rest = u % (spare * 8);
+        *reinterpret_cast<uint4*>(s.smem + block * C::kBlock + (kT - spare + rest / 8) * 128 + (rest & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async();
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    s.tmem = *tmem_slot;
+
+    if (warp >= 8) {
+        regs_decrease<kOtherRegs>();
+        if (warp == 8) {
+            multiply<D, PAGED>(s, a);
+        } else if (warp == 9) {
+            if (lane_id() == 0 && (PAGED ? a.capacity : a.kv_len) > 0) {      // (no keys, no maps)
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+            }
+            produce<D, PAGED>(s, tm_q, tm_k, tm_v, a);
+        }
+        __syncwarp();
+    } else {
+        regs_increase<kSoftmaxRegs>();
+        soften<D, PAGED>(s, a);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(s.tmem, 512);
+    }
+}
+
+// Joins the f pieces of every item: with M = max_p LSE_p and w_p = e^(LSE_p - M),
+// O = sum_p w_p O_p / sum_p w_p and LSE = M + ln sum_p w_p.  A piece without a key
+// of the row has LSE_p = -inf and weight 0.  D / 4 lanes a row.
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant__ WindowArgs a) {
+    constexpr int LPR = D / 4;
+    after_previous();
+    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+    const int c4 = static_cast<int>(threadIdx.x % LPR);
+    const int item = static_cast<int>(unit / (2 * kT)), rr = static_cast<int>(unit % (2 * kT));
+    if (item >= a.n_items / a.f) return;
+    uint32_t blk, hk, g;
+    const int t = rr / kT;
+    const int token = static_cast<int>(a.div_group.divmod(static_cast<uint32_t>(rr % kT), g));
+    const int b = static_cast<int>(a.div_hkv.divmod(a.div_blk.divmod(static_cast<uint32_t>(item), blk), hk));
+    const int q_at = (a.n_blk - 1 - static_cast<int>(blk)) * 2 * a.tokens + t * a.tokens + token;
+    const int tokens = PAGED && a.q_lens != nullptr ? min(__ldg(a.q_lens + b), a.T) : a.T;
+    if (token >= a.tokens || q_at >= tokens) return;
+    const int64_t p0 = static_cast<int64_t>(item) * a.f * (2 * kT) + rr;
+    float mx = -INFINITY;
+    for (int p = 0; p < a.f; ++p) mx = fmaxf(mx, __ldg(a.ws_lse + p0 + p * (2 * kT)));
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool bad = false;           // (a NaN must stay one)
+    for (int p = 0; p < a.f; ++p) {
+        const float lp = __ldg(a.ws_lse + p0 + p * (2 * kT));
+        bad = bad || lp != lp;
+        if (lp == -INFINITY) continue;
+        const float w = expf(lp - mx);
+        const float4 o = __ldg(reinterpret_cast<const float4*>(a.ws_o + (p0 + p * (2 * kT)) * D) + c4);
+        sum += w;
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+    }
+    const float inv = bad ? NAN : (sum > 0.f ? 1.f / sum : 0.f);
+    const int h = static_cast<int>(hk) * a.group + static_cast<int>(g);
+    const int64_t off = b * a.o_sb + static_cast<int64_t>(q_at) * a.o_sn + h * a.o_sh + 4 * c4;
+    if (!in_bounds(off >= 0 && off + 4 <= a.dbg_o_elems, a.status, 0, BND_OUT)) return;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + off) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + off) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (c4 == 0)
+        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + q_at] = bad ? NAN : (sum > 0.f ? mx + logf(sum) : -INFINITY);
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WindowArgs& a, cudaStream_t s) {
+    auto kern = attn_window_kernel<D, PAGED>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(a.n_items), kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv, a);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.f == 1) return e;
+    const int64_t threads = static_cast<int64_t>(a.n_items / a.f) * (2 * kT) * (D / 4);
+    return launch_behind(window_merge_kernel<D, PAGED>, static_cast<unsigned>((threads + 255) / 256), 256, 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_window(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WindowArgs& a,
+                               int D, bool paged, cudaStream_t s) {
+    if (D == 128) return paged ? launch_impl<128, true>(tq, tk, tv, a, s) : launch_impl<128, false>(tq, tk, tv, a, s);
+    return paged ? launch_impl<64, true>(tq, tk, tv, a, s) : launch_impl<64, false>(tq, tk, tv, a, s);
+}
+
+}  // namespace dit

@@ -3,8 +3,11 @@
 // takes.  Used by api_train.cu.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 #include <initializer_list>
+
+#include "window_plan.h"
 
 namespace dit {
 
@@ -21,6 +24,7 @@ struct BwdPlan {
     int q_tiles, kv_tiles, kv_out_tiles;
     int64_t key_items, query_items;
     int f_kv, f_q;              // pieces of a key item, of a cut query item
+    int kv_cut;                 // key tiles of a head that are cut, the leading ones
     int64_t q_whole;            // query items that are not cut, the first of the grid's order
     int64_t stat_bytes, part_kv_bytes, part_q_bytes;
 };
@@ -98,10 +102,68 @@ inline BwdPlan plan_attn_bwd(int B, int Nq, int Nkv, int H, int D, int key_valid
                 p.q_whole = p.query_items - cut;
             }
     }
+    p.kv_cut = p.f_kv > 1 ? p.kv_out_tiles : 0;
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
     p.stat_bytes = up(bh * 2 * p.q_tiles * 128 * 4) + 256;     // and the item counter
     p.part_kv_bytes = p.f_kv > 1 ? up(p.key_items * p.f_kv * 2 * 128 * D * 4) : 0;
     p.part_q_bytes = p.f_q > 1 ? up((p.query_items - p.q_whole) * p.f_q * 128 * D * 4) : 0;
+    return p;
+}
+
+// The same with a window and shared heads.  Items differ: a sink's key tile is seen by
+// every query behind it, a window's by few.  Where a common key tile is longer than
+// the even share all key items are cut, else only the sinks' (the first of the grid's
+// order), where those are; query items are cut when the longest is longer than the
+// share.
+inline BwdPlan plan_attn_bwd_window(int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len, const Window& w, int offset, int sms) {
+    BwdPlan p{};
+    const int64_t bh = static_cast<int64_t>(B) * H, bhk = static_cast<int64_t>(B) * Hkv;
+    const int group = H / Hkv;
+    p.q_tiles = static_cast<int>((static_cast<int64_t>(Nq) + 127) / 128);
+    p.kv_tiles = static_cast<int>((static_cast<int64_t>(key_valid_len) + 127) / 128);
+    p.kv_out_tiles = static_cast<int>((static_cast<int64_t>(Nkv) + 127) / 128);
+    p.key_items = bhk * p.kv_out_tiles;
+    p.query_items = bh * p.q_tiles;
+    p.f_kv = p.f_q = 1;
+    if (sms > 0 && p.kv_tiles > 0 && p.q_tiles > 0) {
+        const double mean = mean_key_tiles(w, Nq, 128, offset, key_valid_len);
+        const double share = 7.0 * static_cast<double>(bh) * p.q_tiles * mean / sms;      // per SM, in products
+        auto pieces = [&](double cost, int64_t tiles) {
+            int64_t f = share > 0 ? static_cast<int64_t>(cost / share + 0.999) : 1;
+            f = std::min<int64_t>({f, tiles / kMinPieceTiles, kMaxPieces, 0x7fffffff / std::max<int64_t>(tiles, 1)});
+            return static_cast<int>(std::max<int64_t>(f, 1));
+        };
+        // the longest query item, and the longest key item beside the sinks' (some of
+        // each: the ends, where a causal mask has them, and a few between)
+        int most_keys = 0, most_queries = 0;
+        const int sink_tiles = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(w.sinks) + 127) / 128, p.kv_tiles));
+        for (int i = 0; i <= 8; ++i) {
+            const int64_t t = static_cast<int64_t>(p.q_tiles - 1) * i / 8;
+            const int64_t last = std::min<int64_t>(t * 128 + 127, Nq - 1);
+            most_keys = std::max(most_keys, key_tiles(w, static_cast<int>(offset + t * 128), static_cast<int>(offset + last), key_valid_len).n);
+            const int64_t k = sink_tiles + static_cast<int64_t>(std::max(p.kv_tiles - 1 - sink_tiles, 0)) * i / 8;
+            // queries from the first that sees the tile's first key to the last that sees its last
+            auto from = [&](int64_t s) {
+                const int64_t f = (s >= 0 ? s + w.frame - 1 : s) / w.frame;
+                return std::min(std::max(f * w.frame - offset, int64_t(0)), static_cast<int64_t>(Nq));
+            };
+            const int64_t first = w.ahead >= kUnbounded ? 0 : from(k * 128 - w.ahead + 1);
+            const int64_t end = w.back >= kUnbounded ? Nq : from(k * 128 + 128 + w.back);
+            if (first < end) most_queries = std::max(most_queries, static_cast<int>((end + 127) / 128 - first / 128));
+        }
+        p.f_q = pieces(3.0 * most_keys, most_keys);
+        p.f_kv = pieces(4.0 * group * most_queries, static_cast<int64_t>(group) * most_queries);
+        p.kv_cut = p.f_kv > 1 ? p.kv_out_tiles : 0;
+        if (p.f_kv == 1 && sink_tiles > 0) {
+            p.f_kv = pieces(4.0 * group * p.q_tiles, static_cast<int64_t>(group) * p.q_tiles);
+            p.kv_cut = p.f_kv > 1 ? sink_tiles : 0;
+        }
+    }
+    p.q_whole = p.f_q > 1 ? 0 : p.query_items;
+    auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    p.stat_bytes = up(bh * 2 * p.q_tiles * 128 * 4) + 256;
+    p.part_kv_bytes = p.f_kv > 1 ? up(bhk * p.kv_cut * p.f_kv * 2 * 128 * D * 4) : 0;
+    p.part_q_bytes = p.f_q > 1 ? up(p.query_items * p.f_q * 128 * D * 4) : 0;
     return p;
 }
 

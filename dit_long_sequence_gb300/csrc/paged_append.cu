@@ -1,0 +1,70 @@
+// paged_append.cu -- K and V of new tokens into the pages of a cache.
+//
+// A copy: token t < new_lens[b] of sequence b goes to position kv_lens[b] -
+// new_lens[b] + t, row position mod page of the page that the table names.  HBM-bound
+// (each new element read and written once); a few tokens are bound by the chain of
+// dependent loads (lengths, table, then the store), which the source's load lies
+// beside.  16 bytes a thread and step, K and V of a token by neighbouring threads.
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+#include "window.h"
+
+namespace dit {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+// VEC: the sources allow 16-byte loads.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+    uint4 v[kUnroll];
+    uint16_t* dst[kUnroll];
+    const uint32_t first = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        dst[u] = nullptr;
+        const uint32_t i = first + u * kThreads;
+        if (i >= a.n) continue;
+        uint32_t part, t, head, d8;
+        const uint32_t token = a.div_parts.divmod(i, part);
+        const int b = static_cast<int>(a.div_t.divmod(token, t));
+        const bool is_v = part >= a.half;
+        head = a.div_d8.divmod(is_v ? part - a.half : part, d8);
+        const int len = max(__ldg(a.kv_lens + b), 0);
+        const int fresh = a.new_lens != nullptr ? min(max(__ldg(a.new_lens + b), 0), a.T) : a.T;
+        const int64_t at = static_cast<int64_t>(len) - fresh + t;
+        if (static_cast<int>(t) >= fresh || at < 0 || at >= a.capacity) continue;
+        const dit_strides4_t& ss = is_v ? a.sv : a.sk;
+        const uint16_t* src = (is_v ? a.v : a.k) + b * ss.b + static_cast<int64_t>(t) * ss.n + head * ss.h + 8 * d8;
+        if constexpr (VEC) {
+            v[u] = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __ldg(src + 2 * k) | (static_cast<uint32_t>(__ldg(src + 2 * k + 1)) << 16);
+            v[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        uint32_t row;
+        const uint32_t slot = a.div_page.divmod(static_cast<uint32_t>(at), row);
+        const int page = __ldg(a.table + b * a.table_sb + slot);
+        if (page < 0 || page >= a.pages) continue;
+        const dit_strides4_t& sd = is_v ? a.dv : a.dk;
+        dst[u] = (is_v ? a.v_cache : a.k_cache) + page * sd.b + static_cast<int64_t>(row) * sd.n + head * sd.h + 8 * d8;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (dst[u] != nullptr) *reinterpret_cast<uint4*>(dst[u]) = v[u];
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a, bool vec, cudaStream_t s) {
+    const unsigned blocks = (a.n + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+    if (vec) paged_append_kernel<true><<<blocks, kThreads, 0, s>>>(a);
+    else paged_append_kernel<false><<<blocks, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace dit

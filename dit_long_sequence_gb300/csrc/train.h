@@ -8,32 +8,12 @@
 #include <cuda_runtime.h>
 
 #include "dit_attn.h"
+#include "fast_div.h"
+#include "window_span.h"
 
 namespace dit {
 
-// ------------------------------------------------------------ index helpers
-
-// n / d and n % d for 0 <= n < 2^31 and a fixed 1 <= d < 2^31 by one multiply:
-// with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1,
-// n / d = (umulhi(n, m) + n) >> s: the round-up reciprocal of Granlund and
-// Montgomery, "Division by invariant integers using multiplication" (1994); the
-// sum stays below 2^32 because umulhi(n, m) <= n < 2^31.
-struct FastDiv {
-    uint32_t d, m, s;
-    FastDiv() : d(1), m(1), s(0) {}
-    explicit FastDiv(uint32_t div) : d(div), s(0) {
-        while ((uint64_t(1) << s) < d) ++s;
-        m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
-    __device__ __forceinline__ uint32_t divmod(uint32_t n, uint32_t& rem) const {
-        const uint32_t q = div(n);
-        rem = n - q * d;
-        return q;
-    }
-#endif
-};
+// ------------------------------------------------------------ launches
 
 #ifdef __CUDACC__
 // Launches a kernel that may be set up while the one before it on the stream
@@ -144,7 +124,15 @@ struct AttnBwdArgs {
     // a second kernel sums in piece order.
     int f_kv, f_q, q_whole;
     int n_kv_items, n_q_items;  // pieces counted
-    FastDiv div_f_kv, div_f_q, div_kv_tiles, div_q_tiles, div_bh, div_h;   // item -> piece, tile, head
+    // With a window (windowed) key items are (b, K/V head, tile), of which the leading
+    // kv_cut tiles of every head are cut, and their pieces (n_kv_cut in all) come
+    // first.  Otherwise Hkv = H, and all key items are cut or none.
+    bool windowed;
+    Window window;
+    int offset, Hkv, group;     // position of query 0, K/V heads, query heads of one
+    int kv_cut, n_kv_cut;
+    FastDiv div_hkv, div_group, div_kv_cut;
+    FastDiv div_f_kv, div_f_q, div_kv_tiles, div_q_tiles, div_bh, div_h;   // item -> piece, tile, head (window: div_kv_tiles of the uncut tiles)
     int grid;
     unsigned int* counter;      // items handed out beyond the first `grid` (nullptr: every grid-th)
     bool wide;                  // gradients may be stored 32 bytes at a time
