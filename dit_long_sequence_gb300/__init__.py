@@ -9,6 +9,8 @@ __all__ = ["attn_fwd", "attn_fwd_ws", "attn_fwd_workspace_bytes", "attn_fwd_mask
            "qkv_cast_fp8", "attn_fwd_fp8", "attn_fwd_fp8_ws",
            "attn_bwd", "attn_bwd_masked", "attn_bwd_workspace_bytes", "layer_norm_fwd", "layer_norm_bwd",
            "layer_norm_bwd_workspace_bytes", "rope", "rope_inv_freq",
+           "attn_fwd_window", "attn_fwd_window_workspace_bytes", "attn_bwd_window", "attn_bwd_window_workspace_bytes",
+           "paged_append", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
            "split_stacked_fp8", "check_watchdog", "watchdog_selftest", "DitError", "library_path"]
 
 

@@ -1,8 +1,8 @@
 """ctypes binding of libditattn.so (include/dit_attn.h).
 
-Argument marshalling only (for the training operators, whose small calls would
-be mostly marshalling, in the CPython extension csrc/py_calls.cpp, loaded at
-the first of them): tensors are passed as device pointers with their
+Argument marshalling only (for the training operators, windowed attention and
+the paged cache, whose small calls would be mostly marshalling, in the CPython
+extension csrc/py_calls.cpp, loaded at the first of them): tensors are passed as device pointers with their
 element strides and the current CUDA stream; every step of the computation
 runs in the library's kernels.  PyTorch supplies device memory and streams.
 There is no fallback: if the library is missing or a call fails, an exception
@@ -52,6 +52,16 @@ class AttnStrides(ctypes.Structure):
 
 class AttnBwdStrides(ctypes.Structure):
     _fields_ = [(n, Strides4) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
+
+
+class Window(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("left", "right", "sinks", "frame")]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_strides", Strides4), ("v_strides", Strides4), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int),
+                ("kv_lens", ctypes.c_void_p)]
 
 
 DIT_ROPE_INTERLEAVED, DIT_ROPE_HALF = 0, 1
@@ -109,6 +119,23 @@ def _declare(lib):
                                         _i, _i, _i, _i, _vp, _i64, _i64, _i, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
     lib.dit_attn_bwd_workspace_bytes.restype = _sz
     lib.dit_attn_bwd_workspace_bytes.argtypes = [_i] * 7
+    _win, _cache = ctypes.POINTER(Window), ctypes.POINTER(PagedCache)
+    lib.dit_attn_fwd_window.restype = _i
+    lib.dit_attn_fwd_window.argtypes = [_vp, _vp, _vp, ctypes.POINTER(AttnStrides), _i, _i, _i, _i, _i, _i, _i, _win, _i, _f, _vp, _i, _vp,
+                                        _vp, _sz, _vp]
+    lib.dit_attn_fwd_window_workspace_bytes.restype = _sz
+    lib.dit_attn_fwd_window_workspace_bytes.argtypes = [_i] * 6 + [_win, _i]
+    lib.dit_attn_bwd_window.restype = _i
+    lib.dit_attn_bwd_window.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(AttnBwdStrides), _i, _i, _i, _i, _i, _i, _i,
+                                        _win, _i, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
+    lib.dit_attn_bwd_window_workspace_bytes.restype = _sz
+    lib.dit_attn_bwd_window_workspace_bytes.argtypes = [_i] * 7 + [_win, _i]
+    lib.dit_paged_append.restype = _i
+    lib.dit_paged_append.argtypes = [_vp, _st, _vp, _st, _cache, _vp, _i, _i, _i, _i, _vp]
+    lib.dit_attn_fwd_paged.restype = _i
+    lib.dit_attn_fwd_paged.argtypes = [_vp, _st, _cache, _vp, _i, _i, _i, _i, _i, _win, _f, _vp, _i, _st, _vp, _vp, _sz, _vp]
+    lib.dit_attn_fwd_paged_workspace_bytes.restype = _sz
+    lib.dit_attn_fwd_paged_workspace_bytes.argtypes = [_i] * 7 + [_win]
     lib.dit_layer_norm_fwd.restype = _i
     lib.dit_layer_norm_fwd.argtypes = [_vp, _i, _st, _i, _i, _i, _i, _vp, _vp, _i, _f, _i, _vp, _i, _st, _vp, _vp, _vp]
     lib.dit_layer_norm_bwd.restype = _i
@@ -147,14 +174,16 @@ def _load_calls():
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
         "dit_attn_bwd", "dit_attn_bwd_masked", "dit_attn_bwd_workspace_bytes", "dit_layer_norm_fwd",
-        "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope")))
+        "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope", "dit_attn_fwd_window",
+        "dit_attn_fwd_window_workspace_bytes", "dit_attn_bwd_window", "dit_attn_bwd_window_workspace_bytes", "dit_paged_append",
+        "dit_attn_fwd_paged", "dit_attn_fwd_paged_workspace_bytes")))
     return module
 
 
 class _Calls:
     """The extension's functions, loaded when one is first asked for: the other
     calls do without it (and without what it is built with)."""
-    _NAMES = ("attn_bwd", "norm_fwd", "norm_bwd", "rope", "bind")
+    _NAMES = ("attn_bwd", "norm_fwd", "norm_bwd", "rope", "window_fwd", "window_bwd", "append", "paged", "bind")
 
     def __getattr__(self, name):
         if name not in self._NAMES:
@@ -190,7 +219,9 @@ EXPORTS = ("dit_attn_fwd", "dit_attn_fwd_ws", "dit_attn_fwd_workspace_bytes", "d
            "dit_check_watchdog",
            "dit_watchdog_selftest", "dit_version",
            "dit_attn_bwd", "dit_attn_bwd_masked", "dit_attn_bwd_workspace_bytes", "dit_layer_norm_fwd",
-           "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope", "dit_rope_inv_freq")
+           "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope", "dit_rope_inv_freq",
+           "dit_attn_fwd_window", "dit_attn_fwd_window_workspace_bytes", "dit_attn_bwd_window", "dit_attn_bwd_window_workspace_bytes",
+           "dit_paged_append", "dit_attn_fwd_paged", "dit_attn_fwd_paged_workspace_bytes")
 
 
 class DitError(RuntimeError):
@@ -685,6 +716,135 @@ def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
     if rc != DIT_OK:
         raise DitError(rc, "dit_attn_bwd_masked")
     return tuple(grads)
+
+
+def _window(left, right, sinks, frame):
+    return ctypes.byref(Window(-1 if left is None else int(left), -1 if right is None else int(right), int(sinks), int(frame)))
+
+
+def attn_fwd_window_workspace_bytes(B: int, Nq: int, H: int, Hkv: int, D: int, key_valid_len: int, *, left: int | None = None,
+                                    right: int | None = 0, sinks: int = 0, frame: int = 1, offset: int = 0) -> int:
+    """Workspace of attn_fwd_window (current device; 0: none)."""
+    return int(_lib.dit_attn_fwd_window_workspace_bytes(int(B), int(Nq), int(H), int(Hkv), int(D), int(key_valid_len),
+                                                        _window(left, right, sinks, frame), int(offset)))
+
+
+def _window_fwd_space(args):
+    q, k, left, right, sinks, frame, offset, key_valid_len = args[0], args[1], *args[3:9]
+    (B, Nq, H, D), (Nkv, Hkv) = q.shape, k.shape[1:3]
+    return attn_fwd_window_workspace_bytes(B, Nq, H, Hkv, D, Nkv if key_valid_len is None else key_valid_len, left=left, right=right,
+                                           sinks=sinks, frame=frame, offset=offset)
+
+
+def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, left: int | None = None, right: int | None = 0,
+                    sinks: int = 0, frame: int = 1, offset: int = 0, key_valid_len: int | None = None, scale: float | None = None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """attn_fwd over a sliding window with sinks, through `dit_attn_fwd_window`.
+
+    A query at position p (its row plus offset), in frame f = p // frame, sees the
+    keys of the frames f - left to f + right (None: no bound on that side) and, of
+    what lies before them, the first `sinks` tokens.  The defaults are the causal
+    mask; frame=n, right=0 lets a video's frames of n tokens see themselves and
+    the past.  q [B, Nq, H, D], k/v [B, Nkv, Hkv, D] bf16, strided as in attn_fwd; query head
+    h reads K/V head h // (H // Hkv).  Returns (out [B, Nq, H, D] in out_dtype, lse [B, H, Nq]
+    fp32); a row that sees nothing gets 0 and -inf."""
+    args = (q, k, v, left, right, sinks, frame, offset, key_valid_len, scale, out, lse, _is_fp32(out_dtype), workspace)
+    if stream is None:
+        rc, o, l = _calls.window_fwd(*args, _stream_ptr(None))
+    else:
+        rc, o, l = _on_stream(_calls.window_fwd, args, stream, (out, lse), _window_fwd_space)
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_attn_fwd_window")
+    return o, l
+
+
+def attn_bwd_window_workspace_bytes(B: int, Nq: int, Nkv: int, H: int, Hkv: int, D: int, key_valid_len: int, *, left: int | None = None,
+                                    right: int | None = 0, sinks: int = 0, frame: int = 1, offset: int = 0) -> int:
+    """Workspace of attn_bwd_window (current device)."""
+    return int(_lib.dit_attn_bwd_window_workspace_bytes(int(B), int(Nq), int(Nkv), int(H), int(Hkv), int(D), int(key_valid_len),
+                                                        _window(left, right, sinks, frame), int(offset)))
+
+
+def _window_bwd_space(args):
+    left, right, sinks, frame, offset, q, k, key_valid_len = *args[:7], args[14]
+    (B, Nq, H, D), (Nkv, Hkv) = q.shape, k.shape[1:3]
+    return attn_bwd_window_workspace_bytes(B, Nq, Nkv, H, Hkv, D, Nkv if key_valid_len is None else key_valid_len, left=left, right=right,
+                                           sinks=sinks, frame=frame, offset=offset)
+
+
+def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor, *,
+                    left: int | None = None, right: int | None = 0, sinks: int = 0, frame: int = 1, offset: int = 0,
+                    dlse: torch.Tensor | None = None, key_valid_len: int | None = None, scale: float | None = None,
+                    dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                    grad_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of attn_fwd_window through `dit_attn_bwd_window`: attn_bwd with the
+    forward call's window; dk and dv [B, Nkv, Hkv, D] are summed over the query heads
+    that share them.  Returns (dq, dk, dv)."""
+    args = (left, right, sinks, frame, offset, q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv,
+            _is_fp32(grad_dtype), workspace)
+    if stream is None:
+        rc, *grads = _calls.window_bwd(*args, _stream_ptr(None))
+    else:
+        rc, *grads = _on_stream(_calls.window_bwd, args, stream, (dq, dk, dv), _window_bwd_space)
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_attn_bwd_window")
+    return tuple(grads)
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                 kv_lens: torch.Tensor, *, new_lens: torch.Tensor | None = None, stream=None):
+    """New tokens' K and V [B, T, Hkv, D] (bf16, channels contiguous, other strides free)
+    into a paged cache, through `dit_paged_append`.
+
+    k_cache, v_cache: bf16 [pages, page_size, Hkv, D], page_size a multiple of 8 (two
+    tensors, or views of one).  page_table: int32 [B, width], the pages of each
+    sequence in order; kv_lens: int32 [B], its tokens, the new ones included; new_lens:
+    int32 [B], how many of the T are new (None: all).  Token t of sequence b goes to
+    position kv_lens[b] - new_lens[b] + t; one without a page is dropped."""
+    args = (k, v, k_cache, v_cache, page_table, kv_lens, new_lens)
+    if stream is None:
+        rc, = _calls.append(*args, _stream_ptr(None))
+    else:
+        rc, = _on_stream(_calls.append, args, stream, ())
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_paged_append")
+
+
+def attn_fwd_paged_workspace_bytes(B: int, T: int, H: int, Hkv: int, D: int, page_size: int, table_width: int, *, left: int | None = None,
+                                   right: int | None = 0, sinks: int = 0, frame: int = 1) -> int:
+    """Workspace of attn_fwd_paged (current device)."""
+    return int(_lib.dit_attn_fwd_paged_workspace_bytes(int(B), int(T), int(H), int(Hkv), int(D), int(page_size), int(table_width),
+                                                       _window(left, right, sinks, frame)))
+
+
+def _paged_space(args):
+    q, cache, table = args[0], args[1], args[3]
+    B, T, H, D = q.shape
+    left, right, sinks, frame = args[6:10]
+    return attn_fwd_paged_workspace_bytes(B, T, H, cache.shape[2], D, cache.shape[1], table.shape[1], left=left, right=right, sinks=sinks,
+                                          frame=frame)
+
+
+def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                   q_lens: torch.Tensor | None = None, left: int | None = None, right: int | None = 0, sinks: int = 0, frame: int = 1,
+                   scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None, stream=None):
+    """attn_fwd_window of a chunk of new tokens, from one to thousands a sequence, over a
+    paged cache that they have been appended to, through `dit_attn_fwd_paged`.
+
+    q [B, T, H, D] bf16; the cache as in paged_append.  Row t < q_lens[b] (None: T) of
+    sequence b is the query at position kv_lens[b] - q_lens[b] + t; the rows behind are
+    left as they were in out and lse.  A page index outside the cache (an evicted page)
+    holds no keys.  The window as in attn_fwd_window.  Returns (out, lse [B, H, T])."""
+    args = (q, k_cache, v_cache, page_table, kv_lens, q_lens, left, right, sinks, frame, scale, out, lse, _is_fp32(out_dtype), workspace)
+    if stream is None:
+        rc, o, l = _calls.paged(*args, _stream_ptr(None))
+    else:
+        rc, o, l = _on_stream(_calls.paged, args, stream, (out, lse), _paged_space)
+    if rc != DIT_OK:
+        raise DitError(rc, "dit_attn_fwd_paged")
+    return o, l
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,

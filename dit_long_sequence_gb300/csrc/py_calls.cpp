@@ -1,5 +1,5 @@
-// py_calls.cpp -- the training operators' calls from Python, as a CPython
-// extension module: argument checks, output and workspace allocation through
+// py_calls.cpp -- the calls of the training operators, of windowed attention and of
+// the paged cache from Python, as a CPython extension module: argument checks, output and workspace allocation through
 // PyTorch, and one call of the C ABI (include/dit_attn.h).
 //
 // Marshalling only.  A small call's time is its host time: through ctypes a
@@ -34,6 +34,13 @@ decltype(&dit_layer_norm_fwd) g_norm_fwd;
 decltype(&dit_layer_norm_bwd) g_norm_bwd;
 decltype(&dit_layer_norm_bwd_workspace_bytes) g_norm_bwd_ws;
 decltype(&dit_rope) g_rope;
+decltype(&dit_attn_fwd_window) g_window_fwd;
+decltype(&dit_attn_fwd_window_workspace_bytes) g_window_fwd_ws;
+decltype(&dit_attn_bwd_window) g_window_bwd;
+decltype(&dit_attn_bwd_window_workspace_bytes) g_window_bwd_ws;
+decltype(&dit_paged_append) g_append;
+decltype(&dit_attn_fwd_paged) g_paged;
+decltype(&dit_attn_fwd_paged_workspace_bytes) g_paged_ws;
 
 // A failed check, carried to the function's end.
 struct Refused {
@@ -130,82 +137,264 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
     return nullptr;
 }
 
+// left, right, sinks, frame at a[0..3]; None: no bound on that side.
+dit_window_t window_of(PyObject* const* a) {
+    dit_window_t w;
+    w.left = a[0] == Py_None ? -1 : small_int(a[0]);
+    w.right = a[1] == Py_None ? -1 : small_int(a[1]);
+    w.sinks = small_int(a[2]);
+    w.frame = small_int(a[3]);
+    if ((a[0] != Py_None && w.left < 0) || (a[1] != Py_None && w.right < 0)) value_error("left and right are None or at least 0");
+    if (w.sinks < 0 || w.frame < 1) value_error("sinks must be at least 0 and frame at least 1");
+    return w;
+}
+float scale_of(PyObject* o, int D) {
+    return o == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D > 0 ? D : 1))) : static_cast<float>(real(o));
+}
+
 // attn_bwd(q, k, v, out, lse, dout, dlse, mask_bits, mask_rows, key_valid_len, scale,
-//          dq, dk, dv, grads_fp32, workspace, stream); None where there is none
+//          dq, dk, dv, grads_fp32, workspace, stream); None where there is none.
+// With a window: its heads may share K and V, q begins at `offset`.
+PyObject* attn_bwd_of(PyObject* const* a, const dit_window_t* window, int offset) {
+    const char* kIn = "q, k, v and dout must be bf16 CUDA tensors";
+    const at::Tensor &q = tensor(a[0], kIn), &k = tensor(a[1], kIn), &v = tensor(a[2], kIn), &dout = tensor(a[5], kIn);
+    const at::Tensor& out = tensor(a[3], "out must be a tensor");
+    const at::Tensor& lse = tensor(a[4], "lse must be a tensor");
+    const at::Tensor* dlse = maybe(a[6], "dlse must be a tensor");
+    const at::Tensor* mask = maybe(a[7], "mask_bits must be a tensor");
+    for (const at::Tensor* t : {&q, &k, &v, &dout})
+        if (!is(*t, at::kBFloat16) || !t->is_cuda()) type_error(kIn);
+    if (q.dim() != 4 || k.dim() != 4) value_error("q, k and v must be [B, N, H, D]");
+    const int B = extent(q.size(0)), Nq = extent(q.size(1)), H = extent(q.size(2)), D = extent(q.size(3));
+    const int Nkv = extent(k.size(1));
+    const int Hkv = extent(k.size(2));
+    if (k.size(0) != B || (window == nullptr && Hkv != H) || k.size(3) != D || v.sizes() != k.sizes() || dout.sizes() != q.sizes())
+        value_error("k and v must be [B, Nkv, H, D] matching q, dout [B, Nq, H, D]");
+    if (!bf16_or_f32(out) || out.sizes() != q.sizes()) value_error("out must be a [B, Nq, H, D] fp32 or bf16 tensor");
+    const int64_t rows[3] = {B, H, Nq};
+    if (!contiguous_f32(lse, rows) || (dlse != nullptr && !contiguous_f32(*dlse, rows)))
+        value_error("lse and dlse must be contiguous fp32 [B, H, Nq] tensors");
+    const int kvl = a[9] == Py_None ? Nkv : small_int(a[9]);
+    int mask_rows = 0;
+    if (mask != nullptr) {
+        if (!is(*mask, at::kInt) || mask->dim() != 3 || !mask->is_cuda() || (mask->size(2) > 1 && mask->stride(2) != 1))
+            value_error("mask_bits must be an int32 CUDA tensor [B or 1, rows, words], words contiguous");
+        if (mask->size(0) != 1 && mask->size(0) != B) value_error("mask_bits must have B or 1 batch entries");
+        mask_rows = a[8] == Py_None ? extent(mask->size(1)) : small_int(a[8]);
+        if (mask_rows > mask->size(1)) value_error("mask_rows exceeds the mask's rows");
+        if (kvl >= 0 && 4 * ((static_cast<int64_t>(kvl) + 127) / 128) > mask->size(2))
+            value_error("mask_bits must have 4 * ceil(key_valid_len / 128) words a row");
+    }
+    const float scale = scale_of(a[10], D);
+    const at::Tensor* given[3] = {maybe(a[11], "dq must be a tensor"), maybe(a[12], "dk must be a tensor"),
+                                  maybe(a[13], "dv must be a tensor")};
+    at::ScalarType type = integer(a[14]) ? at::kFloat : at::kBFloat16;
+    for (const at::Tensor* g : given)
+        if (g != nullptr) {
+            type = g->scalar_type();
+            break;
+        }
+    at::Tensor grads[3];
+    for (int i = 0; i < 3; ++i)
+        if (given[i] != nullptr) {
+            if (!bf16_or_f32(*given[i]) || !is(*given[i], type) || given[i]->sizes() != (i == 0 ? q : k).sizes())
+                value_error("dq must be [B, Nq, H, D], dk and dv [B, Nkv, H, D] tensors of one type, fp32 or bf16");
+            grads[i] = *given[i];
+        }
+    const at::Tensor* workspace = maybe(a[15], "workspace must be a tensor");
+    const dit_stream_t stream = stream_of(a[16]);
+    at::Tensor own;
+    const int rc = unlocked([&] {
+        for (int i = 0; i < 3; ++i)
+            if (given[i] == nullptr) grads[i] = fresh((i == 0 ? q : k).sizes(), type, q);
+        size_t ws_bytes = 0;
+        if (workspace != nullptr) {
+            ws_bytes = workspace->nbytes();
+        } else if ((ws_bytes = window != nullptr ? g_window_bwd_ws(B, Nq, Nkv, H, Hkv, D, kvl, window, offset)
+                                                 : g_attn_bwd_ws(B, Nq, Nkv, H, D, kvl, mask != nullptr)) > 0) {
+            own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, q);
+            workspace = &own;
+        }
+        const dit_attn_bwd_strides_t st{strides4(q),        strides4(k),        strides4(v),        strides4(out), strides4(dout),
+                                        strides4(grads[0]), strides4(grads[1]), strides4(grads[2])};
+        const dit_dtype_t gt = type == at::kFloat ? DIT_F32 : DIT_BF16;
+        if (window != nullptr)
+            return g_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
+                                dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, Hkv, D, kvl, window, offset, scale,
+                                grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), gt, data<void>(workspace), ws_bytes,
+                                stream);
+        if (mask != nullptr)
+            return g_attn_bwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
+                                     dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, data<uint32_t>(mask),
+                                     mask->size(0) == 1 ? 0 : mask->stride(0), mask->stride(1), mask_rows, scale,
+                                     grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), gt,
+                                     data<void>(workspace), ws_bytes, stream);
+        return g_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
+                          dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, scale, grads[0].data_ptr(),
+                          grads[1].data_ptr(), grads[2].data_ptr(), gt, data<void>(workspace), ws_bytes, stream);
+    });
+    return result(rc, {&grads[0], &grads[1], &grads[2]});
+}
 PyObject* attn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 17, [&] {
-        const char* kIn = "q, k, v and dout must be bf16 CUDA tensors";
-        const at::Tensor &q = tensor(a[0], kIn), &k = tensor(a[1], kIn), &v = tensor(a[2], kIn), &dout = tensor(a[5], kIn);
-        const at::Tensor& out = tensor(a[3], "out must be a tensor");
-        const at::Tensor& lse = tensor(a[4], "lse must be a tensor");
-        const at::Tensor* dlse = maybe(a[6], "dlse must be a tensor");
-        const at::Tensor* mask = maybe(a[7], "mask_bits must be a tensor");
-        for (const at::Tensor* t : {&q, &k, &v, &dout})
+    return guarded(n, 17, [&] { return attn_bwd_of(a, nullptr, 0); });
+}
+// window_bwd(left, right, sinks, frame, offset, then attn_bwd's arguments without a mask)
+PyObject* window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 22, [&] {
+        const dit_window_t w = window_of(a);
+        return attn_bwd_of(a + 5, &w, small_int(a[4]));
+    });
+}
+
+// A forward call's results, given ones checked.
+struct Results {
+    at::Tensor out, lse;
+    const at::Tensor *given_out, *given_lse;
+    at::ScalarType type;
+    Results(PyObject* o, PyObject* l, PyObject* fp32, const at::Tensor& q) {
+        given_out = maybe(o, "out must be a tensor");
+        given_lse = maybe(l, "lse must be a tensor");
+        type = integer(fp32) ? at::kFloat : at::kBFloat16;
+        const int64_t rows[3] = {q.size(0), q.size(2), q.size(1)};
+        if (given_out != nullptr) {
+            if (!bf16_or_f32(*given_out) || given_out->sizes() != q.sizes()) value_error("out must be a [B, N, H, D] fp32 or bf16 tensor");
+            out = *given_out;
+        }
+        if (given_lse != nullptr) {
+            if (!contiguous_f32(*given_lse, rows)) value_error("lse must be a contiguous fp32 [B, H, N] tensor");
+            lse = *given_lse;
+        }
+    }
+    void allocate(const at::Tensor& q) {
+        if (given_out == nullptr) out = fresh(q.sizes(), type, q);
+        if (given_lse == nullptr) lse = fresh({q.size(0), q.size(2), q.size(1)}, at::kFloat, q);
+    }
+};
+
+// window_fwd(q, k, v, left, right, sinks, frame, offset, key_valid_len, scale, out, lse, out_fp32, workspace, stream)
+PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&] {
+        const char* kIn = "q, k and v must be bf16 CUDA tensors";
+        const at::Tensor &q = tensor(a[0], kIn), &k = tensor(a[1], kIn), &v = tensor(a[2], kIn);
+        for (const at::Tensor* t : {&q, &k, &v})
             if (!is(*t, at::kBFloat16) || !t->is_cuda()) type_error(kIn);
         if (q.dim() != 4 || k.dim() != 4) value_error("q, k and v must be [B, N, H, D]");
         const int B = extent(q.size(0)), Nq = extent(q.size(1)), H = extent(q.size(2)), D = extent(q.size(3));
-        const int Nkv = extent(k.size(1));
-        if (k.size(0) != B || k.size(2) != H || k.size(3) != D || v.sizes() != k.sizes() || dout.sizes() != q.sizes())
-            value_error("k and v must be [B, Nkv, H, D] matching q, dout [B, Nq, H, D]");
-        if (!bf16_or_f32(out) || out.sizes() != q.sizes()) value_error("out must be a [B, Nq, H, D] fp32 or bf16 tensor");
-        const int64_t rows[3] = {B, H, Nq};
-        if (!contiguous_f32(lse, rows) || (dlse != nullptr && !contiguous_f32(*dlse, rows)))
-            value_error("lse and dlse must be contiguous fp32 [B, H, Nq] tensors");
-        const int kvl = a[9] == Py_None ? Nkv : small_int(a[9]);
-        int mask_rows = 0;
-        if (mask != nullptr) {
-            if (!is(*mask, at::kInt) || mask->dim() != 3 || !mask->is_cuda() || (mask->size(2) > 1 && mask->stride(2) != 1))
-                value_error("mask_bits must be an int32 CUDA tensor [B or 1, rows, words], words contiguous");
-            if (mask->size(0) != 1 && mask->size(0) != B) value_error("mask_bits must have B or 1 batch entries");
-            mask_rows = a[8] == Py_None ? extent(mask->size(1)) : small_int(a[8]);
-            if (mask_rows > mask->size(1)) value_error("mask_rows exceeds the mask's rows");
-            if (kvl >= 0 && 4 * ((static_cast<int64_t>(kvl) + 127) / 128) > mask->size(2))
-                value_error("mask_bits must have 4 * ceil(key_valid_len / 128) words a row");
-        }
-        const float scale = a[10] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D > 0 ? D : 1)))
-                                             : static_cast<float>(real(a[10]));
-        const at::Tensor* given[3] = {maybe(a[11], "dq must be a tensor"), maybe(a[12], "dk must be a tensor"),
-                                      maybe(a[13], "dv must be a tensor")};
-        at::ScalarType type = integer(a[14]) ? at::kFloat : at::kBFloat16;
-        for (const at::Tensor* g : given)
-            if (g != nullptr) {
-                type = g->scalar_type();
-                break;
-            }
-        at::Tensor grads[3];
-        for (int i = 0; i < 3; ++i)
-            if (given[i] != nullptr) {
-                if (!bf16_or_f32(*given[i]) || !is(*given[i], type) || given[i]->sizes() != (i == 0 ? q : k).sizes())
-                    value_error("dq must be [B, Nq, H, D], dk and dv [B, Nkv, H, D] tensors of one type, fp32 or bf16");
-                grads[i] = *given[i];
-            }
-        const at::Tensor* workspace = maybe(a[15], "workspace must be a tensor");
-        const dit_stream_t stream = stream_of(a[16]);
+        const int Nkv = extent(k.size(1)), Hkv = extent(k.size(2));
+        if (k.size(0) != B || k.size(3) != D || v.sizes() != k.sizes()) value_error("k and v must be [B, Nkv, Hkv, D] matching q");
+        const dit_window_t w = window_of(a + 3);
+        const int offset = small_int(a[7]), kvl = a[8] == Py_None ? Nkv : small_int(a[8]);
+        const float scale = scale_of(a[9], D);
+        Results r(a[10], a[11], a[12], q);
+        const at::Tensor* workspace = maybe(a[13], "workspace must be a tensor");
+        const dit_stream_t stream = stream_of(a[14]);
         at::Tensor own;
         const int rc = unlocked([&] {
-            for (int i = 0; i < 3; ++i)
-                if (given[i] == nullptr) grads[i] = fresh((i == 0 ? q : k).sizes(), type, q);
+            r.allocate(q);
             size_t ws_bytes = 0;
             if (workspace != nullptr) {
                 ws_bytes = workspace->nbytes();
-            } else if ((ws_bytes = g_attn_bwd_ws(B, Nq, Nkv, H, D, kvl, mask != nullptr)) > 0) {
+            } else if ((ws_bytes = g_window_fwd_ws(B, Nq, H, Hkv, D, kvl, &w, offset)) > 0) {
                 own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, q);
                 workspace = &own;
             }
-            const dit_attn_bwd_strides_t st{strides4(q),        strides4(k),        strides4(v),        strides4(out), strides4(dout),
-                                            strides4(grads[0]), strides4(grads[1]), strides4(grads[2])};
-            const dit_dtype_t gt = type == at::kFloat ? DIT_F32 : DIT_BF16;
-            if (mask != nullptr)
-                return g_attn_bwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
-                                         dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, data<uint32_t>(mask),
-                                         mask->size(0) == 1 ? 0 : mask->stride(0), mask->stride(1), mask_rows, scale,
-                                         grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), gt,
-                                         data<void>(workspace), ws_bytes, stream);
-            return g_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), code(out), data<float>(&lse),
-                              dout.data_ptr(), data<float>(dlse), &st, B, Nq, Nkv, H, D, kvl, scale, grads[0].data_ptr(),
-                              grads[1].data_ptr(), grads[2].data_ptr(), gt, data<void>(workspace), ws_bytes, stream);
+            const dit_attn_strides_t st{strides4(q), strides4(k), strides4(v), strides4(r.out)};
+            return g_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), &st, B, Nq, Nkv, H, Hkv, D, kvl, &w, offset, scale,
+                                r.out.data_ptr(), code(r.out), data<float>(&r.lse), data<void>(workspace), ws_bytes, stream);
         });
-        return result(rc, {&grads[0], &grads[1], &grads[2]});
+        return result(rc, {&r.out, &r.lse});
+    });
+}
+
+// The cache of k_cache, v_cache [pages, page, Hkv, D], page_table [B, width], kv_lens [B] at a[0..3].
+dit_paged_cache_t cache_of(PyObject* const* a, int64_t B, int64_t D) {
+    const char* kCache = "k_cache and v_cache must be bf16 CUDA tensors";
+    const at::Tensor &k = tensor(a[0], kCache), &v = tensor(a[1], kCache);
+    for (const at::Tensor* t : {&k, &v})
+        if (!is(*t, at::kBFloat16) || !t->is_cuda()) type_error(kCache);
+    if (k.dim() != 4 || v.sizes() != k.sizes() || k.size(3) != D) value_error("k_cache and v_cache must be [pages, page_size, Hkv, D]");
+    const char* kTable = "page_table must be an int32 CUDA tensor [B, width], each row contiguous";
+    const at::Tensor& table = tensor(a[2], kTable);
+    if (!is(table, at::kInt) || !table.is_cuda()) type_error(kTable);
+    if (table.dim() != 2 || table.size(0) != B || (table.size(1) > 1 && table.stride(1) != 1)) value_error(kTable);
+    const char* kLens = "kv_lens must be a contiguous int32 CUDA tensor [B]";
+    const at::Tensor& lens = tensor(a[3], kLens);
+    if (!is(lens, at::kInt) || !lens.is_cuda()) type_error(kLens);
+    if (lens.dim() != 1 || lens.size(0) != B || !lens.is_contiguous()) value_error(kLens);
+    dit_paged_cache_t c;
+    c.k = k.data_ptr();
+    c.v = v.data_ptr();
+    c.k_strides = strides4(k);
+    c.v_strides = strides4(v);
+    c.pages = extent(k.size(0));
+    c.page_size = extent(k.size(1));
+    c.table = data<const int32_t>(&table);
+    c.table_stride = table.stride(0);
+    c.table_width = extent(table.size(1));
+    c.kv_lens = data<const int32_t>(&lens);
+    return c;
+}
+// An int32 [B] tensor of new tokens, or none.
+const int32_t* counts_of(PyObject* o, int64_t B, const char* what) {
+    const at::Tensor* t = maybe(o, what);
+    if (t == nullptr) return nullptr;
+    if (!is(*t, at::kInt) || !t->is_cuda()) type_error(what);
+    if (t->dim() != 1 || t->size(0) != B || !t->is_contiguous()) value_error(what);
+    return data<const int32_t>(t);
+}
+
+// append(k, v, k_cache, v_cache, page_table, kv_lens, new_lens, stream)
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&] {
+        const char* kIn = "k and v must be bf16 CUDA tensors";
+        const at::Tensor &k = tensor(a[0], kIn), &v = tensor(a[1], kIn);
+        for (const at::Tensor* t : {&k, &v})
+            if (!is(*t, at::kBFloat16) || !t->is_cuda()) type_error(kIn);
+        if (k.dim() != 4 || v.sizes() != k.sizes()) value_error("k and v must be [B, T, Hkv, D] tensors of one shape");
+        const int B = extent(k.size(0)), T = extent(k.size(1)), Hkv = extent(k.size(2)), D = extent(k.size(3));
+        const dit_paged_cache_t c = cache_of(a + 2, B, D);
+        if (tensor(a[2], kIn).size(2) != Hkv) value_error("k_cache and v_cache must have the heads of k and v");
+        const int32_t* lens = counts_of(a[6], B, "new_lens must be a contiguous int32 CUDA tensor [B]");
+        const dit_stream_t stream = stream_of(a[7]);
+        const int rc = unlocked([&] {
+            const dit_strides4_t sk = strides4(k), sv = strides4(v);
+            return g_append(k.data_ptr(), &sk, v.data_ptr(), &sv, &c, lens, B, T, Hkv, D, stream);
+        });
+        return result(rc, {});
+    });
+}
+
+// paged(q, k_cache, v_cache, page_table, kv_lens, q_lens, left, right, sinks, frame, scale, out, lse, out_fp32, workspace, stream)
+PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 16, [&] {
+        const char* kIn = "q must be a bf16 CUDA tensor";
+        const at::Tensor& q = tensor(a[0], kIn);
+        if (!is(q, at::kBFloat16) || !q.is_cuda()) type_error(kIn);
+        if (q.dim() != 4) value_error("q must be [B, T, H, D]");
+        const int B = extent(q.size(0)), T = extent(q.size(1)), H = extent(q.size(2)), D = extent(q.size(3));
+        const dit_paged_cache_t c = cache_of(a + 1, B, D);
+        const int Hkv = extent(tensor(a[1], kIn).size(2));
+        const int32_t* lens = counts_of(a[5], B, "q_lens must be a contiguous int32 CUDA tensor [B]");
+        const dit_window_t w = window_of(a + 6);
+        const float scale = scale_of(a[10], D);
+        Results r(a[11], a[12], a[13], q);
+        const at::Tensor* workspace = maybe(a[14], "workspace must be a tensor");
+        const dit_stream_t stream = stream_of(a[15]);
+        at::Tensor own;
+        const int rc = unlocked([&] {
+            r.allocate(q);
+            size_t ws_bytes = 0;
+            if (workspace != nullptr) {
+                ws_bytes = workspace->nbytes();
+            } else if ((ws_bytes = g_paged_ws(B, T, H, Hkv, D, c.page_size, c.table_width, &w)) > 0) {
+                own = fresh({static_cast<int64_t>(ws_bytes)}, at::kByte, q);
+                workspace = &own;
+            }
+            const dit_strides4_t sq = strides4(q), so = strides4(r.out);
+            return g_paged(q.data_ptr(), &sq, &c, lens, B, T, H, Hkv, D, &w, scale, r.out.data_ptr(), code(r.out), &so,
+                           data<float>(&r.lse), data<void>(workspace), ws_bytes, stream);
+        });
+        return result(rc, {&r.out, &r.lse});
     });
 }
 
@@ -385,11 +574,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of the seven C functions above, in that order)
+// bind(addresses of the C functions above, in that order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 7, [&]() -> PyObject* {
-        void* p[7];
-        for (int i = 0; i < 7; ++i) {
+    return guarded(n, 14, [&]() -> PyObject* {
+        void* p[14];
+        for (int i = 0; i < 14; ++i) {
             p[i] = PyLong_AsVoidPtr(a[i]);
             if (p[i] == nullptr) {
                 if (PyErr_Occurred()) python_error();
@@ -403,14 +592,22 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[4]);
         g_norm_bwd_ws = reinterpret_cast<decltype(g_norm_bwd_ws)>(p[5]);
         g_rope = reinterpret_cast<decltype(g_rope)>(p[6]);
+        g_window_fwd = reinterpret_cast<decltype(g_window_fwd)>(p[7]);
+        g_window_fwd_ws = reinterpret_cast<decltype(g_window_fwd_ws)>(p[8]);
+        g_window_bwd = reinterpret_cast<decltype(g_window_bwd)>(p[9]);
+        g_window_bwd_ws = reinterpret_cast<decltype(g_window_bwd_ws)>(p[10]);
+        g_append = reinterpret_cast<decltype(g_append)>(p[11]);
+        g_paged = reinterpret_cast<decltype(g_paged)>(p[12]);
+        g_paged_ws = reinterpret_cast<decltype(g_paged_ws)>(p[13]);
         return Py_NewRef(Py_None);
     });
 }
 
 #define DIT_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {DIT_METHOD(attn_bwd), DIT_METHOD(norm_fwd), DIT_METHOD(norm_bwd), DIT_METHOD(rope), DIT_METHOD(bind),
+                          DIT_METHOD(window_fwd), DIT_METHOD(window_bwd), DIT_METHOD(append), DIT_METHOD(paged),
                           {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "dit_calls", "calls of libditattn's training operators", -1, kMethods,
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "dit_calls", "calls of libditattn's operators", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -27,6 +27,12 @@
  *   dit_attn_bwd           gradients of Q, K, V from the gradient of O, the
  *                          probabilities recomputed from the LSE
  *                          (dit_attn_bwd_masked with the general bit mask).
+ *   dit_attn_fwd_window    attention over a sliding window of frames (or tokens)
+ *   dit_attn_bwd_window    and a few first tokens that stay visible, causal or
+ *                          not, K and V shared by groups of heads; its gradients.
+ *   dit_paged_append       the serving side: new tokens' K and V into the pages
+ *   dit_attn_fwd_paged     of a cache, and the same attention of a chunk of new
+ *                          tokens, from one to thousands, over those pages.
  *   dit_layer_norm_fwd     layer norm / RMS norm of strided rows, one weight or
  *   dit_layer_norm_bwd     one per batch entry, and its gradients.
  *   dit_rope               rotary positions of a strided [B, N, H, D] view, and
@@ -544,6 +550,129 @@ dit_status_t dit_attn_bwd_masked(const void *q, const void *k, const void *v,
  * 0 when there is nothing to compute.  Host only.
  */
 size_t dit_attn_bwd_workspace_bytes(int B, int Nq, int Nkv, int H, int D, int key_valid_len, int masked);
+
+/* What a query sees.  A sequence is divided into frames of `frame` tokens (1: the
+ * tokens themselves).  The query at position p, in frame f = floor(p / frame), sees
+ * the keys j of its sequence with
+ *     j < (f + 1 + right) * frame   and   (j >= (f - left) * frame  or  j < sinks):
+ * its own frame, `left` frames before it, `right` frames after it, and, of the past,
+ * the first `sinks` tokens always.  left < 0: everything before; right < 0:
+ * everything after.  right = 0, frame = 1 is the causal mask, right = 0 with a
+ * frame the block-causal one of a video model.
+ * frame 1 to 2^30, sinks >= 0. */
+typedef struct { int left; int right; int sinks; int frame; } dit_window_t;
+
+/*
+ * dit_attn_fwd_window -- dit_attn_fwd with a window and shared K/V heads: query i
+ * is at position q_offset + i, key j at position j, keys j >= key_valid_len are
+ * not there; query head h reads K/V head h / (H / Hkv).
+ *
+ * q, out    bf16 / out_dtype [B, Nq, H, D], k, v bf16 [B, Nkv, Hkv, D], strides as
+ *           dit_attn_fwd's (rows of out distinct); lse fp32 [B, H, Nq].  D 64 or 128;
+ *           Hkv divides H, H / Hkv at most 128.
+ * q_offset  any sign; |q_offset| + Nq and Nkv at most 2^29, else DIT_ERR_UNSUPPORTED.
+ * A row that sees no key gets O = 0 and LSE = -inf.  Keys that no query of a 256-row
+ * block sees may hold anything, NaN included; V must be finite at the others (a
+ * hidden key's V is multiplied by zero).
+ * workspace device memory of dit_attn_fwd_window_workspace_bytes, 16-byte aligned
+ *           (NULL when that is 0): few rows are cut into key ranges, whose partials
+ *           are joined in a fixed order.  A repeated call gives the same bits.
+ */
+dit_status_t dit_attn_fwd_window(const void *q, const void *k, const void *v, const dit_attn_strides_t *strides,
+                                 int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len,
+                                 const dit_window_t *window, int q_offset, float scale,
+                                 void *out, dit_dtype_t out_dtype, float *lse,
+                                 void *workspace, size_t workspace_bytes, dit_stream_t stream);
+
+/* Workspace bytes of dit_attn_fwd_window on the current device.  Host only. */
+size_t dit_attn_fwd_window_workspace_bytes(int B, int Nq, int H, int Hkv, int D, int key_valid_len,
+                                           const dit_window_t *window, int q_offset);
+
+/*
+ * dit_attn_bwd_window -- the gradients of dit_attn_fwd_window: dit_attn_bwd with its
+ * window, q_offset and shared heads.  dk, dv [B, Nkv, Hkv, D] are sums over the
+ * H / Hkv query heads of a group.
+ *
+ * Tensors, strides, workspace (of dit_attn_bwd_window_workspace_bytes), overlaps and
+ * arithmetic as dit_attn_bwd; sizes as dit_attn_fwd_window.
+ */
+dit_status_t dit_attn_bwd_window(const void *q, const void *k, const void *v,
+                                 const void *out, dit_dtype_t out_dtype, const float *lse,
+                                 const void *dout, const float *dlse,
+                                 const dit_attn_bwd_strides_t *strides,
+                                 int B, int Nq, int Nkv, int H, int Hkv, int D,
+                                 int key_valid_len, const dit_window_t *window, int q_offset, float scale,
+                                 void *dq, void *dk, void *dv, dit_dtype_t grad_dtype,
+                                 void *workspace, size_t workspace_bytes, dit_stream_t stream);
+
+/* Workspace bytes of dit_attn_bwd_window on the current device.  Host only. */
+size_t dit_attn_bwd_window_workspace_bytes(int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len,
+                                           const dit_window_t *window, int q_offset);
+
+/* A paged K/V cache: `pages` pages of `page_size` tokens, and which page of it holds
+ * which tokens of each sequence.
+ *
+ * k, v      bf16, element (page, token of the page, head, d) at page*s.b + token*s.n +
+ *           head*s.h + d (s.d = 1); strides positive multiples of 8, bases 16-byte
+ *           aligned.  Two tensors, or views of one allocation.
+ * page_size a multiple of 8.
+ * table     int32 device array, element (b, i) at b*table_stride + i: the page of
+ *           positions [i*page_size, (i+1)*page_size) of sequence b, i < table_width.
+ *           Several sequences may share pages.  An index outside [0, pages) holds
+ *           no page (an evicted one): its keys are not there.
+ * kv_lens   int32 device array [B]: tokens of each sequence, the new ones included;
+ *           negative counts as 0, positions from table_width * page_size on hold no
+ *           keys. */
+typedef struct {
+    void *k, *v;
+    dit_strides4_t k_strides, v_strides;
+    int pages, page_size;
+    const int32_t *table;
+    int64_t table_stride;
+    int table_width;
+    const int32_t *kv_lens;
+} dit_paged_cache_t;
+
+/*
+ * dit_paged_append -- K and V of new tokens into the cache: token t < new_lens[b] of
+ * sequence b goes to position kv_lens[b] - new_lens[b] + t.
+ *
+ * k, v      bf16, element (b, t, h, d) through their strides (d contiguous; 0
+ *           broadcasts), [B, T, Hkv, D]; D a multiple of 8 up to 1,024.  16 bytes are
+ *           moved at a time where pointers and strides allow.
+ * new_lens  int32 device array [B], or NULL: T each; taken within [0, T].
+ * Tokens without a page (a negative position, one past the table, an index outside
+ * the cache) are dropped; everything else in the cache is left as it was.  Two new
+ * tokens at one place of the cache (a page that two sequences share, appended to by
+ * both) leave either there.
+ */
+dit_status_t dit_paged_append(const void *k, const dit_strides4_t *k_strides, const void *v, const dit_strides4_t *v_strides,
+                              const dit_paged_cache_t *cache, const int32_t *new_lens,
+                              int B, int T, int Hkv, int D, dit_stream_t stream);
+
+/*
+ * dit_attn_fwd_paged -- dit_attn_fwd_window over a cache: row t < q_lens[b] of sequence
+ * b is the query at position kv_lens[b] - q_lens[b] + t.  The new tokens' K and V have
+ * been appended.
+ *
+ * q, out, lse  [B, T, H, D] and [B, H, T] as there; q_lens int32 device array [B], or
+ *           NULL: T each; taken within [0, T].  Rows t >= q_lens[b] of out and lse are
+ *           left as they were.  T at most 2^29.
+ * D 64 or 128; Hkv divides H, H / Hkv at most 128.
+ * Keys that no query of a 256-row block sees (stale rows of a page, evicted tokens)
+ * may hold anything.
+ * workspace device memory of dit_attn_fwd_paged_workspace_bytes, 16-byte aligned.
+ * Lengths are read on the device only.  A repeated call gives the same bits.
+ */
+dit_status_t dit_attn_fwd_paged(const void *q, const dit_strides4_t *q_strides, const dit_paged_cache_t *cache,
+                                const int32_t *q_lens, int B, int T, int H, int Hkv, int D,
+                                const dit_window_t *window, float scale,
+                                void *out, dit_dtype_t out_dtype, const dit_strides4_t *out_strides, float *lse,
+                                void *workspace, size_t workspace_bytes, dit_stream_t stream);
+
+/* Workspace bytes of dit_attn_fwd_paged on the current device.  Host only. */
+size_t dit_attn_fwd_paged_workspace_bytes(int B, int T, int H, int Hkv, int D, int page_size, int table_width,
+                                          const dit_window_t *window);
 
 /*
  * dit_layer_norm_fwd -- y = (x - mean) * rstd * weight + bias over the C
