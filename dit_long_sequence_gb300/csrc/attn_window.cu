@@ -337,49 +337,89 @@ __device__ __forceinline__ void multiply(const Cta<D>& s, const WindowArgs& a) {
 }
 
 // ------------------------------------------------------------ softmax warps (0-7)
+// This thread's query row of an item.  Worked out where it is used, not held: the
+// softmax loop's scores leave few registers.
+struct Row {
+    int tile_row;               // of the item's 256
+    int head, q_at;             // head of the group, token of the sequence
+    bool mine;
+    __device__ __forceinline__ Row(const WindowArgs& a, const Item& it) {
+        int tid;
+        asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+        tile_row = tid;
+        uint32_t g;
+        const int token = static_cast<int>(a.div_group.divmod(static_cast<uint32_t>(tid % kT), g));
+        head = static_cast<int>(g);
+        q_at = it.first + tid / kT * a.tokens + token;
+        mine = token < a.tokens && q_at < it.tokens;
+    }
+};
+// Which chunks of the next tile have a page, asked for a tile ahead.
+template <bool PAGED>
+struct PagedRow {
+    __device__ PagedRow(const WindowArgs&, int) {}
+    __device__ __forceinline__ void ask(const WindowArgs&, int, bool) {}
+    __device__ __forceinline__ uint32_t there(const WindowArgs&, int) const { return ~0u; }
+};
+template <>
+struct PagedRow<true> {
+    const int32_t* row;
+    int kv_len, entry;
+    __device__ PagedRow(const WindowArgs& a, int id) : entry(-1) {
+        const Item it = decode<true>(a, id);
+        row = a.table + it.b * a.table_sb;
+        kv_len = it.kv_len;
+    }
+    __device__ __forceinline__ void ask(const WindowArgs& a, int tile, bool any) {
+        if (any) entry = page_entry(a, row, tile, kv_len);
+    }
+    __device__ __forceinline__ uint32_t there(const WindowArgs& a, int tile) const { return pages_there(a, entry, tile, kv_len); }
+};
 template <int D, bool PAGED>
 __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
     using C = Cfg<D>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const int t = warp >> 2;    // query tile
     const int wq = warp & 3;    // TMEM lane quadrant
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = s.tmem + lane_off + t * 128, tO = s.tmem + lane_off + 256 + t * D;
-    const int r = wq * 32 + lane;                       // this thread's row of the tile
-    uint32_t g;                                         // its query head of the group
-    const int token = static_cast<int>(a.div_group.divmod(static_cast<uint32_t>(r), g));
     int I = 0, J = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
         const int id = take(s, a, n, ROLE_SOFTMAX);
         if (id >= a.n_items) break;
-        const Item it = decode<PAGED>(a, id);
-        const int q_at = it.first + t * a.tokens + token;                   // this row's token
-        const bool mine = token < a.tokens && q_at < it.tokens;
-        // rows that are not there see everything, so that they mask no tile
-        int lo = 0, hi = kNoBound, sinks = 0;
-        if (mine) {
-            const Span sp = span_of(a.win, it.pos + q_at, it.kv_len);
-            lo = sp.lo;
-            hi = sp.hi;
-            sinks = a.win.sinks;
-        }
-        const int32_t* const row = PAGED ? a.table + it.b * a.table_sb : nullptr;
-        int entry = PAGED && it.begin < it.end ? page_entry(a, row, it.tiles.at(it.begin), it.kv_len) : 0;
-        float m = -INFINITY, l = 0.f;
-        for (int i = it.begin; i < it.end; ++i, ++J) {
-            const int tile = it.tiles.at(i), k0 = tile * kT;
-            uint32_t there = ~0u;
-            if constexpr (PAGED) {
-                there = pages_there(a, entry, tile, it.kv_len);
-                if (i + 1 < it.end) entry = page_entry(a, row, it.tiles.at(i + 1), it.kv_len);
+        // Held across the tiles: the row's bounds and the tiles' order.
+        int lo = 0, hi = kNoBound, i, end, ns, shift;
+        bool any_tile;
+        {
+            const Item it = decode<PAGED>(a, id);
+            const Row row(a, it);
+            // rows that are not there see everything, so that they mask no tile
+            if (row.mine) {
+                const Span sp = span_of(a.win, it.pos + row.q_at, it.kv_len);
+                lo = sp.lo;
+                hi = sp.hi;
             }
-            const bool masked = !__all_sync(0xffffffffu, sees_all(lo, hi, sinks, k0)) || there != ~0u;
+            i = it.begin;
+            end = it.end;
+            ns = it.tiles.ns;
+            shift = it.tiles.w0 - ns;
+            any_tile = i < end;
+        }
+        PagedRow<PAGED> pages(a, id);
+        pages.ask(a, i < ns ? i : i + shift, any_tile);
+        float m = -INFINITY, l = 0.f;
+        for (bool first = true; i < end; ++J, first = false) {
+            const int tile = i < ns ? i : i + shift, k0 = tile * kT;
+            ++i;
+            const uint32_t there = pages.there(a, tile);
+            pages.ask(a, i < ns ? i : i + shift, i < end);
+            const bool masked = !__all_sync(0xffffffffu, sees_all(lo, hi, a.win.sinks, k0)) || there != ~0u;
             uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
             if (masked) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    words[w] = seen_word(lo, hi, sinks, k0 + 32 * w);
+                    words[w] = seen_word(lo, hi, a.win.sinks, k0 + 32 * w);
                     if (PAGED && there != ~0u) words[w] &= paged_word(there, a.chunk, w);
                 }
             }
@@ -387,13 +427,12 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            soften_tile<D>(tS, tO, a.scale_log2, i == it.begin, masked, words, m, l);
+            soften_tile<D>(tS, tO, a.scale_log2, first, masked, words, m, l);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(s.bar(C::kPFull + t));
         }
         if (!ok) break;
-        const bool any_tile = it.begin < it.end;
         if (any_tile) {
             ok = wait_bounded(s.bar(C::kOFinal + t), I & 1, s.wd, ROLE_SOFTMAX, SITE_O_FINAL);
             ok = __all_sync(0xffffffffu, ok);
@@ -403,13 +442,17 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
         }
         // The result, from this thread's row: whole 32-byte sectors.  (PV of the
         // next item's first tile overwrites O only after this thread's next P.)
+        int again = id;         // decoded anew: only its number is held across the tiles
+        asm volatile("" : "+r"(again));
+        const Item it = decode<PAGED>(a, again);
+        const Row row(a, it);
         const bool any_key = l > 0.f || l != l;
         const float inv = any_key ? 1.f / l : 0.f;
         const float lse = any_key ? (m + log2f(l)) * kWinLn2 : -INFINITY;
-        const int h = it.hk * a.group + static_cast<int>(g);
-        const int64_t off = it.b * a.o_sb + static_cast<int64_t>(q_at) * a.o_sn + h * a.o_sh;
-        const int64_t part = static_cast<int64_t>(it.id) * (2 * kT) + t * kT + r;
-        const bool stored = mine && in_bounds(a.f > 1 || (off >= 0 && off + D <= a.dbg_o_elems), a.status, ROLE_SOFTMAX, BND_OUT);
+        const int h = it.hk * a.group + row.head;
+        const int64_t off = it.b * a.o_sb + static_cast<int64_t>(row.q_at) * a.o_sn + h * a.o_sh;
+        const int64_t part = static_cast<int64_t>(it.id) * (2 * kT) + row.tile_row;
+        const bool stored = row.mine && in_bounds(a.f > 1 || (off >= 0 && off + D <= a.dbg_o_elems), a.status, ROLE_SOFTMAX, BND_OUT);
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
@@ -418,13 +461,13 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
                 tmem_ld_wait_dep(o);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = any_key ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+            for (int k = 0; k < 32; ++k) o[k] = any_key ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
             if (stored) store_32(a, a.f > 1 ? a.ws_o + part * D + cc * 32 : nullptr, off + cc * 32, o);
             __syncwarp();
         }
         if (stored) {
             if (a.f > 1) a.ws_lse[part] = lse;
-            else a.lse[(static_cast<int64_t>(it.b) * a.H + h) * a.T + q_at] = lse;
+            else a.lse[(static_cast<int64_t>(it.b) * a.H + h) * a.T + row.q_at] = lse;
         }
         tc_fence_before();
     }

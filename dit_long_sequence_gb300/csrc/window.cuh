@@ -87,6 +87,21 @@ __device__ __forceinline__ void clear_unseen(uint8_t* v, const KeyTiles& t, int 
 
 // ------------------------------------------------------------------ softmax
 
+// 32 lanes x 8 columns (one row a thread), there and back.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Max over 64 scores: eight 3-input max chains, then a small tree.
 __device__ __forceinline__ float max_of_64(const float* v) {
     float t[8];
@@ -171,17 +186,18 @@ __device__ __forceinline__ void soften_tile(uint32_t tS, uint32_t tO, float sl2,
         const float m_new = need ? fmaxf(mt, m) : m;
         // (when no row's offset moves, O and P stand as they are)
         if (__any_sync(0xffffffffu, m_new != m)) {
+            // (8 columns at a time: with 32 the loads' registers beside the scores spill in
+            // every tile, 1,954 us against 1,607 of the LTX-2-shaped frames without this path)
             tmem_st_wait();
             const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
             l *= alpha;
+#pragma unroll 1
+            for (int cc = 0; cc < D / 8; ++cc) {
+                uint32_t o[8];
+                tmem_ld8(tO + cc * 8, o);
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                tmem_ld32(tO + cc * 32, o);
-                tmem_ld_wait_dep(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(tO + cc * 32, o);
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st8(tO + cc * 8, o);
             }
             m = m_new;
             la = exp_to_p(s, tS, sl2, off(m));
