@@ -101,15 +101,16 @@ int pieces_of(int B, int T, int H, int Hkv, const dit_window_t& window, int offs
 // Settles the grid and the partials' place in the workspace.
 dit_status_t set_pieces(WindowArgs& a, int f, int D, void* workspace, size_t workspace_bytes) {
     const int64_t items = items_of(a.B, a.T, a.H, a.Hkv);
+    a.part_rows = part_rows_of(a.T, a.group);
     if (items * f > 0x7ffffff0LL) return DIT_ERR_UNSUPPORTED;
     a.f = f;
     a.div_f = FastDiv(static_cast<uint32_t>(f));
     a.n_items = static_cast<int>(items * f);
     if (f > 1) {
-        if (workspace == nullptr || workspace_bytes < static_cast<size_t>(pieces_bytes(items, f, D))) return DIT_ERR_INVALID_ARG;
+        if (workspace == nullptr || workspace_bytes < static_cast<size_t>(pieces_bytes(items, f, a.part_rows, D))) return DIT_ERR_INVALID_ARG;
         if (!aligned16(workspace)) return DIT_ERR_ALIGNMENT;
         a.ws_o = static_cast<float*>(workspace);
-        a.ws_lse = a.ws_o + items * f * 256 * D;
+        a.ws_lse = a.ws_o + items * f * a.part_rows * D;
     }
     return DIT_OK;
 }
@@ -147,7 +148,8 @@ dit_status_t encode_pages(CUtensorMap* map, const void* base, const dit_strides4
 // Pieces of an item over a cache, whose lengths the host does not know: as if every
 // sequence filled its table row.
 int paged_pieces_of(int B, int T, int H, int Hkv, const dit_window_t& window, int64_t capacity, int sms) {
-    const int len = static_cast<int>(capacity);
+    const int len = static_cast<int>(capacity), tokens = 128 / (H / Hkv);
+    if (T <= tokens) return plan_pieces_few(items_of(B, T, H, Hkv), mean_key_tiles(make_window(window), T, tokens, len - T, len), sms);
     return pieces_of(B, T, H, Hkv, window, len - T, len, sms);
 }
 
@@ -163,7 +165,7 @@ size_t dit_attn_fwd_window_workspace_bytes(int B, int Nq, int H, int Hkv, int D,
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     const int f = pieces_of(B, Nq, H, Hkv, *window, q_offset, key_valid_len, device_sm_count(dev));
-    return static_cast<size_t>(pieces_bytes(items_of(B, Nq, H, Hkv), f, D));
+    return static_cast<size_t>(pieces_bytes(items_of(B, Nq, H, Hkv), f, part_rows_of(Nq, H / Hkv), D));
 }
 
 dit_status_t dit_attn_fwd_window(const void* q, const void* k, const void* v, const dit_attn_strides_t* strides, int B, int Nq, int Nkv,
@@ -260,7 +262,7 @@ size_t dit_attn_fwd_paged_workspace_bytes(int B, int T, int H, int Hkv, int D, i
     int dev = 0;
     if (capacity > 0x7fffff00LL || cudaGetDevice(&dev) != cudaSuccess) return 0;
     const int f = paged_pieces_of(B, T, H, Hkv, *window, capacity, device_sm_count(dev));
-    return static_cast<size_t>(pieces_bytes(items_of(B, T, H, Hkv), f, D));
+    return static_cast<size_t>(pieces_bytes(items_of(B, T, H, Hkv), f, part_rows_of(T, H / Hkv), D));
 }
 
 dit_status_t dit_attn_fwd_paged(const void* q, const dit_strides4_t* q_strides, const dit_paged_cache_t* cache, const int32_t* q_lens,

@@ -6,7 +6,8 @@
 // over the keys [0, min(sinks, hi_i)) and [lo_i, hi_i) of row i (window_span.h).  K
 // and V are strided tensors, or the pages of a cache (PAGED).
 //
-// A work item is 256 query rows, two 128-row tiles, of one (batch entry, K/V head).
+// A work item is 256 query rows, two 128-row tiles, of one (batch entry, K/V head);
+// where all rows of a sequence fit one tile (ONE: a few new tokens) it is that tile.
 // Rows are (token, query head of the group): heads that share K and V share their
 // tiles too.  The item walks the key tiles that some row of it sees, the sinks'
 // first; a tile that every row of a warp sees whole passes without a mask, others
@@ -27,6 +28,9 @@
 // first products run.  The last blocks of a sequence, which see the most keys of a
 // causal mask, come first.
 //
+// ONE: S of consecutive tiles alternates between the two buffers, Q_1's shared memory
+// goes to the ring (192 KB of K and V on their way), warps 4-7 leave at once.
+//
 // Few items are cut into key ranges (f pieces), whose normalised partials
 // window_merge_kernel joins.
 #include <cuda.h>
@@ -43,10 +47,13 @@ constexpr uint32_t kSoftmaxRegs = 208;
 constexpr uint32_t kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 
-template <int D>
+// ONE: all rows of an item fit one query tile; its Q takes one tile of shared memory
+// and the ring the rest.
+template <int D, bool ONE>
 struct Cfg {
     static constexpr int kTile = kT * D * 2;
-    static constexpr int kStages = D == 128 ? 4 : 8;     // K/V ring slots
+    static constexpr int kQTiles = ONE ? 1 : 2;
+    static constexpr int kStages = (D == 128 ? 6 : 12) - (ONE ? 0 : (D == 128 ? 2 : 4));     // K/V ring slots
     static constexpr int kBlock = kT * 128;              // 128 rows x 64 bf16 (one swizzle column)
     static constexpr int kQueue = 4;                     // items published ahead at most
     // barriers
@@ -56,11 +63,12 @@ struct Cfg {
     static constexpr int kSFull = kKVEmpty + kStages;    // two
     static constexpr int kPFull = kSFull + 2;            // two
     static constexpr int kOFinal = kPFull + 2;           // two
+    static constexpr int kOSettled = kOFinal + 1;        // ONE: every PV
     static constexpr int kDrain = kOFinal + 2;
     static constexpr int kItemFull = kDrain + 1, kItemEmpty = kItemFull + kQueue;
     static constexpr int kClaim = kItemEmpty + kQueue;
     static constexpr int kNumBars = kClaim + 1;
-    static constexpr int kClaimOffset = (2 + kStages) * kTile;           // 16 bytes
+    static constexpr int kClaimOffset = (kQTiles + kStages) * kTile;           // 16 bytes
     static constexpr int kBarOffset = kClaimOffset + 16;
     static constexpr int kItemOffset = kBarOffset + kNumBars * 8;
     static constexpr int kSmemBytes = 1024 /*alignment slack*/ + kItemOffset + kQueue * 4 + 16;
@@ -134,23 +142,23 @@ __device__ __forceinline__ Item decode(const WindowArgs& a, int id) {
 }
 
 // What the roles of a CTA share.
-template <int D>
+template <int D, bool ONE>
 struct Cta {
-    using C = Cfg<D>;
+    using C = Cfg<D, ONE>;
     uint8_t* smem;
     uint32_t base, bars, tmem;
     Watchdog wd, wd_drain;      // wd_drain ignores the abort flag: it waits for work already in flight
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + i * 8; }
     __device__ __forceinline__ uint32_t q(int t) const { return base + t * C::kTile; }
-    __device__ __forceinline__ uint32_t slot_offset(int i) const { return (2 + i % C::kStages) * C::kTile; }
+    __device__ __forceinline__ uint32_t slot_offset(int i) const { return (C::kQTiles + static_cast<uint32_t>(i) % C::kStages) * C::kTile; }
 };
 __device__ __forceinline__ uint32_t turn(int n, int r) { return static_cast<uint32_t>(n / r) & 1u; }
 
 // The CTA's items, in order: the producer publishes them, the other roles' warps
 // take them.  a.n_items is the end.
-template <int D>
-__device__ __forceinline__ bool publish(const Cta<D>& s, int n, int id) {
-    using C = Cfg<D>;
+template <int D, bool ONE>
+__device__ __forceinline__ bool publish(const Cta<D, ONE>& s, int n, int id) {
+    using C = Cfg<D, ONE>;
     const int slot = n % C::kQueue;
     const bool ok = wait_bounded_warp(s.bar(C::kItemEmpty + slot), turn(n, C::kQueue) ^ 1u, s.wd, ROLE_LOAD, SITE_ITEM_EMPTY);
     if (ok && lane_id() == 0) {
@@ -159,9 +167,9 @@ __device__ __forceinline__ bool publish(const Cta<D>& s, int n, int id) {
     }
     return ok;
 }
-template <int D>
-__device__ __forceinline__ int take(const Cta<D>& s, const WindowArgs& a, int n, uint32_t role) {
-    using C = Cfg<D>;
+template <int D, bool ONE>
+__device__ __forceinline__ int take(const Cta<D, ONE>& s, const WindowArgs& a, int n, uint32_t role) {
+    using C = Cfg<D, ONE>;
     const int slot = n % C::kQueue;
     const bool ok = wait_bounded_warp(s.bar(C::kItemFull + slot), turn(n, C::kQueue), s.wd, role, SITE_ITEM_FULL);
     const int id = ok ? *reinterpret_cast<volatile int*>(s.smem + C::kItemOffset + slot * 4) : a.n_items;
@@ -171,10 +179,10 @@ __device__ __forceinline__ int take(const Cta<D>& s, const WindowArgs& a, int n,
 }
 
 // ------------------------------------------------------------ TMA producer (a warp)
-template <int D, bool PAGED>
-__device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+template <int D, bool PAGED, bool ONE>
+__device__ __forceinline__ void produce(const Cta<D, ONE>& s, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                         const WindowArgs& a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, ONE>;
     constexpr int S = C::kStages;
     const bool leader = lane_id() == 0;
     auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded_warp(s.bar(i), parity, s.wd, ROLE_LOAD, site); };
@@ -191,8 +199,8 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_q
             ok = wait(C::kQEmpty, (I & 1) ^ 1u, SITE_Q_EMPTY);
             if (!ok) break;
             if (leader) {
-                mbar_arrive_expect_tx(s.bar(C::kQFull), 2 * a.tokens * a.group * D * 2);
-                for (int t = 0; t < 2; ++t)
+                mbar_arrive_expect_tx(s.bar(C::kQFull), C::kQTiles * a.tokens * a.group * D * 2);
+                for (int t = 0; t < C::kQTiles; ++t)
                     for (int c = 0; c < D / 64; ++c)
                         tma_load_5d(s.q(t) + c * C::kBlock, &tm_q, s.bar(C::kQFull), c * 64, 0, it.first + t * a.tokens, it.hk, it.b);
             }
@@ -251,34 +259,73 @@ __device__ __forceinline__ void produce(const Cta<D>& s, const CUtensorMap& tm_q
 }
 
 // ------------------------------------------------------------ MMA issuer (a warp)
-template <int D, bool PAGED>
-__device__ __forceinline__ void multiply(const Cta<D>& s, const WindowArgs& a) {
-    using C = Cfg<D>;
+template <int D, bool PAGED, bool ONE>
+__device__ __forceinline__ void multiply(const Cta<D, ONE>& s, const WindowArgs& a) {
+    using C = Cfg<D, ONE>;
     constexpr int S = C::kStages;
     constexpr uint32_t kIdescQK = idesc_bf16_f32(kT, kT, false);
     constexpr uint32_t kIdescPV = idesc_bf16_f32(kT, D, true);
     auto wait = [&](int i, uint32_t parity, uint32_t site) { return wait_bounded_warp(s.bar(i), parity, s.wd, ROLE_MMA, site); };
     auto commit = [&](int i) { umma_commit_warp(s.bar(i)); };
-    // S_t = Q_t K^T: both K-major, K = D channels
-    auto issue_qk = [&](int t, uint32_t k_addr) {
+    // S = Q_t K^T in buffer b: both K-major, K = D channels
+    auto issue_qk = [&](int t, int b, uint32_t k_addr) {
         const uint64_t dq = sdesc_sw128(s.q(t), 16, 1024), dk = sdesc_sw128(k_addr, 16, 1024);
         static_for<D / 16>([&](auto kk) {
             constexpr uint32_t off = (kk.value >> 2) * C::kBlock + (kk.value & 3) * 32;
-            umma_ss_warp<off>(s.tmem + t * 128, dq, dk, kIdescQK, kk.value > 0 ? 1u : 0u);
+            umma_ss_warp<off>(s.tmem + b * 128, dq, dk, kIdescQK, kk.value > 0 ? 1u : 0u);
         });
     };
-    // O_t (+)= P_t V: P from TMEM, V MN-major, K = 128 keys
-    auto issue_pv = [&](int t, uint32_t v_addr, bool accumulate) {
+    // O_t (+)= P V: P from TMEM, V MN-major, K = 128 keys
+    auto issue_pv = [&](int t, int b, uint32_t v_addr, bool accumulate) {
         const uint64_t dv = sdesc_sw128(v_addr, C::kBlock, 1024);
         static_for<kT / 16>([&](auto kk) {
-            umma_ts_warp<kk.value * 16 * 128>(s.tmem + 256 + t * D, s.tmem + t * 128 + kk.value * 8, dv, kIdescPV,
+            umma_ts_warp<kk.value * 16 * 128>(s.tmem + 256 + t * D, s.tmem + b * 128 + kk.value * 8, dv, kIdescPV,
                                               (accumulate || kk.value > 0) ? 1u : 0u);
         });
     };
     int I = 0, R = 0;           // items with tiles, ring slots taken
     int J = 0;                  // key tiles
     bool ok = true;
-    for (int n = 0; ok; ++n) {
+    if constexpr (ONE) {
+        // One query tile: S takes the two buffers in turns, so that the next tile's
+        // scores are there when the softmax warps are done with this one's.
+        for (int n = 0; ok; ++n) {
+            const int id = take(s, a, n, ROLE_MMA);
+            if (id >= a.n_items) break;
+            const Item it = decode<PAGED>(a, id);
+            if (it.begin >= it.end) continue;
+            ok = wait(C::kQFull, I & 1, SITE_Q_FULL);
+            auto next_s = [&](int slot, int j) {
+                ok = ok && wait(C::kKVFull + slot % S, turn(slot, S), SITE_KV_FULL);
+                if (!ok) return;
+                tc_fence_after();
+                issue_qk(0, j & 1, s.base + s.slot_offset(slot));
+                commit(C::kSFull + (j & 1));
+                commit(C::kKVEmpty + slot % S);
+            };
+            next_s(R, J);
+            if (!ok) break;
+            if (it.begin + 1 == it.end) commit(C::kQEmpty);
+            for (int i = it.begin; i < it.end; ++i, ++J, R += 2) {
+                const bool more = i + 1 < it.end;
+                if (more) next_s(R + 2, J + 1);
+                if (ok && i + 2 == it.end) commit(C::kQEmpty);
+                const int rv = R + 1;
+                ok = ok && wait(C::kKVFull + rv % S, turn(rv, S), SITE_KV_FULL);
+                if (!ok) break;
+                clear_unseen<D>(s.smem + s.slot_offset(rv), it.tiles, it.tiles.at(i) * kT);
+                ok = wait(C::kPFull + (J & 1), turn(J, 2), SITE_P_FULL);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(0, J & 1, s.base + s.slot_offset(rv), i > it.begin);
+                commit(C::kKVEmpty + rv % S);
+                commit(C::kOSettled);
+                if (!more) commit(C::kOFinal + 0);
+            }
+            ++I;
+        }
+    }
+    for (int n = 0; !ONE && ok; ++n) {
         const int id = take(s, a, n, ROLE_MMA);
         if (id >= a.n_items) break;
         const Item it = decode<PAGED>(a, id);
@@ -286,9 +333,9 @@ __device__ __forceinline__ void multiply(const Cta<D>& s, const WindowArgs& a) {
         ok = wait(C::kQFull, I & 1, SITE_Q_FULL) && wait(C::kKVFull + R % S, turn(R, S), SITE_KV_FULL);
         if (!ok) break;
         tc_fence_after();
-        issue_qk(0, s.base + s.slot_offset(R));
+        issue_qk(0, 0, s.base + s.slot_offset(R));
         commit(C::kSFull + 0);
-        issue_qk(1, s.base + s.slot_offset(R));
+        issue_qk(1, 1, s.base + s.slot_offset(R));
         commit(C::kSFull + 1);
         commit(C::kKVEmpty + R % S);
         if (it.begin + 1 == it.end) commit(C::kQEmpty);
@@ -303,12 +350,12 @@ __device__ __forceinline__ void multiply(const Cta<D>& s, const WindowArgs& a) {
             ok = wait(C::kPFull + 0, J & 1, SITE_P_FULL);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(0, v_addr, i > it.begin);
+            issue_pv(0, 0, v_addr, i > it.begin);
             if (more) {
                 ok = wait(C::kKVFull + rk % S, turn(rk, S), SITE_KV_FULL);
                 if (!ok) break;
                 tc_fence_after();
-                issue_qk(0, k_addr);
+                issue_qk(0, 0, k_addr);
                 commit(C::kSFull + 0);
             } else {
                 commit(C::kOFinal + 0);
@@ -316,10 +363,10 @@ __device__ __forceinline__ void multiply(const Cta<D>& s, const WindowArgs& a) {
             ok = wait(C::kPFull + 1, J & 1, SITE_P_FULL);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(1, v_addr, i > it.begin);
+            issue_pv(1, 1, v_addr, i > it.begin);
             commit(C::kKVEmpty + rv % S);
             if (more) {
-                issue_qk(1, k_addr);
+                issue_qk(1, 1, k_addr);
                 commit(C::kSFull + 1);
                 commit(C::kKVEmpty + rk % S);
                 if (i + 2 == it.end) commit(C::kQEmpty);
@@ -375,14 +422,15 @@ struct PagedRow<true> {
     }
     __device__ __forceinline__ uint32_t there(const WindowArgs& a, int tile) const { return pages_there(a, entry, tile, kv_len); }
 };
-template <int D, bool PAGED>
-__device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
-    using C = Cfg<D>;
+template <int D, bool PAGED, bool ONE>
+__device__ __forceinline__ void soften(const Cta<D, ONE>& s, const WindowArgs& a) {
+    using C = Cfg<D, ONE>;
     const int warp = threadIdx.x >> 5;
     const int t = warp >> 2;    // query tile
     const int wq = warp & 3;    // TMEM lane quadrant
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = s.tmem + lane_off + t * 128, tO = s.tmem + lane_off + 256 + t * D;
+    if (ONE && t > 0) return;   // (nothing of theirs is waited for)
     int I = 0, J = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -390,7 +438,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
         if (id >= a.n_items) break;
         // Held across the tiles: the row's bounds and the tiles' order.
         int lo = 0, hi = kNoBound, i, end, ns, shift;
-        bool any_tile;
+        bool any_tile, any_row = true;
         {
             const Item it = decode<PAGED>(a, id);
             const Row row(a, it);
@@ -400,6 +448,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
                 lo = sp.lo;
                 hi = sp.hi;
             }
+            if (ONE) any_row = __any_sync(0xffffffffu, row.mine);
             i = it.begin;
             end = it.end;
             ns = it.tiles.ns;
@@ -423,14 +472,20 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
                     if (PAGED && there != ~0u) words[w] &= paged_word(there, a.chunk, w);
                 }
             }
-            ok = wait_bounded(s.bar(C::kSFull + t), J & 1, s.wd, ROLE_SOFTMAX, SITE_S_FULL);
+            const int b = ONE ? J & 1 : t;      // S's buffer, and its barriers
+            ok = wait_bounded(s.bar(C::kSFull + b), ONE ? turn(J, 2) : J & 1, s.wd, ROLE_SOFTMAX, SITE_S_FULL);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            soften_tile<D>(tS, tO, a.scale_log2, first, masked, words, m, l);
-            tmem_st_wait();
+            if (any_row) {      // (a warp without a row leaves its lanes' P as they are: no other row reads them)
+                // (two tiles: S(j) was committed behind PV(j - 1); one: its own barrier)
+                soften_tile<D>(ONE ? tS + b * 128 : tS, tO, a.scale_log2, first, masked, words, m, l, [&]() {
+                    if (ONE && wait_bounded_warp(s.bar(C::kOSettled), (J - 1) & 1, s.wd, ROLE_SOFTMAX, SITE_O_SETTLED)) tc_fence_after();
+                });
+                tmem_st_wait();
+            }
             tc_fence_before();
-            mbar_arrive(s.bar(C::kPFull + t));
+            mbar_arrive(s.bar(C::kPFull + b));
         }
         if (!ok) break;
         if (any_tile) {
@@ -451,7 +506,7 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
         const float lse = any_key ? (m + log2f(l)) * kWinLn2 : -INFINITY;
         const int h = it.hk * a.group + row.head;
         const int64_t off = it.b * a.o_sb + static_cast<int64_t>(row.q_at) * a.o_sn + h * a.o_sh;
-        const int64_t part = static_cast<int64_t>(it.id) * (2 * kT) + row.tile_row;
+        const int64_t part = static_cast<int64_t>(it.id) * a.part_rows + row.tile_row;
         const bool stored = row.mine && in_bounds(a.f > 1 || (off >= 0 && off + D <= a.dbg_o_elems), a.status, ROLE_SOFTMAX, BND_OUT);
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
@@ -473,13 +528,13 @@ __device__ __forceinline__ void soften(const Cta<D>& s, const WindowArgs& a) {
     }
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowArgs a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, ONE>;
     extern __shared__ uint8_t smem_raw[];
-    Cta<D> s;
+    Cta<D, ONE> s;
     s.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     s.base = smem_u32(s.smem);
     s.bars = s.base + C::kBarOffset;
@@ -494,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kNumBars; ++i) {
             const bool all = i == C::kPFull || i == C::kPFull + 1;
             const bool takers = i >= C::kItemEmpty && i < C::kItemEmpty + C::kQueue;     // the MMA and softmax warps
-            mbar_init(s.bar(i), all ? 128 : (takers ? 9 : 1));
+            mbar_init(s.bar(i), all ? 128 : (takers ? (ONE ? 5 : 9) : 1));
         }
         *abort_flag = 0;
         *never_flag = 0;
@@ -504,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Rows of a query tile past its last whole token hold nothing that is copied:
     // zeros, so that they make no NaN and no rescale.
     const int spare = kT - a.tokens * a.group;
-    for (int u = threadIdx.x; u < 2 * (D / 64) * spare * 8; u += kThreads) {
+    for (int u = threadIdx.x; u < C::kQTiles * (D / 64) * spare * 8; u += kThreads) {
         const int block = u / (spare * 8), rest = u % (spare * 8);
         *reinterpret_cast<uint4*>(s.smem + block * C::kBlock + (kT - spare + rest / 8) * 128 + (rest & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -521,19 +576,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) {
         regs_decrease<kOtherRegs>();
         if (warp == 8) {
-            multiply<D, PAGED>(s, a);
+            multiply<D, PAGED, ONE>(s, a);
         } else if (warp == 9) {
             if (lane_id() == 0 && (PAGED ? a.capacity : a.kv_len) > 0) {      // (no keys, no maps)
                 tma_prefetch_desc(&tm_q);
                 tma_prefetch_desc(&tm_k);
                 tma_prefetch_desc(&tm_v);
             }
-            produce<D, PAGED>(s, tm_q, tm_k, tm_v, a);
+            produce<D, PAGED, ONE>(s, tm_q, tm_k, tm_v, a);
         }
         __syncwarp();
     } else {
         regs_increase<kSoftmaxRegs>();
-        soften<D, PAGED>(s, a);
+        soften<D, PAGED, ONE>(s, a);
     }
 
     tc_fence_before();
@@ -553,7 +608,7 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant
     after_previous();
     const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
     const int c4 = static_cast<int>(threadIdx.x % LPR);
-    const int item = static_cast<int>(unit / (2 * kT)), rr = static_cast<int>(unit % (2 * kT));
+    const int item = static_cast<int>(unit / a.part_rows), rr = static_cast<int>(unit % a.part_rows);
     if (item >= a.n_items / a.f) return;
     uint32_t blk, hk, g;
     const int t = rr / kT;
@@ -562,18 +617,18 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant
     const int q_at = (a.n_blk - 1 - static_cast<int>(blk)) * 2 * a.tokens + t * a.tokens + token;
     const int tokens = PAGED && a.q_lens != nullptr ? min(__ldg(a.q_lens + b), a.T) : a.T;
     if (token >= a.tokens || q_at >= tokens) return;
-    const int64_t p0 = static_cast<int64_t>(item) * a.f * (2 * kT) + rr;
+    const int64_t p0 = static_cast<int64_t>(item) * a.f * a.part_rows + rr;
     float mx = -INFINITY;
-    for (int p = 0; p < a.f; ++p) mx = fmaxf(mx, __ldg(a.ws_lse + p0 + p * (2 * kT)));
+    for (int p = 0; p < a.f; ++p) mx = fmaxf(mx, __ldg(a.ws_lse + p0 + static_cast<int64_t>(p) * a.part_rows));
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     bool bad = false;           // (a NaN must stay one)
     for (int p = 0; p < a.f; ++p) {
-        const float lp = __ldg(a.ws_lse + p0 + p * (2 * kT));
+        const float lp = __ldg(a.ws_lse + p0 + static_cast<int64_t>(p) * a.part_rows);
         bad = bad || lp != lp;
         if (lp == -INFINITY) continue;
         const float w = expf(lp - mx);
-        const float4 o = __ldg(reinterpret_cast<const float4*>(a.ws_o + (p0 + p * (2 * kT)) * D) + c4);
+        const float4 o = __ldg(reinterpret_cast<const float4*>(a.ws_o + (p0 + static_cast<int64_t>(p) * a.part_rows) * D) + c4);
         sum += w;
         acc.x = fmaf(w, o.x, acc.x);
         acc.y = fmaf(w, o.y, acc.y);
@@ -593,14 +648,15 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant
         a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + q_at] = bad ? NAN : (sum > 0.f ? mx + logf(sum) : -INFINITY);
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool ONE>
 cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WindowArgs& a, cudaStream_t s) {
-    auto kern = attn_window_kernel<D, PAGED>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+    auto kern = attn_window_kernel<D, PAGED, ONE>;
+    constexpr int kSmem = Cfg<D, ONE>::kSmemBytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(a.n_items), kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv, a);
+    kern<<<static_cast<unsigned>(a.n_items), kThreads, kSmem, s>>>(tq, tk, tv, a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.f == 1) return e;
-    const int64_t threads = static_cast<int64_t>(a.n_items / a.f) * (2 * kT) * (D / 4);
+    const int64_t threads = static_cast<int64_t>(a.n_items / a.f) * a.part_rows * (D / 4);
     return launch_behind(window_merge_kernel<D, PAGED>, static_cast<unsigned>((threads + 255) / 256), 256, 0, s, a);
 }
 
@@ -608,8 +664,13 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 
 cudaError_t launch_attn_window(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WindowArgs& a,
                                int D, bool paged, cudaStream_t s) {
-    if (D == 128) return paged ? launch_impl<128, true>(tq, tk, tv, a, s) : launch_impl<128, false>(tq, tk, tv, a, s);
-    return paged ? launch_impl<64, true>(tq, tk, tv, a, s) : launch_impl<64, false>(tq, tk, tv, a, s);
+    const bool one = one_tile(a);
+    if (D == 128) {
+        if (paged) return one ? launch_impl<128, true, true>(tq, tk, tv, a, s) : launch_impl<128, true, false>(tq, tk, tv, a, s);
+        return one ? launch_impl<128, false, true>(tq, tk, tv, a, s) : launch_impl<128, false, false>(tq, tk, tv, a, s);
+    }
+    if (paged) return one ? launch_impl<64, true, true>(tq, tk, tv, a, s) : launch_impl<64, true, false>(tq, tk, tv, a, s);
+    return one ? launch_impl<64, false, true>(tq, tk, tv, a, s) : launch_impl<64, false, false>(tq, tk, tv, a, s);
 }
 
 }  // namespace dit

@@ -10,7 +10,8 @@
 namespace dit {
 
 enum WindowSite : uint32_t {
-    SITE_Q_EMPTY = 31, SITE_ITEM_FULL = 32, SITE_ITEM_EMPTY = 33, SITE_CLAIM = 34
+    SITE_Q_EMPTY = 31, SITE_ITEM_FULL = 32, SITE_ITEM_EMPTY = 33, SITE_CLAIM = 34,
+    SITE_O_SETTLED = 35
 };
 constexpr int kWinTile = 128;      // rows of a query tile, keys of a key tile
 constexpr float kWinLn2 = 0.6931471805599453f;
@@ -142,9 +143,10 @@ __device__ __forceinline__ float exp_to_p(const float* v, uint32_t tP, float sl2
 // are then scaled by 2^(m_old - m_new)): every P is at most 2^39, which bf16 and
 // the fp32 sums carry with the precision they have at 1.  `first`: the item's
 // first tile, O holds nothing yet.  `masked` (warp-uniform): apply the words.
-template <int D>
+// settled() returns when the products before this tile's P are done with O.
+template <int D, typename F>
 __device__ __forceinline__ void soften_tile(uint32_t tS, uint32_t tO, float sl2, bool first, bool masked,
-                                            const uint32_t (&words)[4], float& m, float& l) {
+                                            const uint32_t (&words)[4], float& m, float& l, F&& settled) {
     uint32_t sr[4][32];
     tmem_ld32(tS, sr[0]);
     tmem_ld32(tS + 32, sr[1]);
@@ -189,6 +191,7 @@ __device__ __forceinline__ void soften_tile(uint32_t tS, uint32_t tO, float sl2,
             // (8 columns at a time: with 32 the loads' registers beside the scores spill in
             // every tile, 1,954 us against 1,607 of the LTX-2-shaped frames without this path)
             tmem_st_wait();
+            settled();
             const float alpha = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
             l *= alpha;
 #pragma unroll 1

@@ -13,7 +13,7 @@
 
 namespace dit {
 
-constexpr int kMaxPiecesFwd = 16;   // key ranges an item is cut into at most
+constexpr int kMaxPiecesFwd = 64;   // key ranges an item is cut into at most
 
 // Attention over a window.  A work item is a block of query rows of one batch
 // entry and one K/V head; its rows are (token, query head of the group), the
@@ -30,8 +30,9 @@ struct WindowArgs {
     float* lse;                 // [B, H, T]
     // Grid: items (b, K/V head, block of two tiles), blocks fastest and the last
     // first, each in f key ranges whose partials (O normalised, LSE) go to ws_o
-    // [item][f][256][D] and ws_lse [item][f][256].
+    // [item][f][part_rows][D] and ws_lse [item][f][part_rows].
     int n_blk, f, n_items;      // n_items: pieces counted
+    int part_rows;              // 256, or the rows of the one tile
     FastDiv div_f, div_blk, div_hkv, div_group;
     float *ws_o, *ws_lse;
     // Paged: position x of sequence b is row x mod page of page
@@ -45,6 +46,8 @@ struct WindowArgs {
     int64_t dbg_o_elems;        // debug library: O elements reachable through its strides
 };
 
+// All rows of a sequence and K/V head fit one query tile.
+inline bool one_tile(const WindowArgs& a) { return a.T <= a.tokens; }
 cudaError_t launch_attn_window(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WindowArgs& a,
                                int D, bool paged, cudaStream_t s);
 

@@ -47,7 +47,7 @@ inline int plan_pieces(int64_t items, double tiles, int sms) {
     if (items <= 0 || sms <= 0 || items >= 4LL * sms) return 1;
     double best = 0;
     int f_best = 1;
-    for (int f = 1; f <= kMaxPiecesFwd && (f == 1 || tiles / f >= 2); ++f) {
+    for (int f = 1; f <= 16 && (f == 1 || tiles / f >= 2); ++f) {
         const double turns = static_cast<double>((items * f + sms - 1) / sms);
         double cost = turns * (tiles / f + kTurnTiles);
         if (f > 1) cost = (cost + kJoinTiles) / 0.95;
@@ -59,7 +59,21 @@ inline int plan_pieces(int64_t items, double tiles, int sms) {
     return f_best;
 }
 
-// Partials of n pieces: 256 rows of O in fp32, then their LSE.
-inline int64_t pieces_bytes(int64_t items, int f, int D) { return f > 1 ? items * f * 256 * (D + 1) * 4 : 0; }
+// A few new tokens over a cache (one tile an item, HBM-bound): sequences' lengths
+// differ and only the device knows them, so the pieces are made for about
+// kPiecesPerSm turns of every SM, of two key tiles at least, which the claims deal
+// out evenly; their partials are a few rows.
+constexpr int kPiecesPerSm = 8;
+inline int plan_pieces_few(int64_t items, double tiles, int sms) {
+    if (items <= 0 || sms <= 0) return 1;
+    int64_t f = (static_cast<int64_t>(kPiecesPerSm) * sms + items - 1) / items;
+    if (f > kMaxPiecesFwd) f = kMaxPiecesFwd;
+    if (static_cast<double>(f) > tiles / 2) f = static_cast<int64_t>(tiles / 2);
+    return f < 1 ? 1 : static_cast<int>(f);
+}
+
+// Rows of a piece's partial, and the partials' bytes: O in fp32, then its LSE.
+inline int part_rows_of(int T, int group) { return T <= 128 / group ? T * group : 256; }
+inline int64_t pieces_bytes(int64_t items, int f, int rows, int D) { return f > 1 ? items * f * rows * (D + 1) * 4 : 0; }
 
 }  // namespace dit

@@ -571,8 +571,8 @@ typedef struct { int left; int right; int sinks; int frame; } dit_window_t;
  *           dit_attn_fwd's (rows of out distinct); lse fp32 [B, H, Nq].  D 64 or 128;
  *           Hkv divides H, H / Hkv at most 128.
  * q_offset  any sign; |q_offset| + Nq and Nkv at most 2^29, else DIT_ERR_UNSUPPORTED.
- * A row that sees no key gets O = 0 and LSE = -inf.  Keys that no query of a 256-row
- * block sees may hold anything, NaN included; V must be finite at the others (a
+ * A row that sees no key gets O = 0 and LSE = -inf.  Keys that no query of a block of
+ * 256 rows, (query, head of the group), sees may hold anything, NaN included; V must be finite at the others (a
  * hidden key's V is multiplied by zero).
  * workspace device memory of dit_attn_fwd_window_workspace_bytes, 16-byte aligned
  *           (NULL when that is 0): few rows are cut into key ranges, whose partials
@@ -659,8 +659,8 @@ dit_status_t dit_paged_append(const void *k, const dit_strides4_t *k_strides, co
  *           NULL: T each; taken within [0, T].  Rows t >= q_lens[b] of out and lse are
  *           left as they were.  T at most 2^29.
  * D 64 or 128; Hkv divides H, H / Hkv at most 128.
- * Keys that no query of a 256-row block sees (stale rows of a page, evicted tokens)
- * may hold anything.
+ * Keys that no query of a block sees (stale rows of a page, evicted tokens) may hold
+ * anything; a block is 256 rows, (token, query head of the group).
  * workspace device memory of dit_attn_fwd_paged_workspace_bytes, 16-byte aligned.
  * Lengths are read on the device only.  A repeated call gives the same bits.
  */
