@@ -574,17 +574,21 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of the C functions above, in that order)
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 14, [&]() -> PyObject* {
-        void* p[14];
-        for (int i = 0; i < 14; ++i) {
-            p[i] = PyLong_AsVoidPtr(a[i]);
-            if (p[i] == nullptr) {
-                if (PyErr_Occurred()) python_error();
-                value_error("a function is missing");
-            }
+// The seven addresses of a bind call.
+void addresses(PyObject* const* a, void* (&p)[7]) {
+    for (int i = 0; i < 7; ++i) {
+        p[i] = PyLong_AsVoidPtr(a[i]);
+        if (p[i] == nullptr) {
+            if (PyErr_Occurred()) python_error();
+            value_error("a function is missing");
         }
+    }
+}
+// bind(addresses of the first seven C functions above, in that order)
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject* {
+        void* p[7];
+        addresses(a, p);
         g_attn_bwd = reinterpret_cast<decltype(g_attn_bwd)>(p[0]);
         g_attn_bwd_masked = reinterpret_cast<decltype(g_attn_bwd_masked)>(p[1]);
         g_attn_bwd_ws = reinterpret_cast<decltype(g_attn_bwd_ws)>(p[2]);
@@ -592,13 +596,21 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[4]);
         g_norm_bwd_ws = reinterpret_cast<decltype(g_norm_bwd_ws)>(p[5]);
         g_rope = reinterpret_cast<decltype(g_rope)>(p[6]);
-        g_window_fwd = reinterpret_cast<decltype(g_window_fwd)>(p[7]);
-        g_window_fwd_ws = reinterpret_cast<decltype(g_window_fwd_ws)>(p[8]);
-        g_window_bwd = reinterpret_cast<decltype(g_window_bwd)>(p[9]);
-        g_window_bwd_ws = reinterpret_cast<decltype(g_window_bwd_ws)>(p[10]);
-        g_append = reinterpret_cast<decltype(g_append)>(p[11]);
-        g_paged = reinterpret_cast<decltype(g_paged)>(p[12]);
-        g_paged_ws = reinterpret_cast<decltype(g_paged_ws)>(p[13]);
+        return Py_NewRef(Py_None);
+    });
+}
+// bind_streaming(addresses of the last seven, in that order)
+PyObject* bind_streaming(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject* {
+        void* p[7];
+        addresses(a, p);
+        g_window_fwd = reinterpret_cast<decltype(g_window_fwd)>(p[0]);
+        g_window_fwd_ws = reinterpret_cast<decltype(g_window_fwd_ws)>(p[1]);
+        g_window_bwd = reinterpret_cast<decltype(g_window_bwd)>(p[2]);
+        g_window_bwd_ws = reinterpret_cast<decltype(g_window_bwd_ws)>(p[3]);
+        g_append = reinterpret_cast<decltype(g_append)>(p[4]);
+        g_paged = reinterpret_cast<decltype(g_paged)>(p[5]);
+        g_paged_ws = reinterpret_cast<decltype(g_paged_ws)>(p[6]);
         return Py_NewRef(Py_None);
     });
 }
@@ -606,6 +618,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define DIT_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {DIT_METHOD(attn_bwd), DIT_METHOD(norm_fwd), DIT_METHOD(norm_bwd), DIT_METHOD(rope), DIT_METHOD(bind),
                           DIT_METHOD(window_fwd), DIT_METHOD(window_bwd), DIT_METHOD(append), DIT_METHOD(paged),
+                          DIT_METHOD(bind_streaming),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "dit_calls", "calls of libditattn's operators", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
