@@ -172,8 +172,10 @@ def _load_calls():
     loader = importlib.machinery.ExtensionFileLoader("dit_calls", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dit_calls", loader))
     loader.exec_module(module)
+
     def addresses(*names):
         return [ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in names]
+
     module.bind(*addresses(
         "dit_attn_bwd", "dit_attn_bwd_masked", "dit_attn_bwd_workspace_bytes", "dit_layer_norm_fwd",
         "dit_layer_norm_bwd", "dit_layer_norm_bwd_workspace_bytes", "dit_rope"))

@@ -78,7 +78,6 @@ void fill_common(WindowArgs& a, int B, int T, int H, int Hkv, const dit_window_t
     a.o_sh = so.h;
     a.lse = lse;
     a.n_blk = static_cast<int>((static_cast<int64_t>(T) + 2 * a.tokens - 1) / (2 * a.tokens));
-    a.div_blk = FastDiv(static_cast<uint32_t>(a.n_blk));
     a.div_hkv = FastDiv(static_cast<uint32_t>(Hkv));
     a.div_group = FastDiv(static_cast<uint32_t>(a.group));
     a.timeout_ns = kWatchdogNs;
@@ -99,9 +98,14 @@ int pieces_of(int B, int T, int H, int Hkv, const dit_window_t& window, int offs
     return plan_pieces(items_of(B, T, H, Hkv), mean_key_tiles(make_window(window), T, rows, offset, kv_len), sms);
 }
 // Settles the grid and the partials' place in the workspace.
-dit_status_t set_pieces(WindowArgs& a, int f, int D, void* workspace, size_t workspace_bytes) {
+dit_status_t set_pieces(WindowArgs& a, int f, int D, int sms, void* workspace, size_t workspace_bytes) {
     const int64_t items = items_of(a.B, a.T, a.H, a.Hkv);
     a.part_rows = part_rows_of(a.T, a.group);
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
+    a.late = late_blocks(a.win, heads, a.n_blk, sms);
+    a.n_main = static_cast<int>(std::min<int64_t>(heads * (a.n_blk - a.late), 0x7fffffff));
+    a.div_blk = FastDiv(static_cast<uint32_t>(std::max(a.n_blk - a.late, 1)));
+    a.div_bhk = FastDiv(static_cast<uint32_t>(heads));
     if (items * f > 0x7ffffff0LL) return DIT_ERR_UNSUPPORTED;
     a.f = f;
     a.div_f = FastDiv(static_cast<uint32_t>(f));
@@ -198,7 +202,7 @@ dit_status_t dit_attn_fwd_window(const void* q, const void* k, const void* v, co
     a.kv_len = key_valid_len;
     a.offset = q_offset;
     const int f = any_keys ? pieces_of(B, Nq, H, Hkv, *window, q_offset, key_valid_len, device_sm_count(dev)) : 1;
-    if ((e = set_pieces(a, f, D, workspace, workspace_bytes)) != DIT_OK) return e;
+    if ((e = set_pieces(a, f, D, device_sm_count(dev), workspace, workspace_bytes)) != DIT_OK) return e;
     if ((e = check_placement({any_keys ? q : nullptr, any_keys ? k : nullptr, any_keys ? v : nullptr, out, lse, f > 1 ? workspace : nullptr},
                              stream)) != DIT_OK)
         return e;
@@ -304,7 +308,7 @@ dit_status_t dit_attn_fwd_paged(const void* q, const dit_strides4_t* q_strides, 
     a.capacity = any_keys ? static_cast<int>(capacity) : 0;
     a.div_page = FastDiv(static_cast<uint32_t>(cache->page_size));
     const int f = any_keys ? paged_pieces_of(B, T, H, Hkv, *window, capacity, device_sm_count(dev)) : 1;
-    if ((e = set_pieces(a, f, D, workspace, workspace_bytes)) != DIT_OK) return e;
+    if ((e = set_pieces(a, f, D, device_sm_count(dev), workspace, workspace_bytes)) != DIT_OK) return e;
     if ((e = check_placement({any_keys ? q : nullptr, any_keys ? cache->k : nullptr, any_keys ? cache->v : nullptr,
                               any_keys ? cache->table : nullptr, cache->kv_lens, q_lens, out, lse, f > 1 ? workspace : nullptr},
                              stream)) != DIT_OK)

@@ -218,17 +218,17 @@ __device__ __forceinline__ Item<KEY> decode_window(const AttnBwdArgs& a, int id)
     Item<KEY> it;
     uint32_t piece = 0, tile, bh, h, item = static_cast<uint32_t>(KEY ? id : id - a.n_kv_items);
     if constexpr (KEY) {
-        // the leading kv_cut tiles of every head in pieces, then the others whole
+        // the leading kv_cut tiles of every head, in f_kv pieces, then the others whole
         const uint32_t cut = static_cast<uint32_t>(a.n_kv_cut);
-        it.cut = item < cut;
-        if (it.cut) {
+        it.cut = item < cut && a.f_kv > 1;
+        it.part_tile = 0;
+        if (item < cut) {
             item = a.div_f_kv.divmod(item, piece);
             bh = a.div_kv_cut.divmod(item, tile);
             it.part_tile = static_cast<int64_t>(item) * a.f_kv + piece;
         } else {
             bh = a.div_kv_tiles.divmod(item - cut, tile);
             tile += static_cast<uint32_t>(a.kv_cut);
-            it.part_tile = 0;
         }
         it.fixed = static_cast<int>(tile);
     } else {

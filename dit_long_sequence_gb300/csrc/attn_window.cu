@@ -106,16 +106,25 @@ struct Item {
     KeyTiles tiles;
     int begin, end;             // the piece's tiles
 };
+// Batch entry, K/V head and block of an item's number.
+__device__ __forceinline__ void place(const WindowArgs& a, uint32_t item, int& b, int& hk, int& blk) {
+    uint32_t inner, head, bhk;
+    if (item < static_cast<uint32_t>(a.n_main)) {
+        bhk = a.div_blk.divmod(item, inner);
+        blk = a.n_blk - 1 - static_cast<int>(inner);
+    } else {
+        blk = a.late - 1 - static_cast<int>(a.div_bhk.divmod(item - static_cast<uint32_t>(a.n_main), bhk));
+    }
+    b = static_cast<int>(a.div_hkv.divmod(bhk, head));
+    hk = static_cast<int>(head);
+}
 template <bool PAGED>
 __device__ __forceinline__ Item decode(const WindowArgs& a, int id) {
     Item it;
     it.id = id;
-    uint32_t piece = 0, blk, hk, rest = static_cast<uint32_t>(id);
+    uint32_t piece = 0, rest = static_cast<uint32_t>(id);
     if (a.f > 1) rest = a.div_f.divmod(rest, piece);
-    rest = a.div_blk.divmod(rest, blk);
-    it.blk = a.n_blk - 1 - static_cast<int>(blk);
-    it.b = static_cast<int>(a.div_hkv.divmod(rest, hk));
-    it.hk = static_cast<int>(hk);
+    place(a, rest, it.b, it.hk, it.blk);
     it.first = it.blk * 2 * a.tokens;
     if constexpr (PAGED) {
         const int len = max(__ldg(a.kv_lens + it.b), 0);
@@ -610,11 +619,12 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant
     const int c4 = static_cast<int>(threadIdx.x % LPR);
     const int item = static_cast<int>(unit / a.part_rows), rr = static_cast<int>(unit % a.part_rows);
     if (item >= a.n_items / a.f) return;
-    uint32_t blk, hk, g;
+    uint32_t g;
+    int b, hk, blk;
+    place(a, static_cast<uint32_t>(item), b, hk, blk);
     const int t = rr / kT;
     const int token = static_cast<int>(a.div_group.divmod(static_cast<uint32_t>(rr % kT), g));
-    const int b = static_cast<int>(a.div_hkv.divmod(a.div_blk.divmod(static_cast<uint32_t>(item), blk), hk));
-    const int q_at = (a.n_blk - 1 - static_cast<int>(blk)) * 2 * a.tokens + t * a.tokens + token;
+    const int q_at = blk * 2 * a.tokens + t * a.tokens + token;
     const int tokens = PAGED && a.q_lens != nullptr ? min(__ldg(a.q_lens + b), a.T) : a.T;
     if (token >= a.tokens || q_at >= tokens) return;
     const int64_t p0 = static_cast<int64_t>(item) * a.f * a.part_rows + rr;
@@ -636,7 +646,7 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant
         acc.w = fmaf(w, o.w, acc.w);
     }
     const float inv = bad ? NAN : (sum > 0.f ? 1.f / sum : 0.f);
-    const int h = static_cast<int>(hk) * a.group + static_cast<int>(g);
+    const int h = hk * a.group + static_cast<int>(g);
     const int64_t off = b * a.o_sb + static_cast<int64_t>(q_at) * a.o_sn + h * a.o_sh + 4 * c4;
     if (!in_bounds(off >= 0 && off + 4 <= a.dbg_o_elems, a.status, 0, BND_OUT)) return;
     if (a.out_bf16)

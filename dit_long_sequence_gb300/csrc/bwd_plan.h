@@ -114,7 +114,8 @@ inline BwdPlan plan_attn_bwd(int B, int Nq, int Nkv, int H, int D, int key_valid
 // every query behind it, a window's by few.  Where a common key tile is longer than
 // the even share all key items are cut, else only the sinks' (the first of the grid's
 // order), where those are; query items are cut when the longest is longer than the
-// share.
+// share.  Whole or cut, the sinks' items come first: 6,144 tokens of 8 heads in frames of
+// 384, the first frame visible to all: 172 us in the heads' order, 133 so.
 inline BwdPlan plan_attn_bwd_window(int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len, const Window& w, int offset, int sms) {
     BwdPlan p{};
     const int64_t bh = static_cast<int64_t>(B) * H, bhk = static_cast<int64_t>(B) * Hkv;
@@ -156,7 +157,7 @@ inline BwdPlan plan_attn_bwd_window(int B, int Nq, int Nkv, int H, int Hkv, int 
         p.kv_cut = p.f_kv > 1 ? p.kv_out_tiles : 0;
         if (p.f_kv == 1 && sink_tiles > 0) {
             p.f_kv = pieces(4.0 * group * p.q_tiles, static_cast<int64_t>(group) * p.q_tiles);
-            p.kv_cut = p.f_kv > 1 ? sink_tiles : 0;
+            p.kv_cut = sink_tiles;      // (whole or not: the longest items first)
         }
     }
     p.q_whole = p.f_q > 1 ? 0 : p.query_items;

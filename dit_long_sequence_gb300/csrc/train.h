@@ -125,8 +125,8 @@ struct AttnBwdArgs {
     int f_kv, f_q, q_whole;
     int n_kv_items, n_q_items;  // pieces counted
     // With a window (windowed) key items are (b, K/V head, tile), of which the leading
-    // kv_cut tiles of every head are cut, and their pieces (n_kv_cut in all) come
-    // first.  Otherwise Hkv = H, and all key items are cut or none.
+    // kv_cut tiles of every head come first, in f_kv pieces each (n_kv_cut in all).
+    // Otherwise Hkv = H, and all key items are cut or none.
     bool windowed;
     Window window;
     int offset, Hkv, group;     // position of query 0, K/V heads, query heads of one

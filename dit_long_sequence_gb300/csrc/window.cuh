@@ -75,13 +75,18 @@ __device__ __forceinline__ void copy_paged(const WindowArgs& a, const CUtensorMa
 template <int D>
 __device__ __forceinline__ void clear_unseen(uint8_t* v, const KeyTiles& t, int k0) {
     const int s = t.sinks - k0, lo = t.lo - k0, hi = t.hi - k0;
-    if (hi >= kWinTile && (lo <= 0 || s >= lo)) return;
-    if (s >= kWinTile) return;
-    for (int u = static_cast<int>(lane_id()); u < kWinTile * (D / 8); u += 32) {
-        const int row = u / (D / 8), part = u % (D / 8);        // 16 bytes of a row
-        if (row < s || (row >= lo && row < hi)) continue;
-        *reinterpret_cast<uint4*>(v + (part >> 3) * kWinTile * 128 + row * 128 + (part & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
+    // (8 or 16 lanes a row, 16 bytes each)
+    constexpr int kLanes = D / 8;
+    const int part = static_cast<int>(lane_id()) % kLanes;
+    uint8_t* const at = v + (part >> 3) * kWinTile * 128 + (part & 7) * 16;
+    auto clear = [&](int begin, int end) {
+        for (int row = begin + static_cast<int>(lane_id()) / kLanes; row < end; row += 32 / kLanes)
+            *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    const int after_sinks = max(s, 0), after = max(hi, after_sinks);
+    if (after_sinks >= kWinTile || (lo <= after_sinks && after >= kWinTile)) return;
+    clear(after_sinks, min(lo, kWinTile));
+    clear(after, kWinTile);
     fence_async();
     __syncwarp();
 }

@@ -31,7 +31,10 @@ struct WindowArgs {
     // Grid: items (b, K/V head, block of two tiles), blocks fastest and the last
     // first, each in f key ranges whose partials (O normalised, LSE) go to ws_o
     // [item][f][part_rows][D] and ws_lse [item][f][part_rows].
-    int n_blk, f, n_items;      // n_items: pieces counted
+    // The first `late` blocks of every head, which see the fewest keys of a causal
+    // mask, come behind all others, heads fastest: the end of the grid is made of them.
+    int n_blk, late, n_main, f, n_items;    // n_main: items before those; n_items: pieces counted
+    FastDiv div_bhk;
     int part_rows;              // 256, or the rows of the one tile
     FastDiv div_f, div_blk, div_hkv, div_group;
     float *ws_o, *ws_lse;

@@ -41,10 +41,12 @@ inline double mean_key_tiles(const Window& w, int T, int rows, int offset, int k
 // turns of its last SM; cut into f ranges, an item has f turns of a part of its
 // tiles.  A turn costs about kTurnTiles tiles beside its own (first copies, the
 // result's way out) and the join of the pieces kJoinTiles; a cut that does not
-// save a twentieth is not made.
+// save a twentieth is not made.  From two turns on the claims even the grid out and
+// the partials' 132 KB a piece cost more than they give (480 items of 6 ragged chunks:
+// 324 us in three pieces, 242 whole).
 constexpr double kTurnTiles = 3, kJoinTiles = 4;
 inline int plan_pieces(int64_t items, double tiles, int sms) {
-    if (items <= 0 || sms <= 0 || items >= 4LL * sms) return 1;
+    if (items <= 0 || sms <= 0 || items >= 2LL * sms) return 1;
     double best = 0;
     int f_best = 1;
     for (int f = 1; f <= 16 && (f == 1 || tiles / f >= 2); ++f) {
@@ -57,6 +59,15 @@ inline int plan_pieces(int64_t items, double tiles, int sms) {
         }
     }
     return f_best;
+}
+
+// Blocks of every head that come last: about two turns of the SMs, where rows see
+// fewer keys the earlier they are (LTX-2-shaped frames: 1,661 us, one turn 1,674, none
+// 1,695).
+inline int late_blocks(const Window& w, int64_t heads, int n_blk, int sms) {
+    if (w.ahead >= kUnbounded || heads <= 0) return 0;
+    const int64_t n = (2LL * sms + heads - 1) / heads;
+    return n < n_blk / 2 ? static_cast<int>(n) : n_blk / 2;
 }
 
 // A few new tokens over a cache (one tile an item, HBM-bound): sequences' lengths

@@ -102,6 +102,6 @@ def test_pieces(ask):
               rng.choice((1, 5, 16, 32, 64, 128, 129, 4000)), rng.choice((1, 2, 3, 5, 8, 128))) for _ in range(400)]
     for (items, tiles, sms, T, group), (f, few, rows) in zip(cases, ask("p " + " ".join(map(str, c)) for c in cases)):
         assert 1 <= f <= 16 and 1 <= few <= 64
-        assert f == 1 or (tiles / f >= 2 and items < 4 * sms)
+        assert f == 1 or (tiles / f >= 2 and items < 2 * sms)
         assert few == 1 or tiles / few >= 2
         assert rows == (T * group if T * group <= 128 and T <= 128 // group else 256)
