@@ -92,17 +92,27 @@ int64_t items_of(int B, int T, int H, int Hkv) {
     const int64_t rows = 2 * (128 / (H / Hkv));
     return static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(T) + rows - 1) / rows);
 }
-// Pieces of an item of attention over `kv_len` keys, queries from position `offset`.
-int pieces_of(int B, int T, int H, int Hkv, const dit_window_t& window, int offset, int kv_len, int sms) {
+struct GridPlan {
+    int f = 1, late = 0;        // pieces of an item, blocks of a head that come last
+};
+// Attention over `kv_len` keys, queries from position `offset`.
+GridPlan plan_of(int B, int T, int H, int Hkv, const dit_window_t& window, int offset, int kv_len, int sms) {
     const int rows = 2 * (128 / (H / Hkv));
-    return plan_pieces(items_of(B, T, H, Hkv), mean_key_tiles(make_window(window), T, rows, offset, kv_len), sms);
+    const Window w = make_window(window);
+    const double mean = mean_key_tiles(w, T, rows, offset, kv_len);
+    const double first = key_tiles(w, offset, offset + std::min(rows, T) - 1, kv_len).n;
+    GridPlan p;
+    p.f = plan_pieces(items_of(B, T, H, Hkv), mean, sms);
+    p.late = late_blocks(first, mean, static_cast<int64_t>(B) * Hkv, (static_cast<int64_t>(T) + rows - 1) / rows, sms);
+    return p;
 }
 // Settles the grid and the partials' place in the workspace.
-dit_status_t set_pieces(WindowArgs& a, int f, int D, int sms, void* workspace, size_t workspace_bytes) {
+dit_status_t set_grid(WindowArgs& a, const GridPlan& plan, int D, void* workspace, size_t workspace_bytes) {
+    const int f = plan.f;
     const int64_t items = items_of(a.B, a.T, a.H, a.Hkv);
     a.part_rows = part_rows_of(a.T, a.group);
     const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
-    a.late = late_blocks(a.win, heads, a.n_blk, sms);
+    a.late = plan.late;
     a.n_main = static_cast<int>(std::min<int64_t>(heads * (a.n_blk - a.late), 0x7fffffff));
     a.div_blk = FastDiv(static_cast<uint32_t>(std::max(a.n_blk - a.late, 1)));
     a.div_bhk = FastDiv(static_cast<uint32_t>(heads));
@@ -149,12 +159,14 @@ dit_status_t encode_pages(CUtensorMap* map, const void* base, const dit_strides4
     const uint32_t box[4] = {64, static_cast<uint32_t>(chunk), 1, 1};
     return encode_tiles(map, base, 4, dims, st, box);
 }
-// Pieces of an item over a cache, whose lengths the host does not know: as if every
-// sequence filled its table row.
-int paged_pieces_of(int B, int T, int H, int Hkv, const dit_window_t& window, int64_t capacity, int sms) {
+// The same over a cache, whose lengths the host does not know: as if every sequence
+// filled its table row.
+GridPlan paged_plan_of(int B, int T, int H, int Hkv, const dit_window_t& window, int64_t capacity, int sms) {
     const int len = static_cast<int>(capacity), tokens = 128 / (H / Hkv);
-    if (T <= tokens) return plan_pieces_few(items_of(B, T, H, Hkv), mean_key_tiles(make_window(window), T, tokens, len - T, len), sms);
-    return pieces_of(B, T, H, Hkv, window, len - T, len, sms);
+    if (T > tokens) return plan_of(B, T, H, Hkv, window, len - T, len, sms);
+    GridPlan p;
+    p.f = plan_pieces_few(items_of(B, T, H, Hkv), key_tiles(make_window(window), len - T, len - 1, len).n, sms);
+    return p;
 }
 
 }  // namespace
@@ -168,7 +180,7 @@ size_t dit_attn_fwd_window_workspace_bytes(int B, int Nq, int H, int Hkv, int D,
     if (key_valid_len > kMaxTokens || std::abs(static_cast<int64_t>(q_offset)) + Nq > kMaxTokens) return 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const int f = pieces_of(B, Nq, H, Hkv, *window, q_offset, key_valid_len, device_sm_count(dev));
+    const int f = plan_of(B, Nq, H, Hkv, *window, q_offset, key_valid_len, device_sm_count(dev)).f;
     return static_cast<size_t>(pieces_bytes(items_of(B, Nq, H, Hkv), f, part_rows_of(Nq, H / Hkv), D));
 }
 
@@ -201,9 +213,9 @@ dit_status_t dit_attn_fwd_window(const void* q, const void* k, const void* v, co
     fill_common(a, B, Nq, H, Hkv, *window, scale, out, out_dtype, strides->o, lse, D);
     a.kv_len = key_valid_len;
     a.offset = q_offset;
-    const int f = any_keys ? pieces_of(B, Nq, H, Hkv, *window, q_offset, key_valid_len, device_sm_count(dev)) : 1;
-    if ((e = set_pieces(a, f, D, device_sm_count(dev), workspace, workspace_bytes)) != DIT_OK) return e;
-    if ((e = check_placement({any_keys ? q : nullptr, any_keys ? k : nullptr, any_keys ? v : nullptr, out, lse, f > 1 ? workspace : nullptr},
+    const GridPlan plan = any_keys ? plan_of(B, Nq, H, Hkv, *window, q_offset, key_valid_len, device_sm_count(dev)) : GridPlan{};
+    if ((e = set_grid(a, plan, D, workspace, workspace_bytes)) != DIT_OK) return e;
+    if ((e = check_placement({any_keys ? q : nullptr, any_keys ? k : nullptr, any_keys ? v : nullptr, out, lse, plan.f > 1 ? workspace : nullptr},
                              stream)) != DIT_OK)
         return e;
     if (any_keys) {
@@ -265,7 +277,7 @@ size_t dit_attn_fwd_paged_workspace_bytes(int B, int T, int H, int Hkv, int D, i
     const int64_t capacity = static_cast<int64_t>(page_size) * table_width;
     int dev = 0;
     if (capacity > 0x7fffff00LL || cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const int f = paged_pieces_of(B, T, H, Hkv, *window, capacity, device_sm_count(dev));
+    const int f = paged_plan_of(B, T, H, Hkv, *window, capacity, device_sm_count(dev)).f;
     return static_cast<size_t>(pieces_bytes(items_of(B, T, H, Hkv), f, part_rows_of(T, H / Hkv), D));
 }
 
@@ -307,10 +319,10 @@ dit_status_t dit_attn_fwd_paged(const void* q, const dit_strides4_t* q_strides, 
     a.chunk = chunk_of(cache->page_size);
     a.capacity = any_keys ? static_cast<int>(capacity) : 0;
     a.div_page = FastDiv(static_cast<uint32_t>(cache->page_size));
-    const int f = any_keys ? paged_pieces_of(B, T, H, Hkv, *window, capacity, device_sm_count(dev)) : 1;
-    if ((e = set_pieces(a, f, D, device_sm_count(dev), workspace, workspace_bytes)) != DIT_OK) return e;
+    const GridPlan plan = any_keys ? paged_plan_of(B, T, H, Hkv, *window, capacity, device_sm_count(dev)) : GridPlan{};
+    if ((e = set_grid(a, plan, D, workspace, workspace_bytes)) != DIT_OK) return e;
     if ((e = check_placement({any_keys ? q : nullptr, any_keys ? cache->k : nullptr, any_keys ? cache->v : nullptr,
-                              any_keys ? cache->table : nullptr, cache->kv_lens, q_lens, out, lse, f > 1 ? workspace : nullptr},
+                              any_keys ? cache->table : nullptr, cache->kv_lens, q_lens, out, lse, plan.f > 1 ? workspace : nullptr},
                              stream)) != DIT_OK)
         return e;
     if (any_keys) {

@@ -24,10 +24,10 @@ inline Window make_window(const dit_window_t& w) {
 }
 
 // Key tiles an item (`rows` query tokens of a sequence of T from position `offset`)
-// walks on the average, from at most 128 of them.
+// walks on the average, from at most 64 of them.
 inline double mean_key_tiles(const Window& w, int T, int rows, int offset, int kv_len) {
     const int64_t blocks = (static_cast<int64_t>(T) + rows - 1) / rows;
-    const int64_t step = blocks > 64 ? blocks / 64 : 1;
+    const int64_t step = blocks > 32 ? blocks / 32 : 1;
     double sum = 0;
     int64_t n = 0;
     for (int64_t i = 0; i < blocks; i += step, ++n) {
@@ -61,20 +61,21 @@ inline int plan_pieces(int64_t items, double tiles, int sms) {
     return f_best;
 }
 
-// Blocks of every head that come last: about two turns of the SMs, where rows see
-// fewer keys the earlier they are (LTX-2-shaped frames: 1,661 us, one turn 1,674, none
-// 1,695).
-inline int late_blocks(const Window& w, int64_t heads, int n_blk, int sms) {
-    if (w.ahead >= kUnbounded || heads <= 0) return 0;
+// Blocks of every head that come last: about two turns of the SMs, where a sequence's
+// first rows see half the keys of the others or less (LTX-2-shaped frames: 1,661 us,
+// one turn 1,674, none 1,695).  A chunk behind a long past has no such rows, and its
+// longest sequence's items would come last (324 us, without 315).
+inline int late_blocks(double first_tiles, double mean_tiles, int64_t heads, int64_t n_blk, int sms) {
+    if (2 * first_tiles > mean_tiles || heads <= 0) return 0;
     const int64_t n = (2LL * sms + heads - 1) / heads;
-    return n < n_blk / 2 ? static_cast<int>(n) : n_blk / 2;
+    return static_cast<int>(n < n_blk / 2 ? n : n_blk / 2);
 }
 
 // A few new tokens over a cache (one tile an item, HBM-bound): sequences' lengths
 // differ and only the device knows them, so the pieces are made for about
 // kPiecesPerSm turns of every SM, of two key tiles at least, which the claims deal
 // out evenly; their partials are a few rows.
-constexpr int kPiecesPerSm = 8;
+constexpr int kPiecesPerSm = 8;     // (48 ragged sequences: 250 us; 4 260, 16 275)
 inline int plan_pieces_few(int64_t items, double tiles, int sms) {
     if (items <= 0 || sms <= 0) return 1;
     int64_t f = (static_cast<int64_t>(kPiecesPerSm) * sms + items - 1) / items;
