@@ -617,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the f pieces of every item: with M = max_p LSE_p and w_p = e^(LSE_p - M),
 // O = sum_p w_p O_p / sum_p w_p and LSE = M + ln sum_p w_p.  A piece without a key
-// of the row has LSE_p = -inf and weight 0.  D / 4 lanes a row.
+// of the row has LSE_p = -inf and weight 0.  D / 4 lanes a row.  (The partials are
+// written while this kernel may already be set up: no read-only loads of them.)
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant__ WindowArgs a) {
     constexpr int LPR = D / 4;
@@ -636,16 +637,16 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const __grid_constant
     if (token >= a.tokens || q_at >= tokens) return;
     const int64_t p0 = static_cast<int64_t>(item) * a.f * a.part_rows + rr;
     float mx = -INFINITY;
-    for (int p = 0; p < a.f; ++p) mx = fmaxf(mx, __ldg(a.ws_lse + p0 + static_cast<int64_t>(p) * a.part_rows));
+    for (int p = 0; p < a.f; ++p) mx = fmaxf(mx, __ldcg(a.ws_lse + p0 + static_cast<int64_t>(p) * a.part_rows));
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     bool bad = false;           // (a NaN must stay one)
     for (int p = 0; p < a.f; ++p) {
-        const float lp = __ldg(a.ws_lse + p0 + static_cast<int64_t>(p) * a.part_rows);
+        const float lp = __ldcg(a.ws_lse + p0 + static_cast<int64_t>(p) * a.part_rows);
         bad = bad || lp != lp;
         if (lp == -INFINITY) continue;
         const float w = expf(lp - mx);
-        const float4 o = __ldg(reinterpret_cast<const float4*>(a.ws_o + (p0 + static_cast<int64_t>(p) * a.part_rows) * D) + c4);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(a.ws_o + (p0 + static_cast<int64_t>(p) * a.part_rows) * D) + c4);
         sum += w;
         acc.x = fmaf(w, o.x, acc.x);
         acc.y = fmaf(w, o.y, acc.y);
