@@ -53,8 +53,8 @@ dit_status_t attn_bwd_common(const void* q, const void* k, const void* v, const 
     if (!known(out_dtype) || !known(grad_dtype)) return DIT_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DIT_ERR_UNSUPPORTED;
     if (B > 65535 || H > 65535) return DIT_ERR_UNSUPPORTED;
-    if (B == 0 || H == 0 || (Nq == 0 && Nkv == 0)) return DIT_OK;
     const int Hkv = window != nullptr ? window->Hkv : H;
+    if (B == 0 || (H == 0 && Hkv == 0) || (Nq == 0 && Nkv == 0)) return DIT_OK;
     const bool any_keys = key_valid_len > 0 && Nq > 0;   // otherwise every gradient is zero
     if (Nq > 0 && dq == nullptr) return DIT_ERR_INVALID_ARG;
     if (Nkv > 0 && (dk == nullptr || dv == nullptr)) return DIT_ERR_INVALID_ARG;
@@ -320,7 +320,8 @@ dit_status_t dit_attn_bwd_window(const void* q, const void* k, const void* v, co
     if (H > 0 && H / Hkv > 128) return DIT_ERR_UNSUPPORTED;
     if (Nkv > kMaxWindowTokens || std::abs(static_cast<int64_t>(q_offset)) + std::max(Nq, 0) > kMaxWindowTokens) return DIT_ERR_UNSUPPORTED;
     const BwdWindow w{make_window(*window), Hkv, q_offset};
-    return attn_bwd_common(q, k, v, out, out_dtype, lse, dout, dlse, strides, B, Nq, Nkv, H, D, key_valid_len, nullptr, &w, scale,
+    // without query heads there are no queries: dk and dv are zeros
+    return attn_bwd_common(q, k, v, out, out_dtype, lse, dout, dlse, strides, B, H == 0 ? std::min(Nq, 0) : Nq, Nkv, H, D, key_valid_len, nullptr, &w, scale,
                            dq, dk, dv, grad_dtype, workspace, workspace_bytes, stream);
 }
 
