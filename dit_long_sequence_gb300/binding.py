@@ -724,6 +724,13 @@ def attn_bwd_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
 
 
 def _window(left, right, sinks, frame):
+    # (in the struct a negative bound is none)
+    if any(bound is not None and bound < 0 for bound in (left, right)):
+        raise ValueError("left and right are None or at least 0")
+    if sinks < 0 or frame < 1:
+        raise ValueError("sinks must be at least 0 and frame at least 1")
+    if max(left or 0, right or 0, sinks, frame) > 0x7fffffff:
+        raise ValueError("an integer argument is out of range")
     return ctypes.byref(Window(-1 if left is None else int(left), -1 if right is None else int(right), int(sinks), int(frame)))
 
 

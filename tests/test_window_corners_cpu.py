@@ -14,3 +14,15 @@ def test_gradients_without_query_heads_are_written(lib):  # noqa: F811
     assert _bwd(lib, H=0, Hkv=2, Nq=-1) == lib.DIT_ERR_INVALID_ARG
     assert _bwd(lib, H=0, Hkv=0, dk=None, dv=None) == lib.DIT_OK
     assert _bwd(lib, H=0, Hkv=2, Nkv=0, kvl=0, dk=None, dv=None) == lib.DIT_OK
+
+
+def test_workspace_functions_refuse_windows_that_the_calls_refuse(lib):  # noqa: F811
+    """A negative bound is a ValueError there as in the calls, not a window without it."""
+    asks = (lambda **w: lib.attn_fwd_window_workspace_bytes(1, 300, 4, 2, 64, 300, **w),
+            lambda **w: lib.attn_bwd_window_workspace_bytes(1, 300, 300, 4, 2, 64, 300, **w),
+            lambda **w: lib.attn_fwd_paged_workspace_bytes(1, 1, 4, 2, 64, 16, 400, **w))
+    for ask in asks:
+        for w in (dict(left=-1), dict(right=-1), dict(left=-2 ** 31), dict(sinks=-1), dict(frame=0), dict(left=2 ** 32), dict(sinks=2 ** 31)):
+            with pytest.raises(ValueError):
+                ask(**w)
+        assert ask(left=None, right=None) >= 0 and ask(left=2 ** 31 - 1, right=2 ** 31 - 1, sinks=2 ** 31 - 1, frame=2 ** 30) >= 0
