@@ -23,6 +23,12 @@ using namespace dit;
 namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 29;
+constexpr int64_t kMaxItems = 0x7ffffff0;      // counted in 32-bit ints on the device
+
+int64_t items_of(int B, int T, int H, int Hkv) {
+    const int64_t rows = 2 * (128 / (H / Hkv));
+    return static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(T) + rows - 1) / rows);
+}
 
 // Sizes, window and scale that every form checks alike; `done`: nothing to compute.
 dit_status_t check_common(int B, int T, int H, int Hkv, int D, const dit_window_t* window, float scale, bool& done) {
@@ -35,7 +41,7 @@ dit_status_t check_common(int B, int T, int H, int Hkv, int D, const dit_window_
     done = B == 0 || T == 0 || H == 0;
     if (done) return DIT_OK;
     if (Hkv == 0 || H % Hkv != 0) return DIT_ERR_INVALID_ARG;
-    if (H / Hkv > 128) return DIT_ERR_UNSUPPORTED;
+    if (H / Hkv > 128 || items_of(B, T, H, Hkv) > kMaxItems) return DIT_ERR_UNSUPPORTED;
     return DIT_OK;
 }
 
@@ -88,10 +94,6 @@ void fill_common(WindowArgs& a, int B, int T, int H, int Hkv, const dit_window_t
 #endif
 }
 
-int64_t items_of(int B, int T, int H, int Hkv) {
-    const int64_t rows = 2 * (128 / (H / Hkv));
-    return static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(T) + rows - 1) / rows);
-}
 struct GridPlan {
     int f = 1, late = 0;        // pieces of an item, blocks of a head that come last
 };
@@ -116,7 +118,7 @@ dit_status_t set_grid(WindowArgs& a, const GridPlan& plan, int D, void* workspac
     a.n_main = static_cast<int>(std::min<int64_t>(heads * (a.n_blk - a.late), 0x7fffffff));
     a.div_blk = FastDiv(static_cast<uint32_t>(std::max(a.n_blk - a.late, 1)));
     a.div_bhk = FastDiv(static_cast<uint32_t>(heads));
-    if (items * f > 0x7ffffff0LL) return DIT_ERR_UNSUPPORTED;
+    if (items * f > kMaxItems) return DIT_ERR_UNSUPPORTED;
     a.f = f;
     a.div_f = FastDiv(static_cast<uint32_t>(f));
     a.n_items = static_cast<int>(items * f);

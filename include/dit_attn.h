@@ -569,11 +569,15 @@ typedef struct { int left; int right; int sinks; int frame; } dit_window_t;
  *
  * q, out    bf16 / out_dtype [B, Nq, H, D], k, v bf16 [B, Nkv, Hkv, D], strides as
  *           dit_attn_fwd's (rows of out distinct); lse fp32 [B, H, Nq].  D 64 or 128;
- *           Hkv divides H, H / Hkv at most 128.
+ *           Hkv divides H, H / Hkv at most 128 (else DIT_ERR_UNSUPPORTED).  B and H at
+ *           most 65,535 and B * Hkv * ceil(Nq / n) at most 2^31 - 16, with the n of the
+ *           paragraph below; else DIT_ERR_UNSUPPORTED.
  * q_offset  any sign; |q_offset| + Nq and Nkv at most 2^29, else DIT_ERR_UNSUPPORTED.
- * A row that sees no key gets O = 0 and LSE = -inf.  Keys that no query of a block of
- * 256 rows, (query, head of the group), sees may hold anything, NaN included; V must be finite at the others (a
- * hidden key's V is multiplied by zero).
+ * A row that sees no key gets O = 0 and LSE = -inf.  Rows are worked on in blocks of
+ * n = 2 * floor(128 / (H / Hkv)) queries, from query 0 on, of the query heads that
+ * share a K/V head.  Keys that no query of a block sees may hold anything for it, NaN
+ * included, and so may K at a key that a row does not see; V must be finite at every
+ * key that a query of the row's block sees (a hidden key's V is multiplied by zero).
  * workspace device memory of dit_attn_fwd_window_workspace_bytes, 16-byte aligned
  *           (NULL when that is 0): few rows are cut into key ranges, whose partials
  *           are joined in a fixed order.  A repeated call gives the same bits.
@@ -594,7 +598,11 @@ size_t dit_attn_fwd_window_workspace_bytes(int B, int Nq, int H, int Hkv, int D,
  * H / Hkv query heads of a group.
  *
  * Tensors, strides, workspace (of dit_attn_bwd_window_workspace_bytes), overlaps and
- * arithmetic as dit_attn_bwd; sizes as dit_attn_fwd_window.
+ * arithmetic as dit_attn_bwd; sizes as dit_attn_fwd_window.  Queries and keys are read
+ * in tiles of 128 rows, from row 0 on.  Where a query of a tile sees a key of another,
+ * all rows of both are multiplied: their q, k, v and dout must be finite, hidden keys'
+ * too (unlike the forward call's).  Keys from key_valid_len on are never read.
+ * H = 0 with Hkv > 0 is a call without queries: dk and dv are written as zeros.
  */
 dit_status_t dit_attn_bwd_window(const void *q, const void *k, const void *v,
                                  const void *out, dit_dtype_t out_dtype, const float *lse,
@@ -615,7 +623,8 @@ size_t dit_attn_bwd_window_workspace_bytes(int B, int Nq, int Nkv, int H, int Hk
  * k, v      bf16, element (page, token of the page, head, d) at page*s.b + token*s.n +
  *           head*s.h + d (s.d = 1); strides positive multiples of 8, bases 16-byte
  *           aligned.  Two tensors, or views of one allocation.
- * page_size a multiple of 8.
+ * page_size a multiple of 8; page_size * table_width at most 2^31 - 256 and pages below
+ *           2^31 - 1, else DIT_ERR_UNSUPPORTED.
  * table     int32 device array, element (b, i) at b*table_stride + i: the page of
  *           positions [i*page_size, (i+1)*page_size) of sequence b, i < table_width.
  *           Several sequences may share pages.  An index outside [0, pages) holds
@@ -641,10 +650,12 @@ typedef struct {
  *           broadcasts), [B, T, Hkv, D]; D a multiple of 8 up to 1,024.  16 bytes are
  *           moved at a time where pointers and strides allow.
  * new_lens  int32 device array [B], or NULL: T each; taken within [0, T].
+ * B at most 65,535, T at most 2^29 and B * T * Hkv * D below 2^33, else
+ * DIT_ERR_UNSUPPORTED (append in several calls).
  * Tokens without a page (a negative position, one past the table, an index outside
  * the cache) are dropped; everything else in the cache is left as it was.  Two new
  * tokens at one place of the cache (a page that two sequences share, appended to by
- * both) leave either there.
+ * both) leave either's there, 16 bytes by 16 bytes: a mixture unless they are equal.
  */
 dit_status_t dit_paged_append(const void *k, const dit_strides4_t *k_strides, const void *v, const dit_strides4_t *v_strides,
                               const dit_paged_cache_t *cache, const int32_t *new_lens,
@@ -658,9 +669,9 @@ dit_status_t dit_paged_append(const void *k, const dit_strides4_t *k_strides, co
  * q, out, lse  [B, T, H, D] and [B, H, T] as there; q_lens int32 device array [B], or
  *           NULL: T each; taken within [0, T].  Rows t >= q_lens[b] of out and lse are
  *           left as they were.  T at most 2^29.
- * D 64 or 128; Hkv divides H, H / Hkv at most 128.
+ * D, heads and sizes as dit_attn_fwd_window's.
  * Keys that no query of a block sees (stale rows of a page, evicted tokens) may hold
- * anything; a block is 256 rows, (token, query head of the group).
+ * anything for it; blocks as there, n tokens from row 0 on.
  * workspace device memory of dit_attn_fwd_paged_workspace_bytes, 16-byte aligned.
  * Lengths are read on the device only.  A repeated call gives the same bits.
  */
