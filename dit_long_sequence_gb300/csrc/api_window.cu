@@ -84,7 +84,6 @@ void fill_common(WindowArgs& a, int B, int T, int H, int Hkv, const dit_window_t
     a.o_sh = so.h;
     a.lse = lse;
     a.n_blk = static_cast<int>((static_cast<int64_t>(T) + 2 * a.tokens - 1) / (2 * a.tokens));
-    a.div_hkv = FastDiv(static_cast<uint32_t>(Hkv));
     a.div_group = FastDiv(static_cast<uint32_t>(a.group));
     a.timeout_ns = kWatchdogNs;
     a.dbg_o_elems = static_cast<int64_t>(B - 1) * so.b + static_cast<int64_t>(T - 1) * so.n + static_cast<int64_t>(H - 1) * so.h + D;
@@ -113,11 +112,7 @@ dit_status_t set_grid(WindowArgs& a, const GridPlan& plan, int D, void* workspac
     const int f = plan.f;
     const int64_t items = items_of(a.B, a.T, a.H, a.Hkv);
     a.part_rows = part_rows_of(a.T, a.group);
-    const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
-    a.late = plan.late;
-    a.n_main = static_cast<int>(std::min<int64_t>(heads * (a.n_blk - a.late), 0x7fffffff));
-    a.div_blk = FastDiv(static_cast<uint32_t>(std::max(a.n_blk - a.late, 1)));
-    a.div_bhk = FastDiv(static_cast<uint32_t>(heads));
+    order_items(a, plan.late);
     if (items * f > kMaxItems) return DIT_ERR_UNSUPPORTED;
     a.f = f;
     a.div_f = FastDiv(static_cast<uint32_t>(f));

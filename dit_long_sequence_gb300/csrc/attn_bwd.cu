@@ -251,20 +251,11 @@ __device__ __forceinline__ Item<KEY> decode_window(const AttnBwdArgs& a, int id)
     if constexpr (KEY) {
         const int k0 = it.fixed * kT, k1 = min(k0 + kT, a.kv_len);
         if (k0 < k1) {
-            // The queries that see a key of the tile, and those that see them all, are
-            // ranges: hi grows with the position and so does lo (but for the sinks).
-            auto from = [&](int64_t s) {        // first query whose frame starts at s or later
-                const int64_t f = (s >= 0 ? s + w.frame - 1 : s) / w.frame;      // (rounds up)
-                return min(max(f * w.frame - a.offset, int64_t(0)), static_cast<int64_t>(a.Nq));
-            };
-            const bool all = w.ahead >= kUnbounded, ever = w.back >= kUnbounded;
-            const int64_t first = all ? 0 : from(k0 - w.ahead + 1), first_full = all ? 0 : from(k1 - w.ahead);
-            const int64_t last = ever || k0 < w.sinks ? a.Nq : from(k1 + w.back);
-            const int64_t last_full = ever || k1 <= w.sinks ? a.Nq : from(k0 + w.back + 1);
-            it.base = static_cast<int>(first / kT);
-            it.per_head = first < last ? static_cast<int>((last + kT - 1) / kT) - it.base : 0;
-            it.full = static_cast<int>((first_full + kT - 1) / kT);
-            it.full_end = last_full >= a.Nq ? a.q_tiles : static_cast<int>(last_full / kT);
+            const QueryRange r = query_range(w, k0, k1, w.sinks, a.Nq, a.offset);
+            it.base = static_cast<int>(r.first / kT);
+            it.per_head = r.first < r.end ? static_cast<int>((r.end + kT - 1) / kT) - it.base : 0;
+            it.full = static_cast<int>((r.full + kT - 1) / kT);
+            it.full_end = r.full_end >= a.Nq ? a.q_tiles : static_cast<int>(r.full_end / kT);
             n = static_cast<uint32_t>(it.per_head) * static_cast<uint32_t>(a.group);
         }
     } else {

@@ -113,18 +113,6 @@ struct Item {
     KeyTiles tiles;
     int begin, end;             // the piece's tiles
 };
-// Batch entry, K/V head and block of an item's number.
-__device__ __forceinline__ void place(const WindowArgs& a, uint32_t item, int& b, int& hk, int& blk) {
-    uint32_t inner, head, bhk;
-    if (item < static_cast<uint32_t>(a.n_main)) {
-        bhk = a.div_blk.divmod(item, inner);
-        blk = a.n_blk - 1 - static_cast<int>(inner);
-    } else {
-        blk = a.late - 1 - static_cast<int>(a.div_bhk.divmod(item - static_cast<uint32_t>(a.n_main), bhk));
-    }
-    b = static_cast<int>(a.div_hkv.divmod(bhk, head));
-    hk = static_cast<int>(head);
-}
 template <bool PAGED>
 __device__ __forceinline__ Item decode(const WindowArgs& a, int id) {
     Item it;

@@ -114,8 +114,10 @@ inline BwdPlan plan_attn_bwd(int B, int Nq, int Nkv, int H, int D, int key_valid
 // every query behind it, a window's by few.  Where a common key tile is longer than
 // the even share all key items are cut, else only the sinks' (the first of the grid's
 // order), where those are; query items are cut when the longest is longer than the
-// share.  Whole or cut, the sinks' items come first: 6,144 tokens of 8 heads in frames of
-// 384, the first frame visible to all: 172 us in the heads' order, 133 so.
+// share.  The sinks' items come first where only they may be cut, whole or cut: 6,144
+// tokens of 8 heads in frames of 384, the first frame visible to all: 172 us in the heads'
+// order, 133 so.  Where all are cut (few items) a sink's has as many pieces as a common
+// one, each longer than those, and stands in its head's place.
 inline BwdPlan plan_attn_bwd_window(int B, int Nq, int Nkv, int H, int Hkv, int D, int key_valid_len, const Window& w, int offset, int sms) {
     BwdPlan p{};
     const int64_t bh = static_cast<int64_t>(B) * H, bhk = static_cast<int64_t>(B) * Hkv;
@@ -143,14 +145,8 @@ inline BwdPlan plan_attn_bwd_window(int B, int Nq, int Nkv, int H, int Hkv, int 
             const int64_t last = std::min<int64_t>(t * 128 + 127, Nq - 1);
             most_keys = std::max(most_keys, key_tiles(w, static_cast<int>(offset + t * 128), static_cast<int>(offset + last), key_valid_len).n);
             const int64_t k = sink_tiles + static_cast<int64_t>(std::max(p.kv_tiles - 1 - sink_tiles, 0)) * i / 8;
-            // queries from the first that sees the tile's first key to the last that sees its last
-            auto from = [&](int64_t s) {
-                const int64_t f = (s >= 0 ? s + w.frame - 1 : s) / w.frame;
-                return std::min(std::max(f * w.frame - offset, int64_t(0)), static_cast<int64_t>(Nq));
-            };
-            const int64_t first = w.ahead >= kUnbounded ? 0 : from(k * 128 - w.ahead + 1);
-            const int64_t end = w.back >= kUnbounded ? Nq : from(k * 128 + 128 + w.back);
-            if (first < end) most_queries = std::max(most_queries, static_cast<int>((end + 127) / 128 - first / 128));
+            const QueryRange r = query_range(w, k * 128, k * 128 + 128, 0, Nq, offset);
+            if (r.first < r.end) most_queries = std::max(most_queries, static_cast<int>((r.end + 127) / 128 - r.first / 128));
         }
         p.f_q = pieces(3.0 * most_keys, most_keys);
         p.f_kv = pieces(4.0 * group * most_queries, static_cast<int64_t>(group) * most_queries);

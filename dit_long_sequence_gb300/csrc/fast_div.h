@@ -3,6 +3,12 @@
 
 #include <cstdint>
 
+#ifdef __CUDACC__
+#define DIT_HD __host__ __device__ __forceinline__
+#else
+#define DIT_HD inline
+#endif
+
 namespace dit {
 
 // n / d and n % d for 0 <= n < 2^31 and a fixed 1 <= d < 2^31 by one multiply:
@@ -17,14 +23,18 @@ struct FastDiv {
         while ((uint64_t(1) << s) < d) ++s;
         m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
     }
-#ifdef __CUDACC__
-    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
-    __device__ __forceinline__ uint32_t divmod(uint32_t n, uint32_t& rem) const {
+    DIT_HD uint32_t div(uint32_t n) const {
+#ifdef __CUDA_ARCH__
+        return (__umulhi(n, m) + n) >> s;
+#else
+        return (static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> 32) + n) >> s;
+#endif
+    }
+    DIT_HD uint32_t divmod(uint32_t n, uint32_t& rem) const {
         const uint32_t q = div(n);
         rem = n - q * d;
         return q;
     }
-#endif
 };
 
 }  // namespace dit

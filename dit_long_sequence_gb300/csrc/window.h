@@ -49,6 +49,19 @@ struct WindowArgs {
     int64_t dbg_o_elems;        // debug library: O elements reachable through its strides
 };
 
+// Batch entry, K/V head and block of an item's number.
+DIT_HD void place(const WindowArgs& a, uint32_t item, int& b, int& hk, int& blk) {
+    uint32_t inner, head, bhk;
+    if (item < static_cast<uint32_t>(a.n_main)) {
+        bhk = a.div_blk.divmod(item, inner);
+        blk = a.n_blk - 1 - static_cast<int>(inner);
+    } else {
+        blk = a.late - 1 - static_cast<int>(a.div_bhk.divmod(item - static_cast<uint32_t>(a.n_main), bhk));
+    }
+    b = static_cast<int>(a.div_hkv.divmod(bhk, head));
+    hk = static_cast<int>(head);
+}
+
 // All rows of a sequence and K/V head fit one query tile.
 inline bool one_tile(const WindowArgs& a) { return a.T <= a.tokens; }
 cudaError_t launch_attn_window(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WindowArgs& a,

@@ -71,6 +71,16 @@ inline int late_blocks(double first_tiles, double mean_tiles, int64_t heads, int
     return static_cast<int>(n < n_blk / 2 ? n : n_blk / 2);
 }
 
+// Settles the items' order (place()) for a's sizes, blocks and heads.
+inline void order_items(WindowArgs& a, int late) {
+    const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv, main = heads * (a.n_blk - late);
+    a.late = late;
+    a.n_main = static_cast<int>(main < 0x7fffffff ? main : 0x7fffffff);
+    a.div_blk = FastDiv(static_cast<uint32_t>(a.n_blk > late ? a.n_blk - late : 1));
+    a.div_bhk = FastDiv(static_cast<uint32_t>(heads));
+    a.div_hkv = FastDiv(static_cast<uint32_t>(a.Hkv));
+}
+
 // A few new tokens over a cache (one tile an item, HBM-bound): sequences' lengths
 // differ and only the device knows them, so the pieces are made for about
 // kPiecesPerSm turns of every SM, of two key tiles at least, which the claims deal

@@ -6,12 +6,6 @@
 
 #include "fast_div.h"
 
-#ifdef __CUDACC__
-#define DIT_HD __host__ __device__ __forceinline__
-#else
-#define DIT_HD inline
-#endif
-
 namespace dit {
 
 // A query at position p, in the frame that starts at s = floor(p / frame) * frame,
@@ -30,16 +24,34 @@ struct Span {
 };
 DIT_HD Span span_of(const Window& w, int pos, int kv_len) {
     const uint32_t up = static_cast<uint32_t>(pos < 0 ? -(pos + 1) : pos);   // (a negative position's frame is the one below)
-#ifdef __CUDA_ARCH__
     const int64_t q = w.by_frame.div(up);
-#else
-    const int64_t q = up / static_cast<uint32_t>(w.frame);
-#endif
     const int64_t s = (pos < 0 ? -q - 1 : q) * w.frame;
     const int64_t lo = s - w.back, hi = s + w.ahead;
     Span r;
     r.hi = static_cast<int>(hi < 0 ? 0 : (hi > kv_len ? kv_len : hi));
     r.lo = static_cast<int>(lo < 0 ? 0 : (lo > r.hi ? r.hi : lo));
+    return r;
+}
+
+// The queries 0 <= i < n, query i at position offset + i, that see a key of [k0, k1),
+// 0 <= k0 < k1, and those that see all of them.  Both are ranges: hi grows with the
+// position and so does lo (but for the sinks).
+struct QueryRange {
+    int64_t first, end;             // that see a key, none where first >= end
+    int64_t full, full_end;         // that see all (at least these: sinks and window together may show all, too)
+};
+DIT_HD QueryRange query_range(const Window& w, int64_t k0, int64_t k1, int sinks, int n, int offset) {
+    auto from = [&](int64_t s) {        // first query whose frame starts at s or later
+        const int64_t f = (s >= 0 ? s + w.frame - 1 : s) / w.frame;      // (rounds up)
+        const int64_t i = f * w.frame - offset;
+        return i < 0 ? int64_t(0) : (i > n ? static_cast<int64_t>(n) : i);
+    };
+    const bool all = w.ahead >= kUnbounded, ever = w.back >= kUnbounded;
+    QueryRange r;
+    r.first = all ? 0 : from(k0 - w.ahead + 1);
+    r.full = all ? 0 : from(k1 - w.ahead);
+    r.end = ever || k0 < sinks ? n : from(k1 + w.back);
+    r.full_end = ever || k1 <= sinks ? n : from(k0 + w.back + 1);
     return r;
 }
 
