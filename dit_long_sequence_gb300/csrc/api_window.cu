@@ -90,6 +90,7 @@ void fill_common(WindowArgs& a, int B, int T, int H, int Hkv, const dit_window_t
 #ifdef DIT_DEBUG
     if (debug_wait_limit_ns() != 0) a.timeout_ns = debug_wait_limit_ns();
     a.dbg_o_elems -= debug_extent_shrink();
+    a.dbg_keys_short = static_cast<int>(std::min<int64_t>(debug_extent_shrink(), kMaxTokens));
 #endif
 }
 

@@ -223,7 +223,7 @@ __device__ __forceinline__ void produce(const Cta<D, ONE>& s, const CUtensorMap&
             }
             if (i == it.end) break;
             const int tile = it.tiles.at(i);
-            if (!in_bounds(tile >= 0 && tile * kT < it.kv_len, a.status, ROLE_LOAD, BND_KEY)) {
+            if (!in_bounds(tile >= 0 && tile * kT < it.kv_len - a.dbg_keys_short, a.status, ROLE_LOAD, BND_KEY)) {
                 *s.wd.abort_flag = 1;
                 ok = false;
                 break;

@@ -47,6 +47,7 @@ struct WindowArgs {
     unsigned int* status;
     unsigned long long timeout_ns;
     int64_t dbg_o_elems;        // debug library: O elements reachable through its strides
+    int dbg_keys_short;         // debug library: keys off the end that the bounds check of a tile allows
 };
 
 // Batch entry, K/V head and block of an item's number.

@@ -19,9 +19,12 @@
  *     stops the other roles, copies and products already in flight are waited
  *     for (with a limit), tensor memory is released and the kernel returns.
  *     The context stays usable; the next call runs normally.
- * dit_attn_bwd and dit_attn_bwd_masked check the rows of every tile they load:
- * a tile outside its tensor is not loaded, records DIT_ERR_BOUNDS, and its CTA
- * winds down as after a wait that ran out (its gradients are then incomplete).
+ * dit_attn_bwd, dit_attn_bwd_masked and dit_attn_bwd_window check the rows of every
+ * tile they load: a tile outside its tensor is not loaded, records DIT_ERR_BOUNDS,
+ * and its CTA winds down as after a wait that ran out (its gradients are then
+ * incomplete).  dit_attn_fwd_window and dit_attn_fwd_paged check the key tiles that
+ * they load in the same way and every O element that they write (a refused one is
+ * skipped).  Faults are not injected into any of these.
  * dit_check_watchdog() (dit_attn.h) reads and clears the report.
  *
  * The product library exports none of these calls and reports neither
@@ -64,8 +67,10 @@ typedef enum {
  *                  allow (0: the true extent).  A positive value makes the
  *                  stores to the last elements fail their check and be
  *                  skipped -- a way to see the checks fire without any access
- *                  outside the caller's buffer.  dit_attn_bwd takes as many
- *                  rows off the extents of q and dout, and of k and v.
+ *                  outside the caller's buffer.  dit_attn_bwd and its forms take as
+ *                  many rows off the extents of q and dout, and of k and v;
+ *                  dit_attn_fwd_window and dit_attn_fwd_paged as many off each
+ *                  sequence's keys beside the elements off O.
  * Returns DIT_ERR_INVALID_ARG for values outside these ranges.  Host only.
  */
 dit_status_t dit_debug_configure(uint32_t fault, int fault_block, int fault_index, uint32_t wait_limit_us,
