@@ -577,7 +577,9 @@ typedef struct { int left; int right; int sinks; int frame; } dit_window_t;
  * n = 2 * floor(128 / (H / Hkv)) queries, from query 0 on, of the query heads that
  * share a K/V head.  Keys that no query of a block sees may hold anything for it, NaN
  * included, and so may K at a key that a row does not see; V must be finite at every
- * key that a query of the row's block sees (a hidden key's V is multiplied by zero).
+ * key that a query of the row's block sees (a hidden key's V is multiplied by zero)
+ * and at most 2^64 in size (P is held relative to an offset up to 39 log2 units below
+ * the row's maximum, and sums before the division are that much larger than O).
  * workspace device memory of dit_attn_fwd_window_workspace_bytes, 16-byte aligned
  *           (NULL when that is 0): few rows are cut into key ranges, whose partials
  *           are joined in a fixed order.  A repeated call gives the same bits.

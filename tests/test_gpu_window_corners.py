@@ -207,3 +207,19 @@ def test_host_memory_is_refused(dl):
             dl.paged_append(kv, kv, cache, cache.clone(), *bad)
     torch.cuda.synchronize()
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 200])
+def test_large_values_under_growing_scores(dl, T, D):
+    """V of 2^64 and scores that grow by 32 log2 units a tile, nearly as far as a row's offset
+    stands still: the sums before the division stay finite."""
+    n, H = 1500, 2
+    q, k, v = rand((1, T, H, D), 180, 0.25), rand((1, n, H, D), 181), rand((1, n, H, D), 182) * 2.0 ** 64
+    q[..., 0] = 8.0
+    k[..., 0] = (torch.arange(n, device=DEV).float() * (0.25 * 0.6931 / 8.0))[None, :, None].to(torch.bfloat16)
+    for w in ((None, 0, 0, 1), (900, 0, 4, 1)):
+        o, l = dl.attn_fwd_window(q, k, v, left=w[0], sinks=w[2], offset=n - T, scale=1.0)
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(o).all())
+        win.check_forward(o, l, win.forward(q, k, v, 1.0, table_of(T, n, w, n - T, n), False))
