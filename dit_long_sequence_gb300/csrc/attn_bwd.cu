@@ -61,7 +61,8 @@
 // With a window (kWindow) the streamed tiles are ranges known from the fixed tile, a
 // key item runs through them for each query head that shares its K and V, and mask
 // words are computed for the tiles that a range's end cuts.  11,040 tokens, causal, 16
-// heads on 4: 1.20 ms (1.46 PFLOP/s executed); 6,144 tokens in frames of 384: 130 us.
+// heads on 4: 1.17 to 1.20 ms (1.46 PFLOP/s executed); 6,144 tokens in frames of 384, 8
+// heads: 129 us.
 //
 // Rows without an allowed key have LSE = -inf; they, and the rows past Nq, get
 // P = 0 through a stored -LSE of -inf (and a stored delta of 0).  Keys past kv_len are zero-filled by the

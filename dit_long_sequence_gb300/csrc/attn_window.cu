@@ -34,12 +34,12 @@
 // Few items are cut into key ranges (f pieces), whose normalised partials
 // window_merge_kernel joins.
 //
-// Bound by the tensor pipe (66% active) and each tile's chain of scores, softmax and
-// product; ONE by HBM.  Measured: 24,576 tokens in frames of 1,536, three back and the
-// first always, 32 heads of 128: 1,802 us back to back under the power cap (1,496
-// TFLOP/s), 1,649 us in single passes; 44,160 tokens, window of 2,048, 16 heads on 4:
-// 598 us (1,220 TFLOP/s).  ONE: a token for 48 sequences of up to 16,384, 32 heads on 8:
-// 248 us, 6.6 TB/s.
+// Bound by the tensor pipe and each tile's chain of scores, softmax and product (12,288
+// tokens in frames of 1,536, 8 heads: pipe 66% active); ONE by HBM.  Measured over the
+// Python call: 24,576 tokens in frames of 1,536, three back and the first always, 32
+// heads of 128: 1,760 to 1,800 us (1,500 to 1,530 TFLOP/s); 44,160 tokens, window of
+// 2,048, 16 heads on 4: 590 us (1,240 TFLOP/s).  ONE: a token for 48 sequences of up to
+// 16,384, 32 heads on 8: 252 and 278 us for two draws of lengths, 6.1 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

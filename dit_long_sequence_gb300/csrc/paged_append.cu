@@ -5,8 +5,8 @@
 // (each new element read and written once); a few tokens are bound by the chain of
 // dependent loads (lengths, table, then the store), which the source's load lies
 // beside.  16 bytes a thread and step, K and V of a token by neighbouring threads.
-// Measured: 4 x 1,536 tokens of 32 heads of 128 (three quarters of them new) 27.4 us,
-// 5.5 TB/s; one token for 48 sequences 4.1 us, the call's own time.
+// Measured: 4 x 1,536 tokens of 32 heads of 128 (three quarters of them new) 28.4 us,
+// 5.3 TB/s; one token for 48 sequences 4.1 us (3.1 replayed from a graph).
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"

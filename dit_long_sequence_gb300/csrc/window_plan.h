@@ -42,8 +42,9 @@ inline double mean_key_tiles(const Window& w, int T, int rows, int offset, int k
 // tiles.  A turn costs about kTurnTiles tiles beside its own (first copies, the
 // result's way out) and the join of the pieces kJoinTiles; a cut that does not
 // save a twentieth is not made.  From two turns on the claims even the grid out and
-// the partials' 132 KB a piece cost more than they give (480 items of 6 ragged chunks:
-// 324 us in three pieces, 242 whole).
+// the partials' 132 KB a piece cost more than they give (480 items of 6 ragged chunks,
+// both on the same lengths: 324 us in three pieces, 242 whole); the last, partial turn
+// is not evened out (384 equal items end 1.19 times the even share).
 constexpr double kTurnTiles = 3, kJoinTiles = 4;
 inline int plan_pieces(int64_t items, double tiles, int sms) {
     if (items <= 0 || sms <= 0 || items >= 2LL * sms) return 1;
@@ -62,9 +63,10 @@ inline int plan_pieces(int64_t items, double tiles, int sms) {
 }
 
 // Blocks of every head that come last: about two turns of the SMs, where a sequence's
-// first rows see half the keys of the others or less (LTX-2-shaped frames: 1,661 us,
-// one turn 1,674, none 1,695).  A chunk behind a long past has no such rows, and its
-// longest sequence's items would come last (324 us, without 315).
+// first rows see half the keys of the others or less (LTX-2-shaped frames, single passes
+// timed in turn: 1,661 us, one turn 1,674, none 1,695).  A chunk behind a long past has
+// no such rows, and its longest sequence's items would come last (another draw of ragged
+// chunks: 324 us, without 315).
 inline int late_blocks(double first_tiles, double mean_tiles, int64_t heads, int64_t n_blk, int sms) {
     if (2 * first_tiles > mean_tiles || heads <= 0) return 0;
     const int64_t n = (2LL * sms + heads - 1) / heads;
@@ -84,8 +86,13 @@ inline void order_items(WindowArgs& a, int late) {
 // A few new tokens over a cache (one tile an item, HBM-bound): sequences' lengths
 // differ and only the device knows them, so the pieces are made for about
 // kPiecesPerSm turns of every SM, of two key tiles at least, which the claims deal
-// out evenly; their partials are a few rows.
-constexpr int kPiecesPerSm = 8;     // (48 ragged sequences: 250 us; 4 260, 16 275)
+// out evenly (a token for 48 ragged sequences, 32 heads on 8: 250 us; 4 turns 260, 16
+// 275).  The number of rows is not looked at: partials are group * T rows a piece (16
+// tokens of eight heads a K/V head for those sequences: 101 MB, 322 us against 270 for
+// one token), and one sequence is cut finer than it needs (16,384 keys, eight K/V heads
+// of eight heads each: 48 us for one token, 60 for 16, and 32 for 17, which is
+// plan_pieces()).
+constexpr int kPiecesPerSm = 8;
 inline int plan_pieces_few(int64_t items, double tiles, int sms) {
     if (items <= 0 || sms <= 0) return 1;
     int64_t f = (static_cast<int64_t>(kPiecesPerSm) * sms + items - 1) / items;
