@@ -792,7 +792,8 @@ def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torc
                     grad_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None, stream=None):
     """Gradients of attn_fwd_window through `dit_attn_bwd_window`: attn_bwd with the
     forward call's window; dk and dv [B, Nkv, Hkv, D] are summed over the query heads
-    that share them.  Returns (dq, dk, dv)."""
+    that share them (zeros without any).  Unlike the forward call it multiplies hidden
+    keys of the tiles it visits, so they must be finite.  Returns (dq, dk, dv)."""
     args = (left, right, sinks, frame, offset, q, k, v, out, lse, dout, dlse, None, None, key_valid_len, scale, dq, dk, dv,
             _is_fp32(grad_dtype), workspace)
     if stream is None:
@@ -847,7 +848,7 @@ def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 
     q [B, T, H, D] bf16; the cache as in paged_append.  Row t < q_lens[b] (None: T) of
     sequence b is the query at position kv_lens[b] - q_lens[b] + t; the rows behind are
-    left as they were in out and lse.  A page index outside the cache (an evicted page)
+    left as they were in out and lse (results allocated here hold anything there).  A page index outside the cache (an evicted page)
     holds no keys.  The window as in attn_fwd_window.  Returns (out, lse [B, H, T])."""
     args = (q, k_cache, v_cache, page_table, kv_lens, q_lens, left, right, sinks, frame, scale, out, lse, _is_fp32(out_dtype), workspace)
     if stream is None:
