@@ -34,16 +34,19 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // The page that holds chunk `lane` of a key tile, -1 in lanes without a chunk or
 // whose keys are not there.  A whole warp; loaded a tile ahead of its use.
 __device__ __forceinline__ int page_entry(const WindowArgs& a, const int32_t* row, int tile, int kv_len) {
-    const int lane = static_cast<int>(lane_id()), key = tile * kWinTile + lane * a.chunk;
-    const bool mine = lane * a.chunk < kWinTile && key < kv_len;
-    return mine ? __ldg(row + a.div_page.div(static_cast<uint32_t>(key))) : -1;
+    const int lane = static_cast<int>(lane_id());
+    // (unsigned: a lane without a chunk may be past 2^31 at the far end of a table)
+    const uint32_t key = static_cast<uint32_t>(tile) * kWinTile + static_cast<uint32_t>(lane * a.chunk);
+    const bool mine = lane * a.chunk < kWinTile && key < static_cast<uint32_t>(kv_len);
+    return mine ? __ldg(row + a.div_page.div(key)) : -1;
 }
 __device__ __forceinline__ bool page_there(const WindowArgs& a, int entry) { return entry >= 0 && entry < a.n_pages; }
 // Bit c: chunk c has a page, or no key below kv_len (those are hidden by a row's hi).
 // All ones in the usual case.
 __device__ __forceinline__ uint32_t pages_there(const WindowArgs& a, int entry, int tile, int kv_len) {
     const int lane = static_cast<int>(lane_id());
-    const bool past = lane * a.chunk >= kWinTile || tile * kWinTile + lane * a.chunk >= kv_len;
+    const uint32_t key = static_cast<uint32_t>(tile) * kWinTile + static_cast<uint32_t>(lane * a.chunk);
+    const bool past = lane * a.chunk >= kWinTile || key >= static_cast<uint32_t>(kv_len);
     return __ballot_sync(0xffffffffu, past || page_there(a, entry));
 }
 // The keys of word w of a tile whose pages are there.

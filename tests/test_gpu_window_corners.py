@@ -223,3 +223,34 @@ def test_large_values_under_growing_scores(dl, T, D):
         torch.cuda.synchronize()
         assert bool(torch.isfinite(o).all())
         win.check_forward(o, l, win.forward(q, k, v, 1.0, table_of(T, n, w, n - T, n), False))
+
+
+@pytest.mark.parametrize("page", [128, 8192])
+@pytest.mark.parametrize("T", [1, 200])
+@pytest.mark.parametrize("left,sinks,frame", [(300, 5, 1), (0, 200, 1000), (0, 3, 50000)])
+def test_positions_next_to_2_31(dl, page, T, left, sinks, frame):
+    """A table of nearly 2^31 tokens whose entries name a few pages over and over: its last
+    tokens appended and attended, and queries past its end."""
+    H, Hkv, D = 4, 2, 64
+    width = (2 ** 31 - 256) // page
+    capacity = width * page
+    cache = rand((3, 2, page, Hkv, D), 190)
+    table = (torch.arange(width, device=DEV) % 3).to(torch.int32).view(1, width).expand(2, -1)
+    lens = ints([capacity, 2 ** 31 - 1])
+    new = rand((2, 3, 2, Hkv, D), 191)
+    dl.paged_append(new[:, :, 0], new[:, :, 1], cache[:, 0], cache[:, 1], table, lens)
+    torch.cuda.synchronize()
+    for t in range(3):
+        at = capacity - 3 + t
+        assert torch.equal(cache[(at // page) % 3, :, at % page], new[0, t])        # (the other sequence's are past the table)
+    q = rand((2, T, H, D), 192, 1.5)
+    out, lse = dl.attn_fwd_paged(q, cache[:, 0], cache[:, 1], table, lens, left=left, sinks=sinks, frame=frame)
+    torch.cuda.synchronize()
+    for b, n in enumerate((capacity, 2 ** 31 - 1)):
+        p = torch.arange(n - T, n, device=DEV)
+        lo = min(int((p[0] // frame - left) * frame), capacity)
+        j = torch.cat((torch.arange(min(sinks, lo), device=DEV), torch.arange(lo, capacity, device=DEV)))
+        k, v = (cache[(j // page) % 3, i, j % page][None] for i in range(2))
+        fp, fj = (p // frame)[:, None], (j // frame)[None]
+        allow = ((fj <= fp) & ((fj >= fp - left) | (j < sinks)[None]))[None, None]
+        win.check_forward(out[b:b + 1], lse[b:b + 1], win.forward(q[b:b + 1], win.shared(k, H), win.shared(v, H), D ** -0.5, allow, True))
